@@ -14,7 +14,7 @@
  *  - Pointers named *_cache, query, key, value, new_key, new_value, out,
  *    block_tables, context_lens, slot_mapping, block_mapping, tmp_out,
  *    max_logits, exp_sums and workspace are caller-owned DEVICE memory, contiguous,
- *    row-major, 16-byte aligned. The library keeps no reference after the
+ *    row-major, 16-byte aligned, where an entry point does not say otherwise. The library keeps no reference after the
  *    call returns.
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream), so that this header needs no CUDA include.
@@ -97,6 +97,78 @@ PA_API pa_status pa_reshape_and_cache(const void *key, const void *value, void *
                                       void *v_cache, const int64_t *slot_mapping, int num_tokens,
                                       int num_blocks, int block_size, int num_kv_heads,
                                       int head_dim, pa_dtype kv_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions. The keys a cache holds and the queries that read it are
+ * usually rotated by their token's position first: pair i of a head's first
+ * rotary_dim dims, (a, b), becomes
+ *     factor * (a cos t - b sin t, b cos t + a sin t),
+ *     t = position * inv_freq[i].
+ * Dims past rotary_dim pass through.
+ * ---------------------------------------------------------------------- */
+typedef enum pa_rope_layout {
+    PA_ROPE_HALF = 0,        /* pair i: dims i and i + rotary_dim / 2 */
+    PA_ROPE_INTERLEAVED = 1  /* pair i: dims 2i and 2i + 1 */
+} pa_rope_layout;
+
+typedef enum pa_rope_scaling {
+    PA_ROPE_UNSCALED = 0, /* base^(-2i / rotary_dim) */
+    PA_ROPE_LINEAR = 1,   /* every frequency divided by scale */
+    PA_ROPE_NTK = 2,      /* base multiplied by scale^(rotary_dim / (rotary_dim - 2)) */
+    PA_ROPE_YARN = 3,     /* by parts: pairs that make more than `high` turns over original_context
+                             kept, fewer than `low` divided by scale, a linear ramp over the pairs
+                             between; factor = 0.1 ln(scale) + 1 for scale > 1 */
+    PA_ROPE_BANDS = 4     /* the same bands, the blend linear in the number of turns; factor 1 */
+} pa_rope_scaling;
+
+/* Host only: the frequencies (radians a position, 64-bit, [rotary_dim / 2])
+ * and the factor of a scaling kind. scale is ignored by PA_ROPE_UNSCALED;
+ * original_context, low and high (0 < low < high, full turns over
+ * original_context) by all but YARN and BANDS. The caller copies inv_freq
+ * to the device once; any other frequencies may be passed as well. */
+PA_API pa_status pa_rope_frequencies(double *inv_freq, float *factor, int rotary_dim, double base,
+                                     pa_rope_scaling kind, double scale, int original_context, double low,
+                                     double high);
+
+/* Rotate num_heads heads of every token.
+ *   x, out      [num_tokens, num_heads, head_dim], heads and dims contiguous,
+ *               token rows x_stride / out_stride elements apart (at least
+ *               num_heads * head_dim): the query and key heads of a fused
+ *               projection's output are one such view. out may be x itself
+ *               (same stride); any other overlap is not allowed. Base and
+ *               stride need only be whole elements; 16-byte alignment of
+ *               both runs fastest.
+ *   positions   [num_tokens] int32. A negative position marks padding:
+ *               nothing of that token is written.
+ *   inv_freq    [rotary_dim / 2] 64-bit, device memory, 8-byte aligned. The
+ *               angle is reduced modulo a turn in integers: it is as exact
+ *               at position 2^31 - 1 as at position 1.
+ *   transpose   1: sin negated -- the gradient with respect to x of the
+ *               rotation, applied to out's gradient.
+ *   rotary_dim even, at most head_dim; head_dim at most 256; all three
+ *   dtypes; computed in fp32 and rounded once. num_tokens == 0 is a no-op.
+ */
+PA_API pa_status pa_rope(void *out, int64_t out_stride, const void *x, int64_t x_stride, const int32_t *positions,
+                         const double *inv_freq, int num_tokens, int num_heads, int head_dim, int rotary_dim,
+                         pa_rope_layout layout, float factor, int transpose, pa_dtype dtype, void *stream);
+
+/* The slot scatter with the rotation on the way: query rows are rotated into
+ * query_out, key rows rotated into their slots of k_cache, value rows copied
+ * into v_cache, in one launch. Same result as pa_rope on query and key
+ * followed by pa_reshape_and_cache.
+ *   query, query_out  as x and out of pa_rope (query_out may be query)
+ *   key, value        [num_tokens, num_kv_heads, head_dim], token rows
+ *                     key_stride / value_stride elements apart
+ *   slot_mapping      as pa_reshape_and_cache; a token whose slot is negative
+ *                     or past the pool has its query rotated all the same,
+ *                     one whose position is negative is skipped whole.
+ *   Requires (num_kv_heads * head_dim * element size) % 16 == 0. */
+PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
+                                   int64_t query_stride, const void *key, int64_t key_stride, const void *value,
+                                   int64_t value_stride, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                   const int32_t *positions, const double *inv_freq, int num_tokens, int num_heads,
+                                   int num_blocks, int block_size, int num_kv_heads, int head_dim, int rotary_dim,
+                                   pa_rope_layout layout, float factor, pa_dtype dtype, void *stream);
 
 /* ------------------------------------------------------------------------
  * Copy-on-write block copy ("copy_blocks").

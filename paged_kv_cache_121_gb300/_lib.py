@@ -31,6 +31,14 @@ SIGNATURES = {
                                      c_int, c_int, c_int, c_int, c_int, c_void_p]),
     "pa_copy_blocks": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                c_int, c_void_p]),
+    "pa_rope_frequencies": (c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_float), c_int,
+                                    ctypes.c_double, c_int, ctypes.c_double, c_int, ctypes.c_double,
+                                    ctypes.c_double]),
+    "pa_rope": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                        c_int, c_float, c_int, c_int, c_void_p]),
+    "pa_rope_and_cache": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                  c_int, c_int, c_int, c_int, c_float, c_int, c_void_p]),
     "pa_decode_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
     "pa_decode_plan": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),
     "pa_decode": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p,

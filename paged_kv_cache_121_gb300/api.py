@@ -18,6 +18,8 @@ from . import _lib
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OUT_OF_BLOCKS = 0, 1, 2, 3
 PA_ERR_WORKSPACE, PA_ERR_TIMEOUT, PA_ERR_CUDA, PA_ERR_NOT_FOUND = 4, 5, 6, 7
 PA_F32, PA_BF16, PA_F16 = 0, 1, 2
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
+PA_ROPE_UNSCALED, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = 0, 1, 2, 3, 4
 
 
 class PAError(RuntimeError):
@@ -73,6 +75,88 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None
     _check(_lib.load().pa_reshape_and_cache(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
                                            _ptr(slot_mapping), T, nb, bs, hkv, d, _dtype(k_cache),
                                            _stream(stream)), "pa_reshape_and_cache")
+
+
+def _on_current_device(*tensors) -> None:
+    """The kernels run on the current device's stream: every tensor has to live there."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _token_rows(t: torch.Tensor, name: str):
+    """(pointer, token stride) of a [tokens, heads, head_dim] view whose heads are contiguous."""
+    T, h, d = (int(x) for x in t.shape)
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: heads and dims must be contiguous")
+    return t.data_ptr(), int(t.stride(0)) if T > 1 else h * d
+
+
+def _rope_vectors(positions, inv_freq, num_tokens: int) -> int:
+    """Check the position and frequency vectors; returns rotary_dim."""
+    if positions.dtype != torch.int32 or tuple(positions.shape) != (num_tokens,):
+        raise TypeError("positions must be int32 [num_tokens]")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be float64 [rotary_dim / 2]")
+    return 2 * int(inv_freq.shape[0])
+
+
+def pa_rope_frequencies(rotary_dim, base, scaling=PA_ROPE_UNSCALED, scale=1.0, original_context=0, low=1.0,
+                        high=32.0) -> Tuple[np.ndarray, float]:
+    """(inv_freq float64 [rotary_dim / 2], factor) of a rotary scaling kind (host only)."""
+    out = np.empty(max(int(rotary_dim) // 2, 1), dtype=np.float64)
+    factor = ctypes.c_float(1.0)
+    _check(_lib.load().pa_rope_frequencies(out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+                                           ctypes.byref(factor), int(rotary_dim), float(base), int(scaling),
+                                           float(scale), int(original_context), float(low), float(high)),
+           "pa_rope_frequencies")
+    return out, factor.value
+
+
+def pa_rope(out, x, positions, inv_freq, layout=PA_ROPE_HALF, factor=1.0, transpose=False, stream=None) -> None:
+    """Rotate the heads of ``x`` [T, H, D] by their token's position into ``out``
+    (which may be ``x``): ``positions`` [T] int32, negative for padding (left
+    unwritten); ``inv_freq`` float64 [rotary_dim / 2] on the device. The token
+    rows of either may be strided (heads and dims contiguous). ``transpose``
+    applies the gradient of the rotation."""
+    T, h, d = (int(v) for v in x.shape)
+    if tuple(out.shape) != (T, h, d) or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    rot = _rope_vectors(positions, inv_freq, T)
+    _on_current_device(out, x, positions, inv_freq)
+    po, so = _token_rows(out, "out")
+    px, sx = _token_rows(x, "x")
+    _check(_lib.load().pa_rope(po, so, px, sx, _ptr(positions), _ptr(inv_freq), T, h, d, rot, int(layout),
+                               float(factor), int(bool(transpose)), _dtype(x), _stream(stream)), "pa_rope")
+
+
+def pa_rope_and_cache(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                      layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
+    """:func:`pa_rope` on ``query`` [T, Hq, D] into ``query_out`` and on ``key`` [T, Hkv, D] into slot
+    slot_mapping[i] (int64) of the caches, ``value`` copied beside it, in one launch."""
+    nb, bs, hkv, d = _cache_dims(k_cache)
+    T, hq, dq = (int(v) for v in query.shape)
+    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (T,):
+        raise TypeError("slot_mapping must be int64 [num_tokens]")
+    if dq != d or tuple(query_out.shape) != (T, hq, d):
+        raise ValueError("query and query_out must be [num_tokens, num_heads, head_dim]")
+    if tuple(key.shape) != (T, hkv, d) or tuple(value.shape) != (T, hkv, d):
+        raise ValueError("key and value must be [num_tokens, num_kv_heads, head_dim]")
+    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache must match")
+    if any(t.dtype != k_cache.dtype for t in (query_out, query, key, value, v_cache)):
+        raise TypeError("query, key, value and the caches must have one dtype")
+    rot = _rope_vectors(positions, inv_freq, T)
+    _on_current_device(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq)
+    po, so = _token_rows(query_out, "query_out")
+    pq, sq = _token_rows(query, "query")
+    pk, sk = _token_rows(key, "key")
+    pv, sv = _token_rows(value, "value")
+    _check(_lib.load().pa_rope_and_cache(po, so, pq, sq, pk, sk, pv, sv, _ptr(k_cache), _ptr(v_cache),
+                                         _ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), T, hq, nb, bs, hkv, d,
+                                         rot, int(layout), float(factor), _dtype(k_cache), _stream(stream)),
+           "pa_rope_and_cache")
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:

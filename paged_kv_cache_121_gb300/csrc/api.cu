@@ -717,6 +717,28 @@ pa_status check_prefix_call(const DecodeShape &s, pa_dtype q_dtype, pa_dtype kv_
     return PA_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------
+// What pa_rope and pa_rope_and_cache check alike; the strides are in elements.
+pa_status check_rope(int num_tokens, int num_heads, int head_dim, int rotary_dim, int layout, float factor,
+                     pa_dtype dtype) {
+    if (num_tokens < 0 || num_heads <= 0 || head_dim <= 0 || rotary_dim <= 0 || rotary_dim % 2 != 0 ||
+        rotary_dim > head_dim || !valid_dtype(dtype) || !std::isfinite(factor))
+        return PA_ERR_INVALID_ARG;
+    if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_INVALID_ARG;
+    if (head_dim > kRopeMaxHeadDim || num_heads > 65535) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+bool aligned_to(const void *p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// A view's base holds whole elements, and its token rows do not overlap.
+bool rope_view_ok(const void *ptr, int64_t stride, int heads, int head_dim, pa_dtype dtype) {
+    return aligned_to(ptr, static_cast<unsigned>(element_bytes(dtype))) &&
+           stride >= static_cast<int64_t>(heads) * head_dim;
+}
+
 }  // namespace
 
 int *device_status_word() {
@@ -1162,6 +1184,143 @@ PA_API pa_status pa_lse_merge(void *out, pa_dtype out_dtype, const float *tmp_ou
                                      context_lens, num_seqs, num_heads, head_dim, max_partitions,
                                      partition_size, sms, as_stream(stream));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_rope_frequencies(double *inv_freq, float *factor, int rotary_dim, double base,
+                                     pa_rope_scaling kind, double scale, int original_context, double low,
+                                     double high) {
+    if (!inv_freq || !factor || rotary_dim <= 0 || rotary_dim % 2 != 0 || !std::isfinite(base) || base <= 1.0)
+        return PA_ERR_INVALID_ARG;
+    if (kind != PA_ROPE_UNSCALED && (!std::isfinite(scale) || scale <= 0.0)) return PA_ERR_INVALID_ARG;
+    if (kind == PA_ROPE_YARN || kind == PA_ROPE_BANDS) {
+        // low and high: full turns over the original context below / above which a pair is
+        // interpolated / kept
+        if (original_context <= 0 || !std::isfinite(low) || !std::isfinite(high) || low <= 0.0 || high <= low)
+            return PA_ERR_INVALID_ARG;
+    }
+    const int pairs = rotary_dim / 2;
+    const double two_pi = 6.283185307179586;
+    *factor = 1.0f;
+    switch (kind) {
+        case PA_ROPE_UNSCALED:
+        case PA_ROPE_LINEAR:
+            for (int i = 0; i < pairs; ++i)
+                inv_freq[i] = std::pow(base, -2.0 * i / rotary_dim) / (kind == PA_ROPE_LINEAR ? scale : 1.0);
+            return PA_OK;
+        case PA_ROPE_NTK: {
+            if (rotary_dim <= 2) return PA_ERR_INVALID_ARG;
+            const double b = base * std::pow(scale, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+            for (int i = 0; i < pairs; ++i) inv_freq[i] = std::pow(b, -2.0 * i / rotary_dim);
+            return PA_OK;
+        }
+        case PA_ROPE_YARN: {
+            // the (fractional) pair that makes n turns over the original context
+            auto pair_of = [&](double n) {
+                return rotary_dim * std::log(original_context / (n * two_pi)) / (2.0 * std::log(base));
+            };
+            const double first = std::max(std::floor(pair_of(high)), 0.0);
+            const double last = std::min(std::ceil(pair_of(low)), rotary_dim - 1.0);
+            for (int i = 0; i < pairs; ++i) {
+                const double f = std::pow(base, -2.0 * i / rotary_dim);
+                const double ramp = std::min(std::max((i - first) / std::max(last - first, 1e-3), 0.0), 1.0);
+                inv_freq[i] = f / scale * ramp + f * (1.0 - ramp);
+            }
+            *factor = scale > 1.0 ? static_cast<float>(0.1 * std::log(scale) + 1.0) : 1.0f;
+            return PA_OK;
+        }
+        case PA_ROPE_BANDS:
+            for (int i = 0; i < pairs; ++i) {
+                const double f = std::pow(base, -2.0 * i / rotary_dim);
+                const double turns = original_context * f / two_pi;
+                const double keep = std::min(std::max((turns - low) / (high - low), 0.0), 1.0);
+                inv_freq[i] = (1.0 - keep) * f / scale + keep * f;
+            }
+            return PA_OK;
+    }
+    return PA_ERR_INVALID_ARG;
+}
+
+PA_API pa_status pa_rope(void *out, int64_t out_stride, const void *x, int64_t x_stride, const int32_t *positions,
+                         const double *inv_freq, int num_tokens, int num_heads, int head_dim, int rotary_dim,
+                         pa_rope_layout layout, float factor, int transpose, pa_dtype dtype, void *stream) {
+    pa_status st = check_rope(num_tokens, num_heads, head_dim, rotary_dim, layout, factor, dtype);
+    if (st != PA_OK) return st;
+    if (num_tokens == 0) return PA_OK;
+    if (!out || !x || !positions || !inv_freq) return PA_ERR_INVALID_ARG;
+    if (!rope_view_ok(out, out_stride, num_heads, head_dim, dtype) ||
+        !rope_view_ok(x, x_stride, num_heads, head_dim, dtype) || !aligned_to(positions, 4) ||
+        !aligned_to(inv_freq, 8))
+        return PA_ERR_INVALID_ARG;
+    int dev;
+    if ((st = current_device(&dev)) != PA_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return PA_ERR_CUDA;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = x;
+    p.out = out;
+    p.x_stride = x_stride;
+    p.out_stride = out_stride;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.head_dim = head_dim;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = layout == PA_ROPE_INTERLEAVED;
+    p.transpose = transpose != 0;
+    p.factor = factor;
+    return launch_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
+                                   int64_t query_stride, const void *key, int64_t key_stride, const void *value,
+                                   int64_t value_stride, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                   const int32_t *positions, const double *inv_freq, int num_tokens, int num_heads,
+                                   int num_blocks, int block_size, int num_kv_heads, int head_dim, int rotary_dim,
+                                   pa_rope_layout layout, float factor, pa_dtype dtype, void *stream) {
+    pa_status st = check_rope(num_tokens, num_heads, head_dim, rotary_dim, layout, factor, dtype);
+    if (st != PA_OK) return st;
+    if (num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
+    if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if ((static_cast<int64_t>(num_kv_heads) * head_dim * element_bytes(dtype)) % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PA_OK;
+    if (!query_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq)
+        return PA_ERR_INVALID_ARG;
+    if (!rope_view_ok(query_out, query_out_stride, num_heads, head_dim, dtype) ||
+        !rope_view_ok(query, query_stride, num_heads, head_dim, dtype) ||
+        !rope_view_ok(key, key_stride, num_kv_heads, head_dim, dtype) ||
+        !rope_view_ok(value, value_stride, num_kv_heads, head_dim, dtype) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned_to(slot_mapping, 8) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))
+        return PA_ERR_INVALID_ARG;
+    int dev;
+    if ((st = current_device(&dev)) != PA_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return PA_ERR_CUDA;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = query;
+    p.out = query_out;
+    p.key = key;
+    p.value = value;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.x_stride = query_stride;
+    p.out_stride = query_out_stride;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = layout == PA_ROPE_INTERLEAVED;
+    p.factor = factor;
+    return launch_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_device_status(int *status, int clear, void *stream) {

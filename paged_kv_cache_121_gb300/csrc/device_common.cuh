@@ -142,6 +142,25 @@ struct PrefixParams {
     float scale_log2;
 };
 
+// Rotary positions (rope.cu): heads of x rotated into out and, with
+// num_kv_heads > 0, keys rotated and values copied into their cache slots.
+struct RopeParams {
+    const void *x;              // [num_tokens, num_heads, head_dim], token rows x_stride elements apart
+    void *out;                  // the same, out_stride apart (may be x itself)
+    const void *key, *value;    // [num_tokens, num_kv_heads, head_dim], or null with num_kv_heads 0
+    void *k_cache, *v_cache;    // [num_slots, num_kv_heads, head_dim]
+    const int64_t *slot_mapping;
+    const int32_t *positions;   // [num_tokens]; negative: padding, nothing is written
+    const double *inv_freq;     // [rotary_dim / 2] radians a position
+    int64_t x_stride, out_stride, key_stride, value_stride;   // elements
+    int64_t num_slots;
+    int num_tokens, num_heads, num_kv_heads, head_dim, rotary_dim;
+    int interleaved, transpose;
+    float factor;               // multiplies cos and sin
+    int tokens_per_cta, heads_per_cta;   // set by the launcher
+};
+constexpr int kRopeMaxHeadDim = 256;
+
 // Raise a kernel's dynamic shared-memory limit once per device (host side;
 // keeps the call out of CUDA-graph capture after the first launch). Each
 // kernel instantiation passes its own `done` mask (bit d: device d set up).

@@ -9,6 +9,7 @@ namespace pa {
 
 struct DecodeParams;
 struct PrefixParams;
+struct RopeParams;
 
 bool decode_mma_supported(int head_dim, int block_size);   // D 64/128, blocks of 1..256 (powers of two)
 int decode_mma_tile_tokens(int block_size);       // tokens per pipeline stage (16)
@@ -72,6 +73,8 @@ cudaError_t launch_lse_merge(void *out, int out_type, const float *tmp_out, cons
 cudaError_t launch_reshape_and_cache(const void *key, const void *value, void *k_cache,
                                      void *v_cache, const int64_t *slot_mapping, int num_tokens,
                                      int64_t num_slots, int row_bytes, cudaStream_t stream);
+// Rotary positions (rope.cu); `type` as kv_type. Sets p's launch fields.
+cudaError_t launch_rope(RopeParams &p, int type, int sms, cudaStream_t stream);
 // Arguments of a decode call (mirrors pa_decode, dtypes as pa_dtype values).
 struct DecodeCall {
     void *out;
