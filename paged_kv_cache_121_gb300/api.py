@@ -22,6 +22,9 @@ PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
 PA_ROPE_UNSCALED, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = 0, 1, 2, 3, 4
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class PAError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -54,6 +57,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:   # the handle without a Stream object around it (0.1 us against 3)
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -78,28 +83,29 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None
 
 
 def _on_current_device(*tensors) -> None:
-    """The kernels run on the current device's stream: every tensor has to live there."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    """The kernels run on a stream of the current device: every tensor has to live there."""
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else 0
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t.get_device() != dev:
             raise ValueError("tensors must be on the current CUDA device")
 
 
-def _token_rows(t: torch.Tensor, name: str):
-    """(pointer, token stride) of a [tokens, heads, head_dim] view whose heads are contiguous."""
-    T, h, d = (int(x) for x in t.shape)
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Token stride of a [tokens, heads, head_dim] view whose heads and dims are contiguous."""
+    T, h, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: heads and dims must be contiguous")
-    return t.data_ptr(), int(t.stride(0)) if T > 1 else h * d
+    return st if T > 1 else h * d
 
 
 def _rope_vectors(positions, inv_freq, num_tokens: int) -> int:
     """Check the position and frequency vectors; returns rotary_dim."""
-    if positions.dtype != torch.int32 or tuple(positions.shape) != (num_tokens,):
+    if positions.dtype != torch.int32 or positions.shape != (num_tokens,):
         raise TypeError("positions must be int32 [num_tokens]")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be float64 [rotary_dim / 2]")
-    return 2 * int(inv_freq.shape[0])
+    return 2 * inv_freq.shape[0]
 
 
 def pa_rope_frequencies(rotary_dim, base, scaling=PA_ROPE_UNSCALED, scale=1.0, original_context=0, low=1.0,
@@ -120,43 +126,41 @@ def pa_rope(out, x, positions, inv_freq, layout=PA_ROPE_HALF, factor=1.0, transp
     unwritten); ``inv_freq`` float64 [rotary_dim / 2] on the device. The token
     rows of either may be strided (heads and dims contiguous). ``transpose``
     applies the gradient of the rotation."""
-    T, h, d = (int(v) for v in x.shape)
-    if tuple(out.shape) != (T, h, d) or out.dtype != x.dtype:
+    T, h, d = x.shape
+    if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and dtype")
     rot = _rope_vectors(positions, inv_freq, T)
+    so, sx = _token_stride(out, "out"), _token_stride(x, "x")
     _on_current_device(out, x, positions, inv_freq)
-    po, so = _token_rows(out, "out")
-    px, sx = _token_rows(x, "x")
-    _check(_lib.load().pa_rope(po, so, px, sx, _ptr(positions), _ptr(inv_freq), T, h, d, rot, int(layout),
-                               float(factor), int(bool(transpose)), _dtype(x), _stream(stream)), "pa_rope")
+    _check(_lib.load().pa_rope(out.data_ptr(), so, x.data_ptr(), sx, _ptr(positions), _ptr(inv_freq), T, h, d, rot,
+                               layout, factor, bool(transpose), _dtype(x), _stream(stream)), "pa_rope")
 
 
 def pa_rope_and_cache(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
                       layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
     """:func:`pa_rope` on ``query`` [T, Hq, D] into ``query_out`` and on ``key`` [T, Hkv, D] into slot
     slot_mapping[i] (int64) of the caches, ``value`` copied beside it, in one launch."""
-    nb, bs, hkv, d = _cache_dims(k_cache)
-    T, hq, dq = (int(v) for v in query.shape)
-    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (T,):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("caches are [num_blocks, block_size, num_kv_heads, head_dim], both alike")
+    nb, bs, hkv, d = k_cache.shape
+    T, hq, _ = query.shape
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise TypeError("slot_mapping must be int64 [num_tokens]")
-    if dq != d or tuple(query_out.shape) != (T, hq, d):
+    if query.shape[2] != d or query_out.shape != query.shape:
         raise ValueError("query and query_out must be [num_tokens, num_heads, head_dim]")
-    if tuple(key.shape) != (T, hkv, d) or tuple(value.shape) != (T, hkv, d):
+    if key.shape != (T, hkv, d) or value.shape != key.shape:
         raise ValueError("key and value must be [num_tokens, num_kv_heads, head_dim]")
-    if tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise ValueError("k_cache and v_cache must match")
-    if any(t.dtype != k_cache.dtype for t in (query_out, query, key, value, v_cache)):
+    dt = k_cache.dtype
+    if not (dt == v_cache.dtype == query.dtype == query_out.dtype == key.dtype == value.dtype):
         raise TypeError("query, key, value and the caches must have one dtype")
     rot = _rope_vectors(positions, inv_freq, T)
+    so, sq = _token_stride(query_out, "query_out"), _token_stride(query, "query")
+    sk, sv = _token_stride(key, "key"), _token_stride(value, "value")
     _on_current_device(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq)
-    po, so = _token_rows(query_out, "query_out")
-    pq, sq = _token_rows(query, "query")
-    pk, sk = _token_rows(key, "key")
-    pv, sv = _token_rows(value, "value")
-    _check(_lib.load().pa_rope_and_cache(po, so, pq, sq, pk, sk, pv, sv, _ptr(k_cache), _ptr(v_cache),
-                                         _ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), T, hq, nb, bs, hkv, d,
-                                         rot, int(layout), float(factor), _dtype(k_cache), _stream(stream)),
-           "pa_rope_and_cache")
+    _check(_lib.load().pa_rope_and_cache(
+        query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv, _ptr(k_cache),
+        _ptr(v_cache), _ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), T, hq, nb, bs, hkv, d, rot, layout, factor,
+        _dtype(k_cache), _stream(stream)), "pa_rope_and_cache")
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:

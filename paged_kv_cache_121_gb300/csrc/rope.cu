@@ -32,32 +32,56 @@ namespace pa {
 
 namespace {
 
-constexpr int kRopeThreads = 128;   // a CTA's threads, unless one head takes more
-constexpr int kUnroll = 3;          // items a thread loads before using any
-constexpr int kMaxTokensPerCta = 8;
+// 128 threads x 3 (token, head) rows a thread, all loaded before any is used.
+// Measured on GB300 over 128 .. 320 threads x 2 .. 4 rows (bf16, heads of 128;
+// 8,192 tokens x 40 heads / 16,400-token append of 32 + 8 + 8 heads): this one
+// 31.0 / 64.8 us, 0.80 / 0.92 of the copy rate; the others 33.0 .. 37.3 / 69.7
+// .. 85.8 us. Small CTAs keep some loading while others wait for their angles.
+constexpr int kRopeThreads = 128;
+constexpr int kUnroll = 3;
+static_assert(kRopeMaxHeadDim <= 2 * kRopeThreads, "a head's threads fit a CTA");
 
-template <typename T>
-struct RopeElem;
-template <>
-struct RopeElem<float> {
-    __device__ static float get(float x) { return x; }
-    __device__ static float put(float x) { return x; }
-};
-template <>
-struct RopeElem<__nv_bfloat16> {
-    __device__ static float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-    __device__ static __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }   // one rounding, at the end
-};
-template <>
-struct RopeElem<__half> {
-    __device__ static float get(__half x) { return __half2float(x); }
-    __device__ static __half put(float x) { return __float2half_rn(x); }
-};
-
-// V elements moved at once.
+// V elements moved at once, two at a time in and out of fp32 (the one
+// rounding is at the end). 16-bit elements stay packed in 32-bit words until
+// they are used: unpacked early they cost the bf16 kernel 20 registers.
 template <typename T, int V>
-struct alignas(sizeof(T) * V) RopeVec {
-    T e[V];
+struct alignas(4 * V) RopeVec {      // fp32
+    float e[V];
+    __device__ float get(int i) const { return e[i]; }
+    __device__ void put(int i, float x) { e[i] = x; }
+    __device__ float2 get2(int i) const { return make_float2(e[2 * i], e[2 * i + 1]); }
+    __device__ void put2(int i, float2 x) {
+        e[2 * i] = x.x;
+        e[2 * i + 1] = x.y;
+    }
+};
+template <typename T, int V>
+struct alignas(2 * V) RopeVec16 {
+    uint32_t w[V / 2];
+};
+template <int V>
+struct alignas(2 * V) RopeVec<__nv_bfloat16, V> : RopeVec16<__nv_bfloat16, V> {
+    __device__ float2 get2(int i) const {
+        return make_float2(bf16_bits_to_float(this->w[i] & 0xffffu), __uint_as_float(this->w[i] & 0xffff0000u));
+    }
+    __device__ void put2(int i, float2 x) { this->w[i] = pack_bf16x2(x.x, x.y); }
+};
+template <int V>
+struct alignas(2 * V) RopeVec<__half, V> : RopeVec16<__half, V> {
+    __device__ float2 get2(int i) const { return __half22float2(*reinterpret_cast<const __half2 *>(&this->w[i])); }
+    __device__ void put2(int i, float2 x) { this->w[i] = pack_f16x2(x.x, x.y); }
+};
+template <>
+struct alignas(2) RopeVec<__nv_bfloat16, 1> {
+    __nv_bfloat16 e;
+    __device__ float get(int) const { return __bfloat162float(e); }
+    __device__ void put(int, float x) { e = __float2bfloat16_rn(x); }
+};
+template <>
+struct alignas(2) RopeVec<__half, 1> {
+    __half e;
+    __device__ float get(int) const { return __half2float(e); }
+    __device__ void put(int, float x) { e = __float2half_rn(x); }
 };
 
 // position * inv_freq as half turns in [-1, 1) (angle / pi).
@@ -83,123 +107,121 @@ __device__ __forceinline__ float half_turns(double inv_freq, int position) {
     return __ll2float_rn(static_cast<int64_t>(phase)) * 0x1p-63f;
 }
 
+// One CTA: tokens_per_cta tokens x heads_per_cta heads of the token's list
+// (query heads, key heads, value heads), at most `slots` x kUnroll of them.
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeMaxHeadDim)
+__global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ float2 cs[];   // [tokens of the CTA][rotary_dim / 2]: factor * (cos, sin)
-    __shared__ int s_pos[kMaxTokensPerCta];
-    __shared__ int64_t s_slot[kMaxTokensPerCta];
     grid_dependency_wait();
     grid_dependents_launch();
     const int pairs = p.rotary_dim / 2;
     const int tok0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.tokens_per_cta, p.num_tokens - tok0);
-    const int nrot = pairs / V;                                  // threads of a head that rotate (two vectors each)
-    const int per_head = nrot + (p.head_dim - p.rotary_dim) / V;   // and those that move a vector past rotary_dim
-    const int slots = static_cast<int>(blockDim.x) / per_head;   // heads in flight
-    const int u = threadIdx.x % per_head, hslot = threadIdx.x / per_head;
+    const int nrot = pairs / V;                                    // threads of a head that rotate (two vectors each)
+    const int pass = (p.head_dim - p.rotary_dim) / V;              // vectors past rotary_dim: two a thread too
+    const int npass = (pass + 1) / 2, per_head = nrot + npass;
+    const int slots = static_cast<int>(blockDim.x) / per_head;     // heads in flight
+    const int hslot = threadIdx.x / per_head, u = threadIdx.x - hslot * per_head;
     const int head0 = blockIdx.y * p.heads_per_cta;
     const int nheads = min(p.heads_per_cta, p.num_heads + 2 * p.num_kv_heads - head0);
-    const int iters = (nheads + slots - 1) / slots;              // per token
     const bool rotates = u < nrot;
+    const bool two = rotates || u - nrot + npass < pass;
     // element offsets of the thread's vectors within a head
     const int off_a = !rotates ? p.rotary_dim + (u - nrot) * V : (kInterleaved && V == 1) ? 2 * u : u * V;
-    const int off_b = (kInterleaved && V == 1) ? 2 * u + 1 : pairs + u * V;
+    const int off_b = !rotates ? off_a + npass * V : (kInterleaved && V == 1) ? 2 * u + 1 : pairs + u * V;
 
-    for (int i = threadIdx.x; i < ntok; i += blockDim.x) {
-        s_pos[i] = p.positions[tok0 + i];
-        if (p.num_kv_heads) s_slot[i] = p.slot_mapping[tok0 + i];
+    // every load of the CTA is on its way before the angles are computed
+    using Vec = RopeVec<T, V>;
+    Vec a[kUnroll], b[kUnroll];
+    int tok[kUnroll], head[kUnroll];   // token within the CTA (-1: none), head of the list
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+        const int n = hslot + k * slots;
+        const int t = n / nheads;
+        tok[k] = t < ntok ? t : -1;
+        head[k] = head0 + (n - t * nheads);
+        if (t >= ntok) continue;
+        const int64_t at = tok0 + t;
+        const int kv = head[k] - p.num_heads;
+        const T *src = kv < 0 ? static_cast<const T *>(p.x) + at * p.x_stride + static_cast<int64_t>(head[k]) * p.head_dim
+                       : kv < p.num_kv_heads
+                           ? static_cast<const T *>(p.key) + at * p.key_stride + static_cast<int64_t>(kv) * p.head_dim
+                           : static_cast<const T *>(p.value) + at * p.value_stride +
+                                 static_cast<int64_t>(kv - p.num_kv_heads) * p.head_dim;
+        a[k] = *reinterpret_cast<const Vec *>(src + off_a);
+        if (two) b[k] = *reinterpret_cast<const Vec *>(src + off_b);
     }
+
     for (int i = threadIdx.x; i < ntok * pairs; i += blockDim.x) {
+        const int t = i / pairs;
         float sn, cn;
-        sincospif(half_turns(p.inv_freq[i % pairs], p.positions[tok0 + i / pairs]), &sn, &cn);
+        sincospif(half_turns(p.inv_freq[i - t * pairs], p.positions[tok0 + t]), &sn, &cn);
         cs[i] = make_float2(cn * p.factor, p.transpose ? -sn * p.factor : sn * p.factor);
     }
     __syncthreads();
-    if (hslot >= slots) return;
 
-    using Vec = RopeVec<T, V>;
-    const int total = ntok * iters;
-    for (int base = 0; base < total; base += kUnroll) {
-        Vec a[kUnroll], b[kUnroll];
-        const T *src[kUnroll];
-        T *dst[kUnroll];
-        bool turn[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int it = base + k;
-            const int t = it / iters, h = head0 + (it - t * iters) * slots + hslot;
-            src[k] = nullptr;
-            dst[k] = nullptr;
-            turn[k] = false;
-            if (it >= total || h >= head0 + nheads || s_pos[t] < 0) continue;   // a negative position: padding
-            const int64_t tok = tok0 + t;
-            const int kv = h - p.num_heads;
-            if (kv < 0) {
-                src[k] = static_cast<const T *>(p.x) + tok * p.x_stride + static_cast<int64_t>(h) * p.head_dim;
-                dst[k] = static_cast<T *>(p.out) + tok * p.out_stride + static_cast<int64_t>(h) * p.head_dim;
-                turn[k] = rotates;
-            } else {
-                const int64_t slot = s_slot[t];
-                if (slot < 0 || slot >= p.num_slots) continue;
-                const bool is_v = kv >= p.num_kv_heads;
-                const int64_t head = is_v ? kv - p.num_kv_heads : kv;
-                src[k] = static_cast<const T *>(is_v ? p.value : p.key) + tok * (is_v ? p.value_stride : p.key_stride) +
-                         head * p.head_dim;
-                dst[k] = static_cast<T *>(is_v ? p.v_cache : p.k_cache) + (slot * p.num_kv_heads + head) * p.head_dim;
-                turn[k] = rotates && !is_v;
-            }
-            a[k] = *reinterpret_cast<const Vec *>(src[k] + off_a);
-            if (rotates) b[k] = *reinterpret_cast<const Vec *>(src[k] + off_b);
+    for (int k = 0; k < kUnroll; ++k) {
+        if (tok[k] < 0) continue;
+        const int64_t at = tok0 + tok[k];
+        if (p.positions[at] < 0) continue;   // padding
+        const int kv = head[k] - p.num_heads;
+        T *dst;
+        if (kv < 0) {
+            dst = static_cast<T *>(p.out) + at * p.out_stride + static_cast<int64_t>(head[k]) * p.head_dim;
+        } else {
+            const int64_t slot = p.slot_mapping[at];
+            if (slot < 0 || slot >= p.num_slots) continue;
+            dst = kv < p.num_kv_heads
+                      ? static_cast<T *>(p.k_cache) + (slot * p.num_kv_heads + kv) * p.head_dim
+                      : static_cast<T *>(p.v_cache) + (slot * p.num_kv_heads + kv - p.num_kv_heads) * p.head_dim;
         }
+        if (rotates && kv < p.num_kv_heads) {
+            const float2 *c = cs + tok[k] * pairs;
+            if constexpr (V == 1) {                  // the pair is the two elements
+                const float2 cc = c[u];
+                const float x = a[k].get(0), y = b[k].get(0);
+                a[k].put(0, x * cc.x - y * cc.y);
+                b[k].put(0, y * cc.x + x * cc.y);
+            } else if constexpr (kInterleaved) {     // pairs inside each vector
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            if (!dst[k]) continue;
-            if (turn[k]) {
-                const float2 *c = cs + ((base + k) / iters) * pairs;
-                if constexpr (kInterleaved && V > 1) {   // pairs inside each vector
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 ca = c[u * (V / 2) + i], cb = c[pairs / 2 + u * (V / 2) + i];
+                    const float2 x = a[k].get2(i), y = b[k].get2(i);
+                    a[k].put2(i, make_float2(x.x * ca.x - x.y * ca.y, x.y * ca.x + x.x * ca.y));
+                    b[k].put2(i, make_float2(y.x * cb.x - y.y * cb.y, y.y * cb.x + y.x * cb.y));
+                }
+            } else {                                 // pairs across the two vectors
 #pragma unroll
-                    for (int e = 0; e < V; e += 2) {
-                        const float2 ca = c[(u * V + e) / 2], cb = c[(pairs + u * V + e) / 2];
-                        const float x0 = RopeElem<T>::get(a[k].e[e]), y0 = RopeElem<T>::get(a[k].e[e + 1]);
-                        const float x1 = RopeElem<T>::get(b[k].e[e]), y1 = RopeElem<T>::get(b[k].e[e + 1]);
-                        a[k].e[e] = RopeElem<T>::put(x0 * ca.x - y0 * ca.y);
-                        a[k].e[e + 1] = RopeElem<T>::put(y0 * ca.x + x0 * ca.y);
-                        b[k].e[e] = RopeElem<T>::put(x1 * cb.x - y1 * cb.y);
-                        b[k].e[e + 1] = RopeElem<T>::put(y1 * cb.x + x1 * cb.y);
-                    }
-                } else {                                 // a pair across the two vectors
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float2 cc = c[u * V + e];
-                        const float x = RopeElem<T>::get(a[k].e[e]), y = RopeElem<T>::get(b[k].e[e]);
-                        a[k].e[e] = RopeElem<T>::put(x * cc.x - y * cc.y);
-                        b[k].e[e] = RopeElem<T>::put(y * cc.x + x * cc.y);
-                    }
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 c0 = c[u * V + 2 * i], c1 = c[u * V + 2 * i + 1];
+                    const float2 x = a[k].get2(i), y = b[k].get2(i);
+                    a[k].put2(i, make_float2(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y));
+                    b[k].put2(i, make_float2(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y));
                 }
             }
-            *reinterpret_cast<Vec *>(dst[k] + off_a) = a[k];
-            if (rotates) *reinterpret_cast<Vec *>(dst[k] + off_b) = b[k];
         }
+        *reinterpret_cast<Vec *>(dst + off_a) = a[k];
+        if (two) *reinterpret_cast<Vec *>(dst + off_b) = b[k];
     }
 }
 
 template <typename T, int V>
 cudaError_t launch_rope_vec(RopeParams &p, int sms, cudaStream_t stream) {
-    const int per_head = p.rotary_dim / 2 / V + (p.head_dim - p.rotary_dim) / V;
-    const int threads = per_head > kRopeThreads ? per_head : kRopeThreads / per_head * per_head;
-    const int slots = threads / per_head;
+    const int per_head = p.rotary_dim / 2 / V + ((p.head_dim - p.rotary_dim) / V + 1) / 2;
+    const int slots = kRopeThreads / per_head;
+    const int threads = slots * per_head;
     const int heads = p.num_heads + 2 * p.num_kv_heads;
-    // Many tokens: a CTA takes every head of a few tokens (angles shared by all).
-    // Few tokens: one item a thread, the heads of a token over several CTAs.
-    const bool few = static_cast<int64_t>(p.num_tokens) * heads < static_cast<int64_t>(sms) * slots * 4;
-    p.heads_per_cta = few ? slots : heads;
-    int tpc = few ? 1 : p.num_tokens / (sms * 8);
-    tpc = tpc < 1 ? 1 : tpc > kMaxTokensPerCta ? kMaxTokensPerCta : tpc;
-    p.tokens_per_cta = tpc;
-    const dim3 grid(static_cast<unsigned>((p.num_tokens + tpc - 1) / tpc),
+    // Few (token, head) rows: one a thread, so that a step's latency is one row's.
+    // Many: kUnroll rows a thread, of whole tokens where they fit (angles shared by their heads).
+    const bool few = static_cast<int64_t>(p.num_tokens) * heads <= static_cast<int64_t>(sms) * slots * 2;
+    const int rows = few ? slots : slots * kUnroll;
+    p.heads_per_cta = heads < rows ? heads : rows;
+    p.tokens_per_cta = rows / p.heads_per_cta;
+    const dim3 grid(static_cast<unsigned>((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta),
                     static_cast<unsigned>((heads + p.heads_per_cta - 1) / p.heads_per_cta));
-    const size_t smem = static_cast<size_t>(tpc) * (p.rotary_dim / 2) * sizeof(float2);
+    const size_t smem = static_cast<size_t>(p.tokens_per_cta) * (p.rotary_dim / 2) * sizeof(float2);
     return p.interleaved ? launch_kernel(rope_kernel<T, V, true>, grid, dim3(threads), smem, stream, 1u, p)
                          : launch_kernel(rope_kernel<T, V, false>, grid, dim3(threads), smem, stream, 1u, p);
 }
@@ -210,7 +232,6 @@ int rope_vector(const RopeParams &p, int elem_bytes) {
     auto fits = [&](int v) {
         const int pairs = p.rotary_dim / 2;
         if (pairs % v || (p.head_dim - p.rotary_dim) % v) return false;
-        if (p.head_dim / v > kRopeThreads * 2) return false;
         auto ok = [&](const void *ptr, int64_t stride) {
             return reinterpret_cast<uintptr_t>(ptr) % (static_cast<uintptr_t>(v) * elem_bytes) == 0 && stride % v == 0;
         };
