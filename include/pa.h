@@ -310,6 +310,71 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
                                   void *stream);
 
 /* ------------------------------------------------------------------------
+ * Attention of several query tokens a sequence over the paged cache: whole
+ * prompts, chunks of prompts behind an earlier part, drafted tokens to verify,
+ * and batches that mix them with single decode tokens. The keys and values of
+ * the query tokens themselves are in the cache already (pa_rope_and_cache or
+ * pa_reshape_and_cache wrote them).
+ *
+ *   query, out    [num_tokens, num_heads, head_dim], the sequences' query
+ *                 tokens one sequence after the other
+ *   query_start   [num_seqs + 1] int32, not decreasing: sequence b owns tokens
+ *                 query_start[b] .. query_start[b + 1] - 1. Rows before
+ *                 query_start[0] or at or past query_start[num_seqs] are left
+ *                 as they were.
+ *   context_lens  [num_seqs] int32: tokens in the cache, the query tokens
+ *                 included
+ *   causal        1: token i of the n query tokens of a sequence sees its
+ *                 first context - n + i + 1 tokens (the query tokens are the
+ *                 context's last ones); 0: every token sees the whole context
+ *                 (states of another sequence, kept in pages). A row that sees
+ *                 nothing is all zeros.
+ *   max_query_len, max_context_len
+ *                 host-side upper bounds; what lies past them is not attended
+ *                 and the rows of a longer query are undefined.
+ *   workspace     at least pa_prefill_workspace_size() bytes, 16-byte aligned,
+ *                 or NULL / 0 bytes: then no context is split between CTAs,
+ *                 which costs time where there are few query tokens. Its
+ *                 contents need no initialisation. Calls that share a
+ *                 workspace must not overlap on the GPU.
+ *   Supported: as pa_decode (head_dim 64 or 128, blocks of 1 to 256, q and kv
+ *   of one dtype, any out dtype, num_heads a multiple of num_kv_heads).
+ *   Scores, softmax statistics and output sums are held in fp32; 16-bit caches
+ *   on the tensor cores round the softmax's weights once to the caches' type.
+ *   A value row that some query rows of a tile do not see has to be finite:
+ *   its weight there is zero, and zero times infinity is not. Rows past a
+ *   context's length may hold anything.
+ * ---------------------------------------------------------------------- */
+PA_API size_t pa_prefill_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int max_query_len, int max_context_len,
+                                        pa_dtype kv_dtype);
+
+PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
+                            const void *k_cache, const void *v_cache, pa_dtype kv_dtype,
+                            const int32_t *block_tables, const int32_t *context_lens,
+                            const int32_t *query_start, int num_seqs, int num_tokens, int num_heads,
+                            int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                            int num_blocks, int max_query_len, int max_context_len, float scale, int causal,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Cross attention: every query token of a sequence over all of an encoder's
+ * states, whose count is unrelated to the query's. The states are contiguous,
+ * as the encoder's projection leaves them; for states kept in pages call
+ * pa_prefill with causal 0.
+ *   k, v          [num_seqs, max_states, num_kv_heads, head_dim]
+ *   state_lens    [num_seqs] int32 (at most max_states; 0 gives zero rows)
+ *   everything else as pa_prefill; workspace as pa_prefill_workspace_size()
+ *   with block_size 16
+ * ---------------------------------------------------------------------- */
+PA_API pa_status pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
+                                    const void *k, const void *v, pa_dtype kv_dtype, const int32_t *state_lens,
+                                    const int32_t *query_start, int num_seqs, int num_tokens, int num_heads,
+                                    int num_kv_heads, int head_dim, int max_states, int max_query_len,
+                                    int max_state_len, float scale, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* ------------------------------------------------------------------------
  * Decode attention for a batch whose sequences share their leading blocks.
  * [P1] "Copy-on-write: when two requests share a prefix" (several block
  * tables point at the same physical blocks, reference-counted); [P5]

@@ -236,6 +236,71 @@ def pa_decode_append(out, query, new_key, new_value, k_cache, v_cache, block_tab
                                        _ptr(workspace), ws_bytes, _stream(stream)), "pa_decode_append")
 
 
+def pa_prefill_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                              max_context_len, kv_dtype=PA_BF16) -> int:
+    return int(_lib.load().pa_prefill_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                                     block_size, max_query_len, max_context_len, kv_dtype))
+
+
+def _prefill_args(out, query, k, v, lens, query_start, workspace):
+    """Checks pa_prefill and pa_cross_attention share; returns the workspace's bytes."""
+    T, hq, d = query.shape
+    if out.shape != query.shape:
+        raise ValueError("out must have query's shape")
+    if k.dim() != 4 or v.shape != k.shape or k.shape[3] != d:
+        raise ValueError("keys and values are [blocks or sequences, tokens, num_kv_heads, head_dim], both alike")
+    if query.dtype != k.dtype or v.dtype != k.dtype:
+        raise TypeError("query, keys and values must have one dtype")
+    if lens.dtype != torch.int32 or query_start.dtype != torch.int32:
+        raise TypeError("lengths and query_start must be int32")
+    if lens.dim() != 1 or query_start.shape != (lens.shape[0] + 1,):
+        raise ValueError("query_start must be [num_seqs + 1]")
+    _on_current_device(out, query, k, v, lens, query_start)
+    if workspace is None:
+        return 0
+    _on_current_device(workspace, out)
+    return workspace.numel() * workspace.element_size()
+
+
+def pa_prefill(out, query, k_cache, v_cache, block_tables, context_lens, query_start, max_query_len, max_context_len,
+               scale, causal=True, workspace=None, stream=None) -> None:
+    """Attention of several query tokens a sequence over the paged cache into
+    ``out`` [T, Hq, D]: sequence b owns tokens ``query_start[b]`` to
+    ``query_start[b + 1]`` of ``query`` [T, Hq, D] (int32 [B + 1]), the last of
+    its ``context_lens[b]`` tokens. ``causal``: token i sees the context up to
+    itself; else all of it. ``workspace``: a uint8 tensor of at least
+    :func:`pa_prefill_workspace_size` bytes, or None (contexts are not split)."""
+    ws_bytes = _prefill_args(out, query, k_cache, v_cache, context_lens, query_start, workspace)
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != context_lens.shape[0]:
+        raise TypeError("block_tables must be int32 [num_seqs, max_blocks]")
+    _on_current_device(block_tables)
+    nb, bs, hkv, d = k_cache.shape
+    T, hq, _ = query.shape
+    _check(_lib.load().pa_prefill(_ptr(out), _dtype(out), _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache),
+                                  _dtype(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(query_start),
+                                  context_lens.shape[0], T, hq, hkv, d, bs, block_tables.shape[1], nb, max_query_len,
+                                  max_context_len, scale, bool(causal), _ptr(workspace), ws_bytes, _stream(stream)),
+           "pa_prefill")
+
+
+def pa_cross_attention(out, query, k, v, state_lens, query_start, max_query_len, max_state_len, scale, workspace=None,
+                       stream=None) -> None:
+    """Every query token of sequence b (tokens ``query_start[b]`` to
+    ``query_start[b + 1]`` of ``query`` [T, Hq, D]) over the first
+    ``state_lens[b]`` of an encoder's states ``k``, ``v`` [B, S, Hkv, D], into
+    ``out`` [T, Hq, D]. ``workspace`` as for :func:`pa_prefill`, sized with
+    block_size 16."""
+    ws_bytes = _prefill_args(out, query, k, v, state_lens, query_start, workspace)
+    if k.shape[0] != state_lens.shape[0]:
+        raise ValueError("keys and values are [num_seqs, max_states, num_kv_heads, head_dim]")
+    n, states, hkv, d = k.shape
+    T, hq, _ = query.shape
+    _check(_lib.load().pa_cross_attention(_ptr(out), _dtype(out), _ptr(query), _dtype(query), _ptr(k), _ptr(v),
+                                          _dtype(k), _ptr(state_lens), _ptr(query_start), n, T, hq, hkv, d, states,
+                                          max_query_len, max_state_len, scale, _ptr(workspace), ws_bytes,
+                                          _stream(stream)), "pa_cross_attention")
+
+
 def pa_swap_blocks(dst_k, dst_v, src_k, src_v, block_mapping, stream=None) -> None:
     """Copy blocks block_mapping[i, 0] of (src_k, src_v) to blocks
     block_mapping[i, 1] of (dst_k, dst_v); either pool may be a pinned host

@@ -739,6 +739,126 @@ bool rope_view_ok(const void *ptr, int64_t stride, int heads, int head_dim, pa_d
            stride >= static_cast<int64_t>(heads) * head_dim;
 }
 
+// ---------------------------------------------------------------------------
+// Several query tokens a sequence: prompts, chunks of prompts, verified drafts
+// (paged, causal or not), and cross attention (contiguous states)
+// ---------------------------------------------------------------------------
+struct PrefillShape {
+    int num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks;
+    int max_query, max_ctx;
+    int contig_stride;   // > 0: contiguous states
+};
+
+constexpr int kPrefillSimtCtasPerSm = 2;      // CTA slots the CUDA-core kernel's split fills
+constexpr int kPrefillSimtMinSplit = 256;     // tokens a piece, at least
+constexpr int kPrefillSimtMaxSplits = 16;
+
+struct PrefillPlan {
+    bool tall;                // CUDA-core kernel: 64-row tiles, else 16
+    int heads_per_tile, ntile, tile_tokens;
+    int64_t tiles;            // upper bound of the batch's row tiles (the lengths are on the device)
+    int nsplit;
+    size_t max_off, sum_off, total;   // workspace: partial outputs, maxima, sums
+};
+
+pa_status check_prefill(const PrefillShape &s, pa_dtype out_dtype, pa_dtype q_dtype, pa_dtype kv_dtype, float scale) {
+    if (s.num_seqs < 0 || s.num_tokens < 0 || s.max_query < 0 || s.max_ctx < 0 || s.num_heads <= 0 ||
+        s.num_kv_heads <= 0 || s.max_blocks <= 0 || s.num_blocks <= 0 || s.block_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (s.num_heads % s.num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    if (s.contig_stride > 0 ? s.max_ctx > s.contig_stride
+                            : static_cast<int64_t>(s.max_ctx) > static_cast<int64_t>(s.max_blocks) * s.block_size)
+        return PA_ERR_INVALID_ARG;
+    if (!valid_dtype(out_dtype) || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    const pa_status st = check_dtypes(q_dtype, kv_dtype);
+    if (st != PA_OK) return st;
+    if (s.head_dim != 64 && s.head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (s.block_size > 256 || s.num_heads > 65535) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+PrefillPlan plan_prefill(const PrefillShape &s, int sms, bool have_workspace) {
+    PrefillPlan pl{};
+    const int group = s.num_heads / s.num_kv_heads;
+    pl.tall = static_cast<int64_t>(s.max_query) * group > prefill_simt_rows(false);
+    const int rows = prefill_simt_rows(pl.tall);
+    pl.heads_per_tile = std::min(group, rows);
+    pl.ntile = (group + pl.heads_per_tile - 1) / pl.heads_per_tile;
+    pl.tile_tokens = rows / pl.heads_per_tile;
+    pl.tiles = std::min<int64_t>(static_cast<int64_t>(s.num_seqs) * cdiv64(s.max_query, pl.tile_tokens),
+                                 static_cast<int64_t>(s.num_tokens) / pl.tile_tokens + s.num_seqs);
+    pl.nsplit = 1;
+    const int64_t units = pl.tiles * s.num_kv_heads * pl.ntile;
+    const int64_t slots = static_cast<int64_t>(sms) * kPrefillSimtCtasPerSm;
+    if (have_workspace && units > 0 && units < slots)
+        pl.nsplit = static_cast<int>(std::max<int64_t>(
+            1, std::min<int64_t>({slots / units, cdiv64(s.max_ctx, kPrefillSimtMinSplit), kPrefillSimtMaxSplits})));
+    if (pl.nsplit > 1) {
+        const size_t rows_all = static_cast<size_t>(s.num_tokens) * s.num_heads * pl.nsplit;
+        pl.max_off = align256(rows_all * s.head_dim * sizeof(float));
+        pl.sum_off = pl.max_off + align256(rows_all * sizeof(float));
+        pl.total = pl.sum_off + align256(rows_all * sizeof(float));
+    }
+    return pl;
+}
+
+pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, const void *query, const void *k_cache,
+                      const void *v_cache, pa_dtype kv_dtype, const int32_t *block_tables,
+                      const int32_t *context_lens, const int32_t *query_start, float scale, bool causal,
+                      void *workspace, size_t workspace_bytes, void *stream) {
+    if (s.num_seqs == 0 || s.num_tokens == 0 || s.max_query == 0) return PA_OK;
+    if (!out || !query || !k_cache || !v_cache || !context_lens || !query_start ||
+        (s.contig_stride == 0 && !block_tables))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) || !aligned_to(query_start, 4))
+        return PA_ERR_INVALID_ARG;
+    int dev;
+    pa_status st = current_device(&dev);
+    if (st != PA_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return PA_ERR_CUDA;
+    const PrefillPlan pl = plan_prefill(s, sms, workspace != nullptr || workspace_bytes != 0);
+    if (pl.total && (!workspace || workspace_bytes < pl.total || !aligned16(workspace))) return PA_ERR_WORKSPACE;
+    const int64_t ytiles = static_cast<int64_t>(s.num_kv_heads) * pl.ntile;
+    if (pl.tiles > INT32_MAX || ytiles > 65535) return PA_ERR_UNSUPPORTED;
+    PrefillParams p;
+    std::memset(&p, 0, sizeof p);
+    p.query = query;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.out = out;
+    p.part_out = static_cast<float *>(workspace);
+    p.part_max = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.max_off);
+    p.part_sum = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.sum_off);
+    p.num_seqs = s.num_seqs;
+    p.num_tokens = s.num_tokens;
+    p.num_heads = s.num_heads;
+    p.num_kv_heads = s.num_kv_heads;
+    p.head_dim = s.head_dim;
+    p.group = s.num_heads / s.num_kv_heads;
+    p.block_size = s.block_size;
+    p.max_blocks = s.max_blocks;
+    p.num_blocks = s.num_blocks;
+    p.contig_stride = s.contig_stride;
+    p.max_query = s.max_query;
+    p.max_ctx = s.max_ctx;
+    p.causal = causal;
+    p.out_type = static_cast<int>(out_dtype);
+    p.heads_per_tile = pl.heads_per_tile;
+    p.ntile = pl.ntile;
+    p.tile_tokens = pl.tile_tokens;
+    p.nsplit = pl.nsplit;
+    p.scale_log2 = scale * kLog2e;
+    const dim3 grid(static_cast<unsigned>(pl.tiles), static_cast<unsigned>(ytiles), static_cast<unsigned>(pl.nsplit));
+    return launch_prefill_simt(p, static_cast<int>(kv_dtype), pl.tall, grid, as_stream(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
 }  // namespace
 
 int *device_status_word() {
@@ -1321,6 +1441,47 @@ PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, co
     p.interleaved = layout == PA_ROPE_INTERLEAVED;
     p.factor = factor;
     return launch_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_prefill_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int max_query_len, int max_context_len, pa_dtype kv_dtype) {
+    const PrefillShape s{num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, INT32_MAX / 256, 1,
+                         max_query_len, max_context_len, 0};
+    if (check_prefill(s, PA_F32, kv_dtype, kv_dtype, 1.f) != PA_OK || num_seqs == 0 || num_tokens == 0) return 0;
+    int dev;
+    if (current_device(&dev) != PA_OK) return 0;
+    const int sms = sm_count(dev);
+    return sms > 0 ? plan_prefill(s, sms, true).total : 0;
+}
+
+PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k_cache,
+                            const void *v_cache, pa_dtype kv_dtype, const int32_t *block_tables,
+                            const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_tokens,
+                            int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                            int num_blocks, int max_query_len, int max_context_len, float scale, int causal,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    const PrefillShape s{num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                         num_blocks, max_query_len, max_context_len, 0};
+    const pa_status st = check_prefill(s, out_dtype, q_dtype, kv_dtype, scale);
+    if (st != PA_OK) return st;
+    return run_prefill(s, out, out_dtype, query, k_cache, v_cache, kv_dtype, block_tables, context_lens, query_start,
+                       scale, causal != 0, workspace, workspace_bytes, stream);
+}
+
+PA_API pa_status pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k,
+                                    const void *v, pa_dtype kv_dtype, const int32_t *state_lens,
+                                    const int32_t *query_start, int num_seqs, int num_tokens, int num_heads,
+                                    int num_kv_heads, int head_dim, int max_states, int max_query_len,
+                                    int max_state_len, float scale, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    if (max_states <= 0) return PA_ERR_INVALID_ARG;
+    const PrefillShape s{num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, kContiguousTile, 1, 1,
+                         max_query_len, max_state_len, max_states};
+    const pa_status st = check_prefill(s, out_dtype, q_dtype, kv_dtype, scale);
+    if (st != PA_OK) return st;
+    if (static_cast<int64_t>(num_seqs) * max_states > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    return run_prefill(s, out, out_dtype, query, k, v, kv_dtype, nullptr, state_lens, query_start, scale, false,
+                       workspace, workspace_bytes, stream);
 }
 
 PA_API pa_status pa_device_status(int *status, int clear, void *stream) {

@@ -10,6 +10,7 @@ namespace pa {
 struct DecodeParams;
 struct PrefixParams;
 struct RopeParams;
+struct PrefillParams;
 
 bool decode_mma_supported(int head_dim, int block_size);   // D 64/128, blocks of 1..256 (powers of two)
 int decode_mma_tile_tokens(int block_size);       // tokens per pipeline stage (16)
@@ -75,6 +76,11 @@ cudaError_t launch_reshape_and_cache(const void *key, const void *value, void *k
                                      int64_t num_slots, int row_bytes, cudaStream_t stream);
 // Rotary positions (rope.cu); `type` as kv_type. Sets p's launch fields.
 cudaError_t launch_rope(RopeParams &p, int type, int sms, cudaStream_t stream);
+// Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid
+// (row tiles of the batch, Hkv * ntile, nsplit); `tall`: 64-row tiles, else 16.
+// With nsplit > 1 the merge is launched too.
+int prefill_simt_rows(bool tall);
+cudaError_t launch_prefill_simt(const PrefillParams &p, int kv_type, bool tall, dim3 grid, cudaStream_t stream);
 // Arguments of a decode call (mirrors pa_decode, dtypes as pa_dtype values).
 struct DecodeCall {
     void *out;
