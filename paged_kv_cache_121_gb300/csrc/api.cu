@@ -213,15 +213,17 @@ pa_status make_cache_map(CUtensorMap *map, const void *cache, int64_t num_blocks
 // Q: rows sequence * G + head, 128 bytes each, with the 128-byte swizzle (the
 // K-major operand layout of the tensor cores). Sequences past the batch read
 // as zeros.
+// box_heads > 0 takes that many heads of the group instead of all.
 pa_status make_query_group_map(CUtensorMap *map, const void *query, int num_seqs, int num_kv_heads, int group,
-                               int head_dim, int seqs, bool f16) {
+                               int head_dim, int seqs, bool f16, int box_heads = 0) {
     auto enc = tensor_map_encoder();
     if (!enc) return PA_ERR_CUDA;
     const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
     const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(head_dim / 64), static_cast<cuuint64_t>(group),
                                 static_cast<cuuint64_t>(num_kv_heads), static_cast<cuuint64_t>(num_seqs)};
     const cuuint64_t strides[4] = {128, row, row * group, row * group * num_kv_heads};
-    const cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(seqs)};
+    const cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(box_heads > 0 ? box_heads : group), 1,
+                               static_cast<cuuint32_t>(seqs)};
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                      const_cast<void *>(query), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -753,12 +755,19 @@ constexpr int kPrefillSimtCtasPerSm = 2;      // CTA slots the CUDA-core kernel'
 constexpr int kPrefillSimtMinSplit = 256;     // tokens a piece, at least
 constexpr int kPrefillSimtMaxSplits = 16;
 
+// A wave's units are cut between CTAs only below this many waves: above, an idle
+// tail is under a tenth of the work and the pieces' traffic is not worth it.
+constexpr int kPrefillCutWaves = 6;
+
 struct PrefillPlan {
-    bool tall;                // CUDA-core kernel: 64-row tiles, else 16
+    bool tc;                  // tensor-core kernel (else CUDA-core)
+    bool tall;                // tc: two row tiles a unit, else one; CUDA-core: 64-row tiles, else 16
     int heads_per_tile, ntile, tile_tokens;
     int64_t tiles;            // upper bound of the batch's row tiles (the lengths are on the device)
-    int nsplit;
-    size_t max_off, sum_off, total;   // workspace: partial outputs, maxima, sums
+    int ctas;                 // tc: the persistent grid
+    int nsplit;               // CUDA-core: pieces of a context; tc: 2 where the last wave may be cut
+    int max_tail;             // tc: units the cut wave can have
+    size_t max_off, sum_off, info_off, total;   // workspace: partial outputs, maxima, sums, tail layout
 };
 
 pa_status check_prefill(const PrefillShape &s, pa_dtype out_dtype, pa_dtype q_dtype, pa_dtype kv_dtype, float scale) {
@@ -777,18 +786,44 @@ pa_status check_prefill(const PrefillShape &s, pa_dtype out_dtype, pa_dtype q_dt
     return PA_OK;
 }
 
-PrefillPlan plan_prefill(const PrefillShape &s, int sms, bool have_workspace) {
+PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool have_workspace) {
     PrefillPlan pl{};
     const int group = s.num_heads / s.num_kv_heads;
-    pl.tall = static_cast<int64_t>(s.max_query) * group > prefill_simt_rows(false);
-    const int rows = prefill_simt_rows(pl.tall);
+    pl.tc = is16(kv_dtype) && prefill_tc_supported(s.head_dim, s.block_size, s.contig_stride > 0);
+    int rows;
+    if (pl.tc) {
+        rows = prefill_tc_rows();
+    } else {
+        pl.tall = static_cast<int64_t>(s.max_query) * group > prefill_simt_rows(false);
+        rows = prefill_simt_rows(pl.tall);
+    }
     pl.heads_per_tile = std::min(group, rows);
     pl.ntile = (group + pl.heads_per_tile - 1) / pl.heads_per_tile;
     pl.tile_tokens = rows / pl.heads_per_tile;
+    if (pl.tc) {
+        // more query tokens than one row tile holds: two share every K/V tile
+        pl.tall = s.max_query > pl.tile_tokens;
+        if (pl.tall) pl.tile_tokens *= 2;
+    }
     pl.tiles = std::min<int64_t>(static_cast<int64_t>(s.num_seqs) * cdiv64(s.max_query, pl.tile_tokens),
                                  static_cast<int64_t>(s.num_tokens) / pl.tile_tokens + s.num_seqs);
     pl.nsplit = 1;
     const int64_t units = pl.tiles * s.num_kv_heads * pl.ntile;
+    if (pl.tc) {
+        const int64_t slots = std::min(sms, prefill_tc_max_ctas());
+        const bool cut = have_workspace && units < slots * kPrefillCutWaves && s.max_ctx > 2 * prefill_tc_tile();
+        pl.ctas = static_cast<int>(cut ? slots : std::min(slots, std::max<int64_t>(units, 1)));
+        if (!cut) return pl;
+        pl.nsplit = 2;
+        pl.max_tail = static_cast<int>(std::min(units, slots));
+        // a piece's slot is its CTA plus its unit of the cut wave
+        const size_t pieces = static_cast<size_t>(slots + pl.max_tail) * (pl.tall ? 2 : 1) * rows;
+        pl.max_off = align256(pieces * s.head_dim * sizeof(float));
+        pl.sum_off = pl.max_off + align256(pieces * sizeof(float));
+        pl.info_off = pl.sum_off + align256(pieces * sizeof(float));
+        pl.total = pl.info_off + align256(prefill_tc_info_bytes());
+        return pl;
+    }
     const int64_t slots = static_cast<int64_t>(sms) * kPrefillSimtCtasPerSm;
     if (have_workspace && units > 0 && units < slots)
         pl.nsplit = static_cast<int>(std::max<int64_t>(
@@ -818,7 +853,7 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
     if (st != PA_OK) return st;
     const int sms = sm_count(dev);
     if (sms <= 0) return PA_ERR_CUDA;
-    const PrefillPlan pl = plan_prefill(s, sms, workspace != nullptr || workspace_bytes != 0);
+    const PrefillPlan pl = plan_prefill(s, kv_dtype, sms, workspace != nullptr || workspace_bytes != 0);
     if (pl.total && (!workspace || workspace_bytes < pl.total || !aligned16(workspace))) return PA_ERR_WORKSPACE;
     const int64_t ytiles = static_cast<int64_t>(s.num_kv_heads) * pl.ntile;
     if (pl.tiles > INT32_MAX || ytiles > 65535) return PA_ERR_UNSUPPORTED;
@@ -853,6 +888,25 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
     p.tile_tokens = pl.tile_tokens;
     p.nsplit = pl.nsplit;
     p.scale_log2 = scale * kLog2e;
+    if (pl.tc) {
+        p.status = status_word(dev);
+        if (!p.status) return PA_ERR_CUDA;
+        p.max_tail = pl.max_tail;
+        p.tail_info = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.info_off);
+        const bool contig = s.contig_stride > 0, f16 = kv_dtype == PA_F16;
+        // contiguous states [B, stride, Hkv, D] are mapped as one block of B * stride tokens
+        const int64_t blocks = contig ? 1 : s.num_blocks;
+        const int64_t tokens = contig ? static_cast<int64_t>(s.num_seqs) * s.contig_stride : s.block_size;
+        const int box = prefill_tc_box_tokens(s.block_size, contig);
+        CUtensorMap tk, tv, tq;
+        if ((st = make_cache_map(&tk, k_cache, blocks, tokens, s.num_kv_heads, s.head_dim, box, 1, 1, f16)) != PA_OK ||
+            (st = make_cache_map(&tv, v_cache, blocks, tokens, s.num_kv_heads, s.head_dim, box, 1, 0, f16)) != PA_OK ||
+            (st = make_query_group_map(&tq, query, s.num_tokens, s.num_kv_heads, p.group, s.head_dim,
+                                       pl.tall ? pl.tile_tokens / 2 : pl.tile_tokens, f16, pl.heads_per_tile)) != PA_OK)
+            return st;
+        return launch_prefill_tc(p, pl.tall, f16, tk, tv, tq, pl.ctas, as_stream(stream)) == cudaSuccess ? PA_OK
+                                                                                                       : PA_ERR_CUDA;
+    }
     const dim3 grid(static_cast<unsigned>(pl.tiles), static_cast<unsigned>(ytiles), static_cast<unsigned>(pl.nsplit));
     return launch_prefill_simt(p, static_cast<int>(kv_dtype), pl.tall, grid, as_stream(stream)) == cudaSuccess
                ? PA_OK
@@ -1451,7 +1505,7 @@ PA_API size_t pa_prefill_workspace_size(int num_seqs, int num_tokens, int num_he
     int dev;
     if (current_device(&dev) != PA_OK) return 0;
     const int sms = sm_count(dev);
-    return sms > 0 ? plan_prefill(s, sms, true).total : 0;
+    return sms > 0 ? plan_prefill(s, kv_dtype, sms, true).total : 0;
 }
 
 PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k_cache,

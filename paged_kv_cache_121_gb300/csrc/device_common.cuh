@@ -183,7 +183,10 @@ struct PrefillParams {
     int out_type;                 // public dtype code
     int heads_per_tile, ntile;    // query heads of a KV head in one tile; tiles of the group
     int tile_tokens;              // query tokens in a row tile
-    int nsplit;                   // prefill_simt: pieces a context is cut into
+    int nsplit;                   // prefill_simt: pieces a context is cut into; prefill_tc: 2 where the last
+                                  //   wave's units may be cut, else 1
+    int max_tail;                 // prefill_tc: units the cut wave can have
+    int *tail_info;               // prefill_tc: its layout, written for the merge
     float scale_log2;
 };
 

@@ -1,0 +1,981 @@
+// Attention of several query tokens a sequence on the fifth-generation tensor
+// cores (tcgen05 + tensor memory), sm_103a: 16-bit caches, paged in blocks of
+// 8 to 256 tokens (powers of two) or contiguous.
+//
+// Mathematics: O = softmax(scale Q K^T + mask) V, the softmax held as a running
+// maximum m and sum l of base-2 exponentials while 128-token K/V tiles stream
+// past. m only moves when a score passes it by more than 2^8 (then O and l are
+// rescaled): the result is the same, O is almost never touched.
+//
+// Rows. A row is (query token, query head); a KV head's rows are packed token
+// by token, heads_per_tile heads each, into tiles of at most 128 rows, one
+// tensor-memory lane each, so that a K/V tile is read once for all of them.
+// A unit of work is one (row tiles, KV head):
+//  * kTwoTiles: two row tiles share every K/V tile (many query tokens: bound by
+//    the matrix products, 256 rows to a K/V byte);
+//  * else one row tile whose K/V tiles the two softmax groups take in turn (few
+//    query tokens: bound by the cache's bytes), joined in the epilogue.
+// Either way two softmax groups of four warps alternate on the tensor cores:
+// while one group turns its scores into weights, the other's products run.
+//
+// CTA (12 warps, one CTA per SM, persistent over units):
+//  * warps 0-3, 4-7: softmax group 0, 1. One row a thread: scores from tensor
+//    memory, weights back into the same columns as the 16-bit A operand of the
+//    second product (no shared memory in between), then the epilogue.
+//  * warp 8: issues the MMAs: per tile S = Q K^T (128 x 128 x D) and O += P V
+//    (128 x D x 128). A group's next S overwrites its P: both run on the one
+//    tensor pipe in issue order.
+//  * warps 9, 10: K tiles, 64 tokens each; warp 11: the schedule, Q and V
+//    tiles. TMA boxes, one per cache block (at most 64 tokens); K one box per
+//    64-dim half, V both halves in one. A thread starts a box every ~50 ns, so
+//    blocks of 16 need three issuing warps.
+//
+// Schedule: whole units, CTA c taking c, c + C, ...; where the host allows, the
+// units of the last partial wave are cut into equal ranges of tiles over all
+// CTAs instead, pieces of a unit going to the workspace for the merge kernel.
+//
+// Tokens past a context's end: K's are masked after the product; V's rows are
+// zeroed in shared memory (a zero weight times a NaN is not zero). Every wait
+// is bounded; on expiry the kernel records a timeout, drains what it started
+// and frees its tensor memory.
+#include <climits>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kM = 128;              // rows of a row tile: tensor-memory lanes
+constexpr int kTile = 128;           // context tokens per K/V tile
+constexpr int kKSlots = 3, kVSlots = 2;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 11;
+constexpr int kSegs = 2;             // published segments in flight
+constexpr int kSegReaders = 11;      // MMA warp, two K warps, eight softmax warps
+constexpr float kSlack = 8.f;        // base-2 headroom before the running maximum moves
+constexpr int kMaxTail = 160;        // units of a partial wave: fewer than CTAs
+// p.tail_info: units of the cut wave, CTAs that share it | their tiles' prefix sums | unit descriptors
+constexpr int kTailPrefix = 2, kTailUnits = kTailPrefix + kMaxTail + 1, kTailInts = kTailUnits + 8 * kMaxTail;
+constexpr int kMinPiece = 4;         // tiles a CTA takes of a cut wave, at least
+
+template <int D, bool kTwoTiles>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kGroupsQ = kTwoTiles ? 2 : 1;      // row tiles of a unit
+    static constexpr int kQBytes = kHalves * kM * 128;      // one row tile
+    static constexpr int kSlotBytes = kHalves * kTile * 128;
+    static constexpr int kKOff = kGroupsQ * kQBytes;
+    static constexpr int kVOff = kKOff + kKSlots * kSlotBytes;
+    static constexpr int kBarOff = kVOff + kVSlots * kSlotBytes;
+};
+
+// One piece of a unit: K/V tiles [t0, t0 + n) of rows of one KV head.
+struct Seg {
+    int b, q0;            // sequence; first query token of the unit (in the batch)
+    int tok0, ntok;       // the same within the sequence; query tokens of the unit
+    int ctx, qlen;
+    int kvh, h0, nh;      // KV head; first query head of its group, heads here
+    int t0, n;
+    int cnt[2];           // tiles each softmax group takes
+    int piece;            // workspace slot, -1: the whole unit (final output), -2: no more work
+};
+
+struct Shared {
+    uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
+    uint64_t join_full[2];                 // one row tile: a group's maxima and sums are posted
+    uint64_t done;
+    uint32_t tmem;
+    int abort_flag;
+    int k_issued[2], v_issued, q_issued;   // tiles whose copies have been started
+    Seg seg[kSegs];
+    int tail_prefix[kMaxTail + 1];         // tiles of the cut wave's units, summed
+    int tail_work[kMaxTail];
+};
+struct SharedJoin {                        // one row tile, two groups: their maxima and sums
+    float m[2][2][kM], l[2][2][kM];        // [segment parity][group][row]
+};
+
+template <int D, bool kTwoTiles>
+constexpr size_t smem_bytes() {
+    return 1024 + Cfg<D, kTwoTiles>::kBarOff + sizeof(Shared) + (kTwoTiles ? 0 : sizeof(SharedJoin));
+}
+static_assert(smem_bytes<128, true>() <= 227 * 1024 && smem_bytes<128, false>() <= 227 * 1024, "shared memory of a CTA");
+
+// A whole warp waits; the answer is the same in all its lanes (a warp whose
+// lanes gave up at different times would part at its next warp-wide step).
+__device__ __forceinline__ bool wait_bar(const PrefillParams &p, Shared *sh, uint64_t *bar, uint32_t parity) {
+    bool ok = mbar_try_wait(smem_addr(bar), parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (!ok && !*reinterpret_cast<volatile int *>(&sh->abort_flag)) {
+        ok = mbar_wait(smem_addr(bar), parity);
+        if (!ok) {
+            record_status(p.status, kStatusTimeout);
+            *reinterpret_cast<volatile int *>(&sh->abort_flag) = 1;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit A packed two to a column.
+__device__ __forceinline__ void tc_mma_16bit_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Warp-wide: 128 consecutive fp32 columns of this warp's 32 lanes, one wait (in
+// the same block, so that no use is scheduled before it).
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+    uint32_t r[128];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+        "}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
+        "}, [%129];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr), "r"(taddr + 64)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    if constexpr (kF16) return pack_f16x2(a, b);
+    else return pack_bf16x2(a, b);
+}
+
+// Tiles a unit (row tiles from token tok0 of the sequence) has to visit.
+__device__ __forceinline__ int unit_tiles(const PrefillParams &p, const PrefillSeq &s, int tile) {
+    const int last = min((tile + 1) * p.tile_tokens, s.qlen) - 1;
+    return (prefill_sees(p, s, last) + kTile - 1) / kTile;
+}
+
+// ---------------------------------------------------------------------------
+// The schedule (one warp): segments of this CTA, in order.
+// ---------------------------------------------------------------------------
+struct Scheduler {
+    int64_t units, nfull;    // all units; units taken whole
+    int64_t next;            // next whole unit of this CTA
+    int tail, tail_ctas;     // units of the cut wave, CTAs that share it
+    int64_t tail_tiles, a, e;   // its tiles; this CTA's remaining range
+    int r;                   // unit of the cut wave that holds tile a
+    int tail_unit;           // unit of the cut wave handed out last
+    int base, before;        // resume point of the search: first sequence of a chunk, tiles before it
+};
+
+// Find row tile x at or after the scheduler's resume point (x never decreases
+// within the whole units, nor within the tail).
+__device__ __forceinline__ int sched_find(const PrefillParams &p, Scheduler &sc, int64_t x, int lane, int &tile, int &ntiles) {
+    for (; sc.base < p.num_seqs; sc.base += 32) {
+        const int b = sc.base + lane;
+        int n = 0;
+        if (b < p.num_seqs) n = (prefill_seq(p, b).qlen + p.tile_tokens - 1) / p.tile_tokens;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, x < sc.before + sum);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            tile = static_cast<int>(x - sc.before) - __shfl_sync(0xffffffffu, sum - n, l);
+            ntiles = __shfl_sync(0xffffffffu, n, l);
+            return sc.base + l;
+        }
+        sc.before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return -1;
+}
+
+template <bool kTwoTiles>
+__device__ __forceinline__ void fill_seg(const PrefillParams &p, Seg &g, int b, int tile, int y, int t0, int t1,
+                                         int piece) {
+    const PrefillSeq s = prefill_seq(p, b);
+    const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
+    g.b = b;
+    g.tok0 = tile * p.tile_tokens;
+    g.q0 = s.q0 + g.tok0;
+    g.ntok = min(p.tile_tokens, s.qlen - g.tok0);
+    g.ctx = s.ctx;
+    g.qlen = s.qlen;
+    g.kvh = y / p.ntile;
+    g.h0 = (y % p.ntile) * p.heads_per_tile;
+    g.nh = min(p.heads_per_tile, p.group - g.h0);
+    const int tiles = unit_tiles(p, s, tile);
+    g.t0 = t0;
+    g.n = max(0, min(t1, tiles) - t0);
+    if (kTwoTiles) {   // the first row tile may see one K/V tile fewer, the second may have no tokens
+        const int first = (prefill_sees(p, s, g.tok0 + min(row_tokens, g.ntok) - 1) + kTile - 1) / kTile;
+        g.cnt[0] = max(0, min(g.n, first - t0));
+        g.cnt[1] = g.ntok > row_tokens ? g.n : 0;
+    } else {
+        g.cnt[0] = (g.n + 1) / 2;
+        g.cnt[1] = g.n / 2;
+    }
+    g.piece = piece;
+}
+
+__device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, int lane) {
+    int64_t x = 0;
+    for (int b = lane; b < p.num_seqs; b += 32) x += (prefill_seq(p, b).qlen + p.tile_tokens - 1) / p.tile_tokens;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    const int ys = p.num_kv_heads * p.ntile;
+    const int ctas = gridDim.x;
+    sc.units = x * ys;
+    sc.nfull = sc.units;
+    sc.next = blockIdx.x;
+    sc.tail = 0;
+    sc.base = sc.before = 0;
+    sc.a = sc.e = 0;
+    sc.r = sc.tail_unit = 0;
+    sc.tail_ctas = 1;
+    sc.tail_tiles = 0;
+    const int64_t rem = sc.units % ctas;
+    // a wave that fills nine tenths of the CTAs is as good uncut, without the merge
+    if (p.nsplit > 1 && rem > 0 && rem * 10 < static_cast<int64_t>(ctas) * 9) {
+        sc.nfull = sc.units - rem;
+        sc.tail = static_cast<int>(rem);
+        // tiles of the tail's row tiles [x_lo, x_hi], lanes over sequences
+        const int64_t x_lo = sc.nfull / ys, x_hi = (sc.units - 1) / ys;
+        int64_t before = 0;
+        for (int base = 0; base < p.num_seqs; base += 32) {
+            const int b = base + lane;
+            PrefillSeq s{};
+            int n = 0;
+            if (b < p.num_seqs) {
+                s = prefill_seq(p, b);
+                n = (s.qlen + p.tile_tokens - 1) / p.tile_tokens;
+            }
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            const int64_t first = before + sum - n;                 // this sequence's row tiles: first .. first + n - 1
+            const int64_t lo = first > x_lo ? first : x_lo, hi = first + n - 1 < x_hi ? first + n - 1 : x_hi;
+            for (int64_t t = lo; t <= hi; ++t)
+                sh->tail_work[t - x_lo] = max(1, unit_tiles(p, s, n - 1 - static_cast<int>(t - first)));
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        __syncwarp();
+        int total = 0;
+        for (int r0 = 0; r0 < sc.tail; r0 += 32) {
+            const int r = r0 + lane;
+            const int w = r < sc.tail ? sh->tail_work[(sc.nfull + r) / ys - x_lo] : 0;
+            int sum = w;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            if (r < sc.tail) sh->tail_prefix[r + 1] = total + sum;
+            total += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) sh->tail_prefix[0] = 0;
+        __syncwarp();
+        sc.tail_tiles = total;
+        sc.tail_ctas = max(1, min(ctas, total / kMinPiece));
+        if (static_cast<int>(blockIdx.x) < sc.tail_ctas) {
+            sc.a = sc.tail_tiles * blockIdx.x / sc.tail_ctas;
+            sc.e = sc.tail_tiles * (blockIdx.x + 1) / sc.tail_ctas;
+            while (sc.a < sc.e && sh->tail_prefix[sc.r + 1] <= sc.a) ++sc.r;
+        }
+    }
+    if (blockIdx.x == 0 && p.nsplit > 1) {   // for the merge
+        for (int i = lane; i <= sc.tail; i += 32) p.tail_info[kTailPrefix + i] = sc.tail ? sh->tail_prefix[i] : 0;
+        if (lane == 0) {
+            p.tail_info[0] = sc.tail;
+            p.tail_info[1] = sc.tail_ctas;
+        }
+    }
+}
+
+// The next segment of this CTA into g (lane 0 writes it).
+template <bool kTwoTiles>
+__device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, Scheduler &sc, Seg &g, int lane) {
+    const int ys = p.num_kv_heads * p.ntile;
+    int64_t u;
+    int t0 = 0, t1 = INT_MAX, piece = -1;
+    if (sc.next < sc.nfull) {
+        u = sc.next;
+        sc.next += gridDim.x;
+    } else if (sc.a < sc.e) {
+        while (sh->tail_prefix[sc.r + 1] <= sc.a) ++sc.r;
+        sc.tail_unit = sc.r;
+        const int p0 = sh->tail_prefix[sc.r], p1 = sh->tail_prefix[sc.r + 1];
+        u = sc.nfull + sc.r;
+        t0 = static_cast<int>(sc.a) - p0;
+        t1 = static_cast<int>(sc.e < p1 ? sc.e : p1) - p0;
+        if (t0 > 0 || t1 < p1 - p0) piece = static_cast<int>(blockIdx.x) + sc.r;
+        sc.a = p0 + t1;
+    } else {
+        if (lane == 0) g.piece = -2;
+        return;
+    }
+    int tile = 0, ntiles = 0;
+    const int b = sched_find(p, sc, u / ys, lane, tile, ntiles);
+    // within a sequence the last row tile first: the longest work of a causal mask starts first
+    if (lane == 0) {
+        if (b < 0) g.piece = -2;
+        else fill_seg<kTwoTiles>(p, g, b, ntiles - 1 - tile, static_cast<int>(u % ys), t0, t1, piece);
+    }
+}
+
+// Tokens of one TMA box: a cache block, at most 64.
+__device__ __forceinline__ int box_tokens(const PrefillParams &p) {
+    return p.contig_stride > 0 ? 64 : min(p.block_size, 64);
+}
+
+// The ids of the blocks a producer warp is about to load, 32 at a time.
+struct BlockIds {
+    int first;     // block index of lane 0's entry; -1: nothing loaded
+    int id;
+};
+__device__ __forceinline__ int block_id(const PrefillParams &p, BlockIds &c, int b, int blk, int nblk, int lane) {
+    if (c.first < 0 || blk < c.first || blk >= c.first + 32) {
+        c.first = blk;
+        const int e = blk + lane;
+        c.id = e < nblk ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + e] : -1;
+    }
+    return __shfl_sync(0xffffffffu, c.id, blk - c.first);
+}
+
+template <int D, bool kTwoTiles, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                  const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ PrefillParams p) {
+    using C = Cfg<D, kTwoTiles>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *q_s = smem, *k_s = smem + C::kKOff, *v_s = smem + C::kVOff;
+    Shared *sh = reinterpret_cast<Shared *>(smem + C::kBarOff);
+    SharedJoin *join = reinterpret_cast<SharedJoin *>(sh + 1);   // one row tile only
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == kVWarp && lane == 0) {
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        for (int i = 0; i < kKSlots; ++i) {
+            mbar_init(smem_addr(&sh->k_full[i]), 2);
+            mbar_init(smem_addr(&sh->k_empty[i]), 1);
+        }
+        for (int i = 0; i < kVSlots; ++i) {
+            mbar_init(smem_addr(&sh->v_full[i]), 1);
+            mbar_init(smem_addr(&sh->v_empty[i]), 1);
+        }
+        mbar_init(smem_addr(&sh->q_full), 1);
+        mbar_init(smem_addr(&sh->q_empty), 1);
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(smem_addr(&sh->s_full[g]), 1);
+            mbar_init(smem_addr(&sh->p_full[g]), 4);
+            mbar_init(smem_addr(&sh->o_full[g]), 1);
+            mbar_init(smem_addr(&sh->o_free[g]), kTwoTiles ? 4 : 8);
+            mbar_init(smem_addr(&sh->join_full[g]), 4);
+        }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(smem_addr(&sh->seg_full[i]), 1);
+            mbar_init(smem_addr(&sh->seg_empty[i]), kSegReaders);
+        }
+        mbar_init(smem_addr(&sh->done), 1);
+        sh->abort_flag = 0;
+        sh->k_issued[0] = sh->k_issued[1] = sh->v_issued = sh->q_issued = 0;
+        mbar_fence_init();
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&sh->tmem), 512u);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    grid_dependency_wait();
+    // tensor-memory columns: S (and P) of group g at 128 g, O at 256 + 128 g
+    auto s_col = [&](int g) { return tmem + g * 128; };
+    auto o_col = [&](int g) { return tmem + 256 + g * 128; };
+    const int R = box_tokens(p);
+
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == kVWarp) {
+            // ---------------- the schedule, Q and V ----------------
+            Scheduler sc;
+            sched_init(p, sh, sc, lane);
+            const uint64_t policy = l2_policy_evict_normal(), q_policy = l2_policy_evict_first();
+            const int q_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
+            int tiles = 0;
+            for (int k = 0;; ++k) {
+                Seg *g = &sh->seg[k % kSegs];
+                if (k >= kSegs && !wait_bar(p, sh, &sh->seg_empty[k % kSegs], ((k / kSegs) - 1) & 1)) break;
+                sched_next<kTwoTiles>(p, sh, sc, *g, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh->seg_full[k % kSegs]));
+                if (g->piece == -2) break;
+                if (lane == 0 && g->piece >= 0 && g->t0 == 0) {   // a cut unit, for the merge
+                    int *d = p.tail_info + kTailUnits + sc.tail_unit * 8;
+                    d[0] = g->q0;
+                    d[1] = g->ntok;
+                    d[2] = g->kvh;
+                    d[3] = g->h0;
+                    d[4] = g->nh;
+                }
+                if (k > 0 && !wait_bar(p, sh, &sh->q_empty, (k - 1) & 1)) break;
+                if (lane == 0) {
+                    const uint32_t qf = smem_addr(&sh->q_full);
+                    mbar_arrive_expect_tx(qf, static_cast<uint32_t>(C::kGroupsQ * C::kHalves * q_tokens *
+                                                                    p.heads_per_tile * 128));
+                    // (dim, half, head in group, KV head, token): rows token * heads_per_tile + head
+                    for (int t = 0; t < C::kGroupsQ; ++t)
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tma_load_5d(smem_addr(q_s + t * C::kQBytes + h * (kM * 128)), &tmap_q, 0, h, g->h0, g->kvh,
+                                        g->q0 + t * q_tokens, qf, q_policy);
+                    sh->q_issued = k + 1;
+                }
+                BlockIds ids{-1, 0};
+                const int b = g->b, ctx = g->ctx, kvh = g->kvh, n = g->n, first = g->t0;
+                const int nblk = (ctx + p.block_size - 1) / p.block_size;
+                bool ok = true;
+                for (int i = 0; i < n && ok; ++i, ++tiles) {
+                    const int slot = tiles % kVSlots, t0 = (first + i) * kTile;
+                    if (tiles >= kVSlots && !wait_bar(p, sh, &sh->v_empty[slot], ((tiles / kVSlots) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int boxes = (min(ctx - t0, kTile) + R - 1) / R;
+                    const uint32_t full = smem_addr(&sh->v_full[slot]);
+                    const uint32_t dst = smem_addr(v_s + slot * C::kSlotBytes);
+                    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    for (int j = 0; j < boxes; ++j) {
+                        const int tok = t0 + j * R;
+                        int at = tok, blk = 0;
+                        if (p.contig_stride > 0) {
+                            at += b * p.contig_stride;
+                        } else {
+                            blk = block_id(p, ids, b, tok / p.block_size, nblk, lane);
+                            at = tok % p.block_size;
+                        }
+                        if (lane == 0)
+                            tma_load_5d(dst + j * (C::kHalves * R * 128), &tmap_v, 0, at, 0, kvh, blk, full, policy);
+                    }
+                    if (lane == 0) sh->v_issued = tiles + 1;
+                }
+                if (!ok) break;
+            }
+        } else if (warp != kMmaWarp) {
+            // ---------------- K, 64 tokens of every tile ----------------
+            const int part = warp - kKWarp;
+            const uint64_t policy = l2_policy_evict_normal();
+            int tiles = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const Seg *g = &sh->seg[k % kSegs];
+                if (!wait_bar(p, sh, &sh->seg_full[k % kSegs], (k / kSegs) & 1) || g->piece == -2) break;
+                const int b = g->b, ctx = g->ctx, kvh = g->kvh, n = g->n, first = g->t0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
+                const int nblk = (ctx + p.block_size - 1) / p.block_size;
+                BlockIds ids{-1, 0};
+                for (int i = 0; i < n; ++i, ++tiles) {
+                    const int slot = tiles % kKSlots, t0 = (first + i) * kTile + part * 64;
+                    if (tiles >= kKSlots && !wait_bar(p, sh, &sh->k_empty[slot], ((tiles / kKSlots) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int boxes = max(0, (min(ctx - t0, 64) + R - 1) / R);
+                    const uint32_t full = smem_addr(&sh->k_full[slot]);
+                    const uint32_t dst = smem_addr(k_s + slot * C::kSlotBytes) + part * 64 * 128;
+                    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    for (int j = 0; j < boxes; ++j) {
+                        const int tok = t0 + j * R;
+                        int at = tok, blk = 0;
+                        if (p.contig_stride > 0) {
+                            at += b * p.contig_stride;
+                        } else {
+                            blk = block_id(p, ids, b, tok / p.block_size, nblk, lane);
+                            at = tok % p.block_size;
+                        }
+                        if (lane == 0) {
+#pragma unroll
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tma_load_5d(dst + h * (kTile * 128) + j * (R * 128), &tmap_k, 0, at, h, kvh, blk, full,
+                                            policy);
+                        }
+                    }
+                    if (lane == 0) sh->k_issued[part] = tiles + 1;
+                }
+            }
+        } else {
+            // ---------------- MMA issue ----------------
+            constexpr uint32_t id_qk = idesc_16bit_f32(kM, kTile, false, false, kF16);
+            constexpr uint32_t id_pv = idesc_16bit_f32(kM, D, false, true, kF16);
+            // V boxes are [R tokens][128 bytes] per half, boxes of kHalves halves one after another
+            const uint32_t v_lbo = R * 128, v_sbo = R >= 16 ? 1024 : C::kHalves * 1024;
+            const int v_box = C::kHalves * R * 128, r_shift = 31 - __clz(R);
+            int kt = 0, vt = 0;                  // tiles whose K / V the products have taken
+            int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const Seg *g = &sh->seg[k % kSegs];
+                if (!wait_bar(p, sh, &sh->seg_full[k % kSegs], (k / kSegs) & 1) || g->piece == -2) break;
+                const int n = g->n, ctx = g->ctx, first = g->t0;
+                const int cnt[2] = {g->cnt[0], g->cnt[1]};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
+                if (!wait_bar(p, sh, &sh->q_full, k & 1)) break;
+                auto wait_k = [&]() { return wait_bar(p, sh, &sh->k_full[kt % kKSlots], (kt / kKSlots) & 1); };
+                auto issue_s = [&](int grp) {
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t qd = smem_desc_sw128(smem_addr(q_s + (kTwoTiles ? grp : 0) * C::kQBytes), 16, 1024);
+                        const uint64_t kd = smem_desc_sw128(smem_addr(k_s + (kt % kKSlots) * C::kSlotBytes), 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const int half = kk / 4, off = (kk % 4) * 32;
+                            tc_mma_16bit(s_col(grp), qd + desc_step(half * (kM * 128) + off),
+                                         kd + desc_step(half * (kTile * 128) + off), id_qk, kk > 0 ? 1u : 0u);
+                        }
+                        tc_commit(smem_addr(&sh->s_full[grp]));
+                    }
+                    __syncwarp();
+                };
+                auto release_k = [&]() {
+                    if (lane == 0) tc_commit(smem_addr(&sh->k_empty[kt % kKSlots]));
+                    ++kt;
+                };
+                // V of tile i has landed; rows past the context are zeroed
+                auto wait_v = [&](int i) {
+                    if (!wait_bar(p, sh, &sh->v_full[vt % kVSlots], (vt / kVSlots) & 1)) return false;
+                    const int valid = ctx - (first + i) * kTile;
+                    if (valid < kTile) {
+                        unsigned char *v = v_s + (vt % kVSlots) * C::kSlotBytes;
+                        for (int x = lane; x < (kTile - valid) * C::kHalves * 8; x += 32) {
+                            const int row = valid + x / (C::kHalves * 8), c = x % (C::kHalves * 8);
+                            *reinterpret_cast<uint4 *>(v + (row / R) * v_box + (c / 8) * (R * 128) + (row % R) * 128 +
+                                                       (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    return true;
+                };
+                auto issue_pv = [&](int grp, int j) {   // j: the group's tile
+                    if (!wait_bar(p, sh, &sh->p_full[grp], s_cnt[grp] & 1)) return false;
+                    if (j == 0 && o_cnt[grp] > 0 && !wait_bar(p, sh, &sh->o_free[grp], (o_cnt[grp] - 1) & 1)) return false;
+                    ++s_cnt[grp];
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t vd = smem_desc_sw128(smem_addr(v_s + (vt % kVSlots) * C::kSlotBytes), v_lbo, v_sbo);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk) {
+                            // (R is a power of two)
+                            const int off = R >= 16 ? ((kk * 16) >> r_shift) * v_box + ((kk * 16) & (R - 1)) * 128 : kk * 2 * v_box;
+                            tc_mma_16bit_ts(o_col(grp), s_col(grp) + kk * 8, vd + desc_step(off), id_pv,
+                                            (j > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                auto group_done = [&](int grp) {
+                    if (lane == 0) tc_commit(smem_addr(&sh->o_full[grp]));
+                    ++o_cnt[grp];
+                };
+                auto q_done = [&]() {
+                    if (lane == 0) tc_commit(smem_addr(&sh->q_empty));
+                };
+                if (n == 0) q_done();
+                if constexpr (kTwoTiles) {
+                    if (n > 0) {
+                        if (!wait_k()) break;
+                        for (int grp = 0; grp < 2; ++grp)
+                            if (cnt[grp] > 0) issue_s(grp);
+                        release_k();
+                        if (n == 1) q_done();
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        if (!wait_v(i)) { ok = false; break; }
+                        bool have_k = false;
+                        for (int grp = 0; grp < 2; ++grp) {
+                            if (i < cnt[grp]) {
+                                if (!issue_pv(grp, i)) { ok = false; break; }
+                                if (i == cnt[grp] - 1) group_done(grp);
+                            }
+                            if (grp == 1 && lane == 0) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
+                            if (i + 1 < cnt[grp]) {
+                                if (!have_k && !wait_k()) { ok = false; break; }
+                                have_k = true;
+                                issue_s(grp);
+                            }
+                        }
+                        ++vt;
+                        if (ok && i + 1 < n) {
+                            if (!have_k && !wait_k()) { ok = false; break; }
+                            release_k();
+                            if (i + 2 == n) q_done();
+                        }
+                    }
+                } else {
+                    for (int i = 0; i < min(n, 2) && ok; ++i) {
+                        if (!wait_k()) { ok = false; break; }
+                        issue_s(i);
+                        release_k();
+                        if (i == n - 1) q_done();
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int grp = i & 1;
+                        if (!wait_v(i) || !issue_pv(grp, i >> 1)) { ok = false; break; }
+                        if (lane == 0) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
+                        ++vt;
+                        if ((i >> 1) == cnt[grp] - 1) group_done(grp);
+                        if (i + 2 < n) {
+                            if (!wait_k()) { ok = false; break; }
+                            issue_s(grp);
+                            release_k();
+                            if (i + 3 == n) q_done();
+                        }
+                    }
+                }
+            }
+            // every MMA this thread issued has completed once `done` arrives
+            if (lane == 0) {
+                tc_commit(smem_addr(&sh->done));
+                if (!mbar_wait(smem_addr(&sh->done), 0)) record_status(p.status, kStatusTimeout);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------- softmax ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
+        const int rt = row / p.heads_per_tile, rh = row - rt * p.heads_per_tile;
+        const float sl2 = p.scale_log2;
+        int s_cnt = 0, o_cnt = 0, o_other = 0;   // tiles; segments in which this / the other group had any
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Seg *g = &sh->seg[k % kSegs];
+            if (!wait_bar(p, sh, &sh->seg_full[k % kSegs], (k / kSegs) & 1) || g->piece == -2) break;
+            const int cnt = g->cnt[grp], first = g->t0, piece = g->piece, q0 = g->q0;
+            const int tok = (kTwoTiles ? grp * row_tokens : 0) + rt;            // query token within the unit
+            const bool live = rt < row_tokens && tok < g->ntok && rh < g->nh;
+            // rows that are not there need no masking but the context's end: their outputs are never stored
+            const int sees = !live || !p.causal ? g->ctx : max(0, g->ctx - g->qlen + g->tok0 + tok + 1);
+            const int64_t orow = static_cast<int64_t>(q0 + tok) * p.num_heads + g->kvh * p.group + g->h0 + rh;
+            const int other = kTwoTiles ? 0 : g->cnt[grp ^ 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
+            const int whole = __reduce_min_sync(0xffffffffu, sees);             // every row of the warp sees these tokens
+            float m = -1e30f, l = 0.f;   // finite: a row that has seen nothing keeps l = 0 with no inf - inf
+            for (int j = 0; j < cnt; ++j) {
+                if (!wait_bar(p, sh, &sh->s_full[grp], s_cnt & 1)) { ok = false; break; }
+                ++s_cnt;
+                tc_fence_after();
+                const int t0 = (first + (kTwoTiles ? j : 2 * j + grp)) * kTile;
+                float s[kTile];
+                tmem_ld128(s_col(grp) + lanes, s);
+                float mul = sl2;
+                bool up = sl2 >= 0.f;
+                if (t0 + kTile > whole) {   // scaled here, so that -inf is the mask whatever the scale
+                    const int valid = sees - t0;
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) s[c] = c < valid ? s[c] * sl2 : -INFINITY;
+                    mul = 1.f;
+                    up = true;
+                }
+                float mx;
+                {
+                    float a[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) a[c] = s[c];
+                    if (up) {
+#pragma unroll
+                        for (int c = 4; c < kTile; ++c) a[c & 3] = fmaxf(a[c & 3], s[c]);
+                        mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                    } else {
+#pragma unroll
+                        for (int c = 4; c < kTile; ++c) a[c & 3] = fminf(a[c & 3], s[c]);
+                        mx = fminf(fminf(a[0], a[1]), fminf(a[2], a[3]));
+                    }
+                    mx *= mul;
+                }
+                const bool need = mx > m + kSlack;
+                const float m_new = need ? mx : m;
+                const float alpha = fast_exp2(m - m_new);
+                m = m_new;
+                l *= alpha;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c0 = 0; c0 < kTile; c0 += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float p0 = fast_exp2(fmaf(s[c0 + 2 * c], mul, -m));
+                        const float p1 = fast_exp2(fmaf(s[c0 + 2 * c + 1], mul, -m));
+                        sum[c & 3] += p0 + p1;
+                        w[c] = pack16<kF16>(p0, p1);   // the weights' one rounding, to the caches' type
+                    }
+                    tmem_st16_nowait(s_col(grp) + lanes + c0 / 2, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                // S of this tile was issued behind the group's previous P V: O is at rest here
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(o_col(grp) + lanes + c, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(o_col(grp) + lanes + c, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[grp]));
+            }
+            if (!ok) break;
+            // ---- epilogue ----
+            float inv = 0.f, wa = 1.f, wb = 0.f;   // O = inv * (wa O_grp + wb O_other)
+            if constexpr (!kTwoTiles) {            // the other group's share of the row
+                join->m[k & 1][grp][row] = m;
+                join->l[k & 1][grp][row] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh->join_full[grp]));
+                if (!wait_bar(p, sh, &sh->join_full[grp ^ 1], k & 1)) break;
+                const float mo = join->m[k & 1][grp ^ 1][row], lo = join->l[k & 1][grp ^ 1][row];
+                const float M = fmaxf(m, mo);
+                wa = cnt > 0 ? fast_exp2(m - M) : 0.f;
+                wb = other > 0 ? fast_exp2(mo - M) : 0.f;
+                l = (cnt > 0 ? l * wa : 0.f) + (other > 0 ? lo * wb : 0.f);
+                m = M;
+            }
+            inv = piece >= 0 ? 1.f : l > 0.f ? 1.f / l : l;   // pieces stay unnormalised; 0: an empty row; NaN stays
+            wa *= inv;
+            wb *= inv;
+            if (cnt > 0 && !wait_bar(p, sh, &sh->o_full[grp], o_cnt & 1)) break;
+            if (!kTwoTiles && other > 0 && !wait_bar(p, sh, &sh->o_full[grp ^ 1], o_other & 1)) break;
+            tc_fence_after();
+            // one row tile: each group writes half of the columns, from both groups' O
+            constexpr int kCols = kTwoTiles ? D : D / 2;
+            const int col0 = kTwoTiles ? 0 : grp * kCols;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) {
+                float o[32];
+                if (cnt > 0) {
+                    tmem_ld32(o_col(grp) + lanes + col0 + c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= wa;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (!kTwoTiles && other > 0) {
+                    float x[32];
+                    tmem_ld32(o_col(grp ^ 1) + lanes + col0 + c, x);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = fmaf(x[e], wb, o[e]);
+                }
+                if (c + 32 == kCols) {   // O has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (cnt > 0) mbar_arrive(smem_addr(&sh->o_free[grp]));
+                        if (!kTwoTiles && other > 0) mbar_arrive(smem_addr(&sh->o_free[grp ^ 1]));
+                    }
+                }
+                if (piece >= 0) {        // [piece][row tile][column][row]: coalesced over the warp's rows
+                    float *dst = p.part_out +
+                                 ((static_cast<int64_t>(piece) * C::kGroupsQ + (kTwoTiles ? grp : 0)) * D + col0 + c) * kM + row;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) dst[e * kM] = o[e];
+                } else if (live) {
+                    if (p.out_type == 0) {
+                        float *dst = static_cast<float *>(p.out) + orow * D + col0 + c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else {
+                        uint16_t *dst = static_cast<uint16_t *>(p.out) + orow * D + col0 + c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                w[x] = p.out_type == 1 ? pack_bf16x2(o[e + 2 * x], o[e + 2 * x + 1])
+                                                       : pack_f16x2(o[e + 2 * x], o[e + 2 * x + 1]);
+                            *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+            }
+            if (piece >= 0 && (kTwoTiles || grp == 0)) {
+                const int64_t at = (static_cast<int64_t>(piece) * C::kGroupsQ + (kTwoTiles ? grp : 0)) * kM + row;
+                p.part_max[at] = m;
+                p.part_sum[at] = l;
+            }
+            if (cnt > 0) ++o_cnt;
+            if (other > 0) ++o_other;
+        }
+    }
+
+    // ---- drain: copies still landing (after a timeout), then the tensor memory ----
+    grid_dependents_launch();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&sh->abort_flag)) {
+        // bounded: a slot whose second half was never started does not complete
+        const int nk = min(sh->k_issued[0], sh->k_issued[1]);
+        for (int s = 0; s < kKSlots && s < nk; ++s) mbar_wait_for(smem_addr(&sh->k_full[s]), ((nk - 1 - s) / kKSlots) & 1, 100000000ull);
+        for (int s = 0; s < kVSlots && s < sh->v_issued; ++s)
+            mbar_wait_for(smem_addr(&sh->v_full[s]), ((sh->v_issued - 1 - s) / kVSlots) & 1, 100000000ull);
+        if (sh->q_issued) mbar_wait_for(smem_addr(&sh->q_full), (sh->q_issued - 1) & 1, 100000000ull);
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512u);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The cut wave's pieces joined: one CTA per (unit, row tile, 16 columns), a
+// thread per row; piece weights 2^(m_i - M).
+// ---------------------------------------------------------------------------
+constexpr int kMergeCols = 16;
+
+__global__ void __launch_bounds__(kM)
+prefill_tc_merge_kernel(const __grid_constant__ PrefillParams p, int row_tiles) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int r = blockIdx.x, rt = blockIdx.y, c0 = blockIdx.z * kMergeCols, row = threadIdx.x;
+    const int *info = p.tail_info;
+    const int tail = info[0];
+    if (r >= tail) return;
+    const int64_t ctas = info[1], tiles = info[kTailPrefix + tail];
+    const int64_t p0 = info[kTailPrefix + r], p1 = info[kTailPrefix + r + 1];
+    // CTA c took tiles [c tiles / ctas, (c + 1) tiles / ctas): tile x belongs to ((x + 1) ctas - 1) / tiles
+    const int first = static_cast<int>(((p0 + 1) * ctas - 1) / tiles), last = static_cast<int>((p1 * ctas - 1) / tiles);
+    if (first == last) return;   // taken whole: written by its CTA
+    const int *d = info + kTailUnits + r * 8;
+    const int row_tokens = p.tile_tokens / row_tiles;
+    const int t = row / p.heads_per_tile, h = row - t * p.heads_per_tile, tok = rt * row_tokens + t;
+    if (t >= row_tokens || tok >= d[1] || h >= d[4]) return;
+    float M = -1e30f, l = 0.f, o[kMergeCols];
+#pragma unroll
+    for (int e = 0; e < kMergeCols; ++e) o[e] = 0.f;
+    for (int c = first; c <= last; ++c) M = fmaxf(M, p.part_max[(static_cast<int64_t>(c + r) * row_tiles + rt) * kM + row]);
+    for (int c = first; c <= last; ++c) {
+        const int64_t piece = static_cast<int64_t>(c + r) * row_tiles + rt;
+        const float w = fast_exp2(p.part_max[piece * kM + row] - M);
+        l = fmaf(w, p.part_sum[piece * kM + row], l);
+        const float *src = p.part_out + (piece * p.head_dim + c0) * kM + row;
+#pragma unroll
+        for (int e = 0; e < kMergeCols; ++e) o[e] = fmaf(w, src[e * kM], o[e]);
+    }
+    const float inv = l > 0.f ? 1.f / l : l;
+    const int64_t at = (static_cast<int64_t>(d[0] + tok) * p.num_heads + d[2] * p.group + d[3] + h) * p.head_dim + c0;
+#pragma unroll
+    for (int e = 0; e < kMergeCols; e += 2) store_pair_as(p.out, p.out_type, at + e, o[e] * inv, o[e + 1] * inv);
+}
+
+template <int D, bool kTwoTiles, bool kF16>
+cudaError_t launch_impl(const PrefillParams &p, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq,
+                        int ctas, cudaStream_t stream) {
+    auto kern = prefill_tc_kernel<D, kTwoTiles, kF16>;
+    constexpr size_t smem = smem_bytes<D, kTwoTiles>();
+    static unsigned long long done = 0;
+    cudaError_t e = ensure_smem_limit(kern, smem, done);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_kernel(kern, dim3(ctas), dim3(kThreads), smem, stream, 1u, tk, tv, tq, p)) != cudaSuccess) return e;
+    if (p.nsplit <= 1) return cudaSuccess;
+    const int row_tiles = kTwoTiles ? 2 : 1;
+    return launch_kernel(prefill_tc_merge_kernel, dim3(p.max_tail, row_tiles, D / kMergeCols), dim3(kM), 0, stream, 1u, p,
+                         row_tiles);
+}
+
+template <int D, bool kTwoTiles>
+cudaError_t launch_type(const PrefillParams &p, bool f16, const CUtensorMap &tk, const CUtensorMap &tv,
+                        const CUtensorMap &tq, int ctas, cudaStream_t stream) {
+    return f16 ? launch_impl<D, kTwoTiles, true>(p, tk, tv, tq, ctas, stream)
+               : launch_impl<D, kTwoTiles, false>(p, tk, tv, tq, ctas, stream);
+}
+
+}  // namespace
+
+bool prefill_tc_supported(int head_dim, int block_size, bool contiguous) {
+    return (head_dim == 64 || head_dim == 128) &&
+           (contiguous || (block_size >= 8 && block_size <= 256 && (block_size & (block_size - 1)) == 0));
+}
+int prefill_tc_rows() { return kM; }
+int prefill_tc_tile() { return kTile; }
+int prefill_tc_max_ctas() { return kMaxTail; }
+int prefill_tc_box_tokens(int block_size, bool contiguous) { return contiguous || block_size > 64 ? 64 : block_size; }
+size_t prefill_tc_info_bytes() { return kTailInts * sizeof(int); }
+
+cudaError_t launch_prefill_tc(const PrefillParams &p, bool two_tiles, bool f16, const CUtensorMap &tk,
+                              const CUtensorMap &tv, const CUtensorMap &tq, int ctas, cudaStream_t stream) {
+    if (p.head_dim == 128)
+        return two_tiles ? launch_type<128, true>(p, f16, tk, tv, tq, ctas, stream)
+                         : launch_type<128, false>(p, f16, tk, tv, tq, ctas, stream);
+    return two_tiles ? launch_type<64, true>(p, f16, tk, tv, tq, ctas, stream)
+                     : launch_type<64, false>(p, f16, tk, tv, tq, ctas, stream);
+}
+
+}  // namespace pa
