@@ -128,6 +128,16 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
     return p;
 }
 
+// One lane of a converged warp, always the same: the one that issues MMAs, TMA
+// copies and commits. What the instructions take is computed from values known
+// to be uniform: an MMA then issues every 64 cycles (M = N = 128, K = 16), the
+// tensor pipe's own rate, where descriptors in per-thread registers took up to 146.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit A packed two to a column.
 __device__ __forceinline__ void tc_mma_16bit_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                 uint32_t accumulate) {
@@ -138,6 +148,8 @@ __device__ __forceinline__ void tc_mma_16bit_ts(uint32_t d_tmem, uint32_t a_tmem
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// A value all lanes hold alike, made known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Warp-wide: 128 consecutive fp32 columns of this warp's 32 lanes, one wait (in
 // the same block, so that no use is scheduled before it).
@@ -407,7 +419,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     unsigned char *q_s = smem, *k_s = smem + C::kKOff, *v_s = smem + C::kVOff;
     Shared *sh = reinterpret_cast<Shared *>(smem + C::kBarOff);
     SharedJoin *join = reinterpret_cast<SharedJoin *>(sh + 1);   // one row tile only
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (warp == kVWarp && lane == 0) {
         tma_prefetch_desc(&tmap_q);
@@ -444,12 +456,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh->tmem;
+    const uint32_t tmem = uniform(sh->tmem);
     grid_dependency_wait();
     // tensor-memory columns: S (and P) of group g at 128 g, O at 256 + 128 g
     auto s_col = [&](int g) { return tmem + g * 128; };
     auto o_col = [&](int g) { return tmem + 256 + g * 128; };
-    const int R = box_tokens(p);
+    const int R = box_tokens(p), r_shift = 31 - __clz(R);                    // powers of two, like the block size
+    const int bs_shift = 31 - __clz(p.block_size);
 
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
@@ -476,20 +489,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     d[4] = g->nh;
                 }
                 if (k > 0 && !wait_bar(p, sh, &sh->q_empty, (k - 1) & 1)) break;
-                if (lane == 0) {
-                    const uint32_t qf = smem_addr(&sh->q_full);
+                const int b = uniform(g->b), ctx = uniform(g->ctx), kvh = uniform(g->kvh), n = uniform(g->n),
+                          first = uniform(g->t0), h0 = uniform(g->h0), q0 = uniform(g->q0);
+                const uint32_t qf = smem_addr(&sh->q_full);
+                if (elect_one()) {
                     mbar_arrive_expect_tx(qf, static_cast<uint32_t>(C::kGroupsQ * C::kHalves * q_tokens *
                                                                     p.heads_per_tile * 128));
                     // (dim, half, head in group, KV head, token): rows token * heads_per_tile + head
+#pragma unroll
                     for (int t = 0; t < C::kGroupsQ; ++t)
+#pragma unroll
                         for (int h = 0; h < C::kHalves; ++h)
-                            tma_load_5d(smem_addr(q_s + t * C::kQBytes + h * (kM * 128)), &tmap_q, 0, h, g->h0, g->kvh,
-                                        g->q0 + t * q_tokens, qf, q_policy);
+                            tma_load_5d(smem_addr(q_s + t * C::kQBytes + h * (kM * 128)), &tmap_q, 0, h, h0, kvh,
+                                        q0 + t * q_tokens, qf, q_policy);
                     sh->q_issued = k + 1;
                 }
+                __syncwarp();
                 BlockIds ids{-1, 0};
-                const int b = g->b, ctx = g->ctx, kvh = g->kvh, n = g->n, first = g->t0;
-                const int nblk = (ctx + p.block_size - 1) / p.block_size;
+                const int nblk = (ctx + p.block_size - 1) >> bs_shift;
                 bool ok = true;
                 for (int i = 0; i < n && ok; ++i, ++tiles) {
                     const int slot = tiles % kVSlots, t0 = (first + i) * kTile;
@@ -497,21 +514,23 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         ok = false;
                         break;
                     }
-                    const int boxes = (min(ctx - t0, kTile) + R - 1) / R;
+                    const int boxes = (min(ctx - t0, kTile) + R - 1) >> r_shift;
                     const uint32_t full = smem_addr(&sh->v_full[slot]);
                     const uint32_t dst = smem_addr(v_s + slot * C::kSlotBytes);
-                    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    __syncwarp();
                     for (int j = 0; j < boxes; ++j) {
                         const int tok = t0 + j * R;
                         int at = tok, blk = 0;
                         if (p.contig_stride > 0) {
                             at += b * p.contig_stride;
                         } else {
-                            blk = block_id(p, ids, b, tok / p.block_size, nblk, lane);
-                            at = tok % p.block_size;
+                            blk = block_id(p, ids, b, tok >> bs_shift, nblk, lane);
+                            at = tok & (p.block_size - 1);
                         }
-                        if (lane == 0)
+                        if (elect_one())
                             tma_load_5d(dst + j * (C::kHalves * R * 128), &tmap_v, 0, at, 0, kvh, blk, full, policy);
+                        __syncwarp();
                     }
                     if (lane == 0) sh->v_issued = tiles + 1;
                 }
@@ -526,10 +545,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             for (int k = 0; ok; ++k) {
                 const Seg *g = &sh->seg[k % kSegs];
                 if (!wait_bar(p, sh, &sh->seg_full[k % kSegs], (k / kSegs) & 1) || g->piece == -2) break;
-                const int b = g->b, ctx = g->ctx, kvh = g->kvh, n = g->n, first = g->t0;
-                __syncwarp();
+                const int b = uniform(g->b), ctx = uniform(g->ctx), kvh = uniform(g->kvh), n = uniform(g->n),
+                          first = uniform(g->t0);
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
-                const int nblk = (ctx + p.block_size - 1) / p.block_size;
+                const int nblk = (ctx + p.block_size - 1) >> bs_shift;
                 BlockIds ids{-1, 0};
                 for (int i = 0; i < n; ++i, ++tiles) {
                     const int slot = tiles % kKSlots, t0 = (first + i) * kTile + part * 64;
@@ -537,25 +556,27 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         ok = false;
                         break;
                     }
-                    const int boxes = max(0, (min(ctx - t0, 64) + R - 1) / R);
+                    const int boxes = max(0, min(ctx - t0, 64) + R - 1) >> r_shift;
                     const uint32_t full = smem_addr(&sh->k_full[slot]);
                     const uint32_t dst = smem_addr(k_s + slot * C::kSlotBytes) + part * 64 * 128;
-                    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    __syncwarp();
                     for (int j = 0; j < boxes; ++j) {
                         const int tok = t0 + j * R;
                         int at = tok, blk = 0;
                         if (p.contig_stride > 0) {
                             at += b * p.contig_stride;
                         } else {
-                            blk = block_id(p, ids, b, tok / p.block_size, nblk, lane);
-                            at = tok % p.block_size;
+                            blk = block_id(p, ids, b, tok >> bs_shift, nblk, lane);
+                            at = tok & (p.block_size - 1);
                         }
-                        if (lane == 0) {
+                        if (elect_one()) {
 #pragma unroll
                             for (int h = 0; h < C::kHalves; ++h)
                                 tma_load_5d(dst + h * (kTile * 128) + j * (R * 128), &tmap_k, 0, at, h, kvh, blk, full,
                                             policy);
                         }
+                        __syncwarp();
                     }
                     if (lane == 0) sh->k_issued[part] = tiles + 1;
                 }
@@ -566,22 +587,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             constexpr uint32_t id_pv = idesc_16bit_f32(kM, D, false, true, kF16);
             // V boxes are [R tokens][128 bytes] per half, boxes of kHalves halves one after another
             const uint32_t v_lbo = R * 128, v_sbo = R >= 16 ? 1024 : C::kHalves * 1024;
-            const int v_box = C::kHalves * R * 128, r_shift = 31 - __clz(R);
+            const int v_box = C::kHalves * R * 128;
             int kt = 0, vt = 0;                  // tiles whose K / V the products have taken
             int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const Seg *g = &sh->seg[k % kSegs];
                 if (!wait_bar(p, sh, &sh->seg_full[k % kSegs], (k / kSegs) & 1) || g->piece == -2) break;
-                const int n = g->n, ctx = g->ctx, first = g->t0;
-                const int cnt[2] = {g->cnt[0], g->cnt[1]};
-                __syncwarp();
+                const int n = uniform(g->n), ctx = uniform(g->ctx), first = uniform(g->t0);
+                const int cnt[2] = {uniform(g->cnt[0]), uniform(g->cnt[1])};
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
                 if (!wait_bar(p, sh, &sh->q_full, k & 1)) break;
                 auto wait_k = [&]() { return wait_bar(p, sh, &sh->k_full[kt % kKSlots], (kt / kKSlots) & 1); };
                 auto issue_s = [&](int grp) {
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint64_t qd = smem_desc_sw128(smem_addr(q_s + (kTwoTiles ? grp : 0) * C::kQBytes), 16, 1024);
                         const uint64_t kd = smem_desc_sw128(smem_addr(k_s + (kt % kKSlots) * C::kSlotBytes), 16, 1024);
 #pragma unroll
@@ -595,7 +615,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     __syncwarp();
                 };
                 auto release_k = [&]() {
-                    if (lane == 0) tc_commit(smem_addr(&sh->k_empty[kt % kKSlots]));
+                    if (elect_one()) tc_commit(smem_addr(&sh->k_empty[kt % kKSlots]));
                     ++kt;
                 };
                 // V of tile i has landed; rows past the context are zeroed
@@ -619,7 +639,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     if (j == 0 && o_cnt[grp] > 0 && !wait_bar(p, sh, &sh->o_free[grp], (o_cnt[grp] - 1) & 1)) return false;
                     ++s_cnt[grp];
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint64_t vd = smem_desc_sw128(smem_addr(v_s + (vt % kVSlots) * C::kSlotBytes), v_lbo, v_sbo);
 #pragma unroll
                         for (int kk = 0; kk < kTile / 16; ++kk) {
@@ -633,16 +653,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     return true;
                 };
                 auto group_done = [&](int grp) {
-                    if (lane == 0) tc_commit(smem_addr(&sh->o_full[grp]));
+                    if (elect_one()) tc_commit(smem_addr(&sh->o_full[grp]));
                     ++o_cnt[grp];
                 };
                 auto q_done = [&]() {
-                    if (lane == 0) tc_commit(smem_addr(&sh->q_empty));
+                    if (elect_one()) tc_commit(smem_addr(&sh->q_empty));
                 };
                 if (n == 0) q_done();
                 if constexpr (kTwoTiles) {
                     if (n > 0) {
                         if (!wait_k()) break;
+#pragma unroll
                         for (int grp = 0; grp < 2; ++grp)
                             if (cnt[grp] > 0) issue_s(grp);
                         release_k();
@@ -651,12 +672,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     for (int i = 0; i < n && ok; ++i) {
                         if (!wait_v(i)) { ok = false; break; }
                         bool have_k = false;
+#pragma unroll
                         for (int grp = 0; grp < 2; ++grp) {
                             if (i < cnt[grp]) {
                                 if (!issue_pv(grp, i)) { ok = false; break; }
                                 if (i == cnt[grp] - 1) group_done(grp);
                             }
-                            if (grp == 1 && lane == 0) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
+                            if (grp == 1) if (elect_one()) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
                             if (i + 1 < cnt[grp]) {
                                 if (!have_k && !wait_k()) { ok = false; break; }
                                 have_k = true;
@@ -680,7 +702,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     for (int i = 0; i < n && ok; ++i) {
                         const int grp = i & 1;
                         if (!wait_v(i) || !issue_pv(grp, i >> 1)) { ok = false; break; }
-                        if (lane == 0) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
+                        if (elect_one()) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
                         ++vt;
                         if ((i >> 1) == cnt[grp] - 1) group_done(grp);
                         if (i + 2 < n) {
