@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kM = 128;              // rows of a row tile: tensor-memory lanes
 constexpr int kTile = 128;           // context tokens per K/V tile
-constexpr int kKSlots = 3, kVSlots = 2;
+constexpr int kSlots = 5;            // ring of K and V tiles, in the order the products take them
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 11;
 constexpr int kSegs = 2;             // published segments in flight
@@ -67,9 +67,12 @@ struct Cfg {
     static constexpr int kGroupsQ = kTwoTiles ? 2 : 1;      // row tiles of a unit
     static constexpr int kQBytes = kHalves * kM * 128;      // one row tile
     static constexpr int kSlotBytes = kHalves * kTile * 128;
-    static constexpr int kKOff = kGroupsQ * kQBytes;
-    static constexpr int kVOff = kKOff + kKSlots * kSlotBytes;
-    static constexpr int kBarOff = kVOff + kVSlots * kSlotBytes;
+    static constexpr int kRingOff = kGroupsQ * kQBytes;
+    static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+    // Place in the ring's order of tile i of a segment's n. Two row tiles: K0 V0 K1 V1 ...;
+    // one, whose first two score tiles come before any weights: K0 K1 V0 K2 V1 ... V(n-1).
+    __device__ static int k_fill(int i) { return kTwoTiles ? 2 * i : i == 0 ? 0 : 2 * i - 1; }
+    __device__ static int v_fill(int i, int n) { return kTwoTiles || i == n - 1 ? 2 * i + 1 : 2 * i + 2; }
 };
 
 // One piece of a unit: K/V tiles [t0, t0 + n) of rows of one KV head.
@@ -84,15 +87,16 @@ struct Seg {
 };
 
 struct Shared {
-    uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+    uint64_t full[kSlots], empty[kSlots];  // K: one arrival of each K warp; V: two of its warp
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
+    uint64_t v_fixed;                      // a V tile's rows past the context are zeroed
     uint64_t join_full[2];                 // one row tile: a group's maxima and sums are posted
     uint64_t done;
     uint32_t tmem;
     int abort_flag;
-    int k_issued[2], v_issued, q_issued;   // tiles whose copies have been started
+    int last_fill[kSlots], q_issued;       // what has been started, for the drain after a timeout
     Seg seg[kSegs];
     int tail_prefix[kMaxTail + 1];         // tiles of the cut wave's units, summed
     int tail_work[kMaxTail];
@@ -120,6 +124,16 @@ __device__ __forceinline__ bool wait_bar(const PrefillParams &p, Shared *sh, uin
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+
+// The same for a single thread (the MMA issuer inside a segment).
+__device__ __forceinline__ bool wait_bar_one(const PrefillParams &p, Shared *sh, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(smem_addr(bar), parity)) return true;
+    if (*reinterpret_cast<volatile int *>(&sh->abort_flag)) return false;
+    if (mbar_wait(smem_addr(bar), parity)) return true;
+    record_status(p.status, kStatusTimeout);
+    *reinterpret_cast<volatile int *>(&sh->abort_flag) = 1;
+    return false;
 }
 
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
@@ -207,6 +221,49 @@ template <bool kF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
     if constexpr (kF16) return pack_f16x2(a, b);
     else return pack_bf16x2(a, b);
+}
+
+// Two fp32 values in one register pair, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The largest (kMax) or smallest of a row's scores, three operands at a time.
+template <bool kMax>
+__device__ __forceinline__ float best3(float a, float b, float c) {
+    float r;
+    if constexpr (kMax) asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    else asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+template <bool kMax>
+__device__ __forceinline__ float row_max(const float (&s)[kTile]) {
+    float a[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) a[c] = s[c];
+#pragma unroll
+    for (int c = 4; c + 8 <= kTile; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = best3<kMax>(a[e], s[c + 2 * e], s[c + 2 * e + 1]);
+    // (kTile - 4) % 8 == 4 scores are left
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = best3<kMax>(a[e], s[kTile - 4 + e], a[e]);
+    return best3<kMax>(best3<kMax>(a[0], a[1], a[2]), a[3], a[3]);
 }
 
 // Tiles a unit (row tiles from token tok0 of the sequence) has to visit.
@@ -416,7 +473,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *q_s = smem, *k_s = smem + C::kKOff, *v_s = smem + C::kVOff;
+    unsigned char *q_s = smem, *ring = smem + C::kRingOff;
     Shared *sh = reinterpret_cast<Shared *>(smem + C::kBarOff);
     SharedJoin *join = reinterpret_cast<SharedJoin *>(sh + 1);   // one row tile only
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -425,19 +482,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         tma_prefetch_desc(&tmap_q);
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
-        for (int i = 0; i < kKSlots; ++i) {
-            mbar_init(smem_addr(&sh->k_full[i]), 2);
-            mbar_init(smem_addr(&sh->k_empty[i]), 1);
-        }
-        for (int i = 0; i < kVSlots; ++i) {
-            mbar_init(smem_addr(&sh->v_full[i]), 1);
-            mbar_init(smem_addr(&sh->v_empty[i]), 1);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_addr(&sh->full[i]), 2);
+            mbar_init(smem_addr(&sh->empty[i]), 1);
+            sh->last_fill[i] = -1;
         }
         mbar_init(smem_addr(&sh->q_full), 1);
         mbar_init(smem_addr(&sh->q_empty), 1);
         for (int g = 0; g < 2; ++g) {
             mbar_init(smem_addr(&sh->s_full[g]), 1);
-            mbar_init(smem_addr(&sh->p_full[g]), 4);
+            mbar_init(smem_addr(&sh->p_full[g][0]), 4);
+            mbar_init(smem_addr(&sh->p_full[g][1]), 4);
             mbar_init(smem_addr(&sh->o_full[g]), 1);
             mbar_init(smem_addr(&sh->o_free[g]), kTwoTiles ? 4 : 8);
             mbar_init(smem_addr(&sh->join_full[g]), 4);
@@ -447,8 +502,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             mbar_init(smem_addr(&sh->seg_empty[i]), kSegReaders);
         }
         mbar_init(smem_addr(&sh->done), 1);
+        mbar_init(smem_addr(&sh->v_fixed), 1);
         sh->abort_flag = 0;
-        sh->k_issued[0] = sh->k_issued[1] = sh->v_issued = sh->q_issued = 0;
+        sh->q_issued = 0;
         mbar_fence_init();
     } else if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(&sh->tmem), 512u);
@@ -465,14 +521,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const int bs_shift = 31 - __clz(p.block_size);
 
     if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kVWarp) {
             // ---------------- the schedule, Q and V ----------------
             Scheduler sc;
             sched_init(p, sh, sc, lane);
             const uint64_t policy = l2_policy_evict_normal(), q_policy = l2_policy_evict_first();
             const int q_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
-            int tiles = 0;
+            int fills = 0;                       // of the segments before
             for (int k = 0;; ++k) {
                 Seg *g = &sh->seg[k % kSegs];
                 if (k >= kSegs && !wait_bar(p, sh, &sh->seg_empty[k % kSegs], ((k / kSegs) - 1) & 1)) break;
@@ -508,16 +564,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 BlockIds ids{-1, 0};
                 const int nblk = (ctx + p.block_size - 1) >> bs_shift;
                 bool ok = true;
-                for (int i = 0; i < n && ok; ++i, ++tiles) {
-                    const int slot = tiles % kVSlots, t0 = (first + i) * kTile;
-                    if (tiles >= kVSlots && !wait_bar(p, sh, &sh->v_empty[slot], ((tiles / kVSlots) - 1) & 1)) {
+                for (int i = 0; i < n; ++i) {
+                    const int f = fills + C::v_fill(i, n), slot = f % kSlots, t0 = (first + i) * kTile;
+                    if (f >= kSlots && !wait_bar(p, sh, &sh->empty[slot], ((f / kSlots) - 1) & 1)) {
                         ok = false;
                         break;
                     }
                     const int boxes = (min(ctx - t0, kTile) + R - 1) >> r_shift;
-                    const uint32_t full = smem_addr(&sh->v_full[slot]);
-                    const uint32_t dst = smem_addr(v_s + slot * C::kSlotBytes);
-                    if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    const uint32_t full = smem_addr(&sh->full[slot]);
+                    const uint32_t dst = smem_addr(ring + slot * C::kSlotBytes);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                        mbar_arrive(full);
+                        sh->last_fill[slot] = f;
+                    }
                     __syncwarp();
                     for (int j = 0; j < boxes; ++j) {
                         const int tok = t0 + j * R;
@@ -532,15 +592,31 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                             tma_load_5d(dst + j * (C::kHalves * R * 128), &tmap_v, 0, at, 0, kvh, blk, full, policy);
                         __syncwarp();
                     }
-                    if (lane == 0) sh->v_issued = tiles + 1;
+                    const int valid = ctx - t0;
+                    if (valid < kTile) {   // the context ends inside the tile: zero its other rows once it has landed
+                        if (!wait_bar(p, sh, &sh->full[slot], (f / kSlots) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        unsigned char *v = ring + slot * C::kSlotBytes;
+                        for (int x = lane; x < (kTile - valid) * C::kHalves * 8; x += 32) {
+                            const int row = valid + x / (C::kHalves * 8), c = x % (C::kHalves * 8);
+                            *reinterpret_cast<uint4 *>(v + (row >> r_shift) * (C::kHalves * R * 128) + (c / 8) * (R * 128) +
+                                                       (row & (R - 1)) * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&sh->v_fixed));
+                    }
                 }
                 if (!ok) break;
+                fills += 2 * n;
             }
         } else if (warp != kMmaWarp) {
             // ---------------- K, 64 tokens of every tile ----------------
             const int part = warp - kKWarp;
             const uint64_t policy = l2_policy_evict_normal();
-            int tiles = 0;
+            int fills = 0;
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const Seg *g = &sh->seg[k % kSegs];
@@ -550,16 +626,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
                 const int nblk = (ctx + p.block_size - 1) >> bs_shift;
                 BlockIds ids{-1, 0};
-                for (int i = 0; i < n; ++i, ++tiles) {
-                    const int slot = tiles % kKSlots, t0 = (first + i) * kTile + part * 64;
-                    if (tiles >= kKSlots && !wait_bar(p, sh, &sh->k_empty[slot], ((tiles / kKSlots) - 1) & 1)) {
+                for (int i = 0; i < n; ++i) {
+                    const int f = fills + C::k_fill(i), slot = f % kSlots, t0 = (first + i) * kTile + part * 64;
+                    if (f >= kSlots && !wait_bar(p, sh, &sh->empty[slot], ((f / kSlots) - 1) & 1)) {
                         ok = false;
                         break;
                     }
                     const int boxes = max(0, min(ctx - t0, 64) + R - 1) >> r_shift;
-                    const uint32_t full = smem_addr(&sh->k_full[slot]);
-                    const uint32_t dst = smem_addr(k_s + slot * C::kSlotBytes) + part * 64 * 128;
-                    if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                    const uint32_t full = smem_addr(&sh->full[slot]);
+                    const uint32_t dst = smem_addr(ring + slot * C::kSlotBytes) + part * 64 * 128;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                        sh->last_fill[slot] = f;
+                    }
                     __syncwarp();
                     for (int j = 0; j < boxes; ++j) {
                         const int tok = t0 + j * R;
@@ -578,8 +657,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         }
                         __syncwarp();
                     }
-                    if (lane == 0) sh->k_issued[part] = tiles + 1;
                 }
+                fills += 2 * n;
             }
         } else {
             // ---------------- MMA issue ----------------
@@ -588,8 +667,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             // V boxes are [R tokens][128 bytes] per half, boxes of kHalves halves one after another
             const uint32_t v_lbo = R * 128, v_sbo = R >= 16 ? 1024 : C::kHalves * 1024;
             const int v_box = C::kHalves * R * 128;
-            int kt = 0, vt = 0;                  // tiles whose K / V the products have taken
-            int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+            int fills = 0, fixed = 0;            // of the segments before: ring tiles, zeroed V tiles
+            int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};   // a group's tiles; its segments with any
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const Seg *g = &sh->seg[k % kSegs];
@@ -598,124 +677,111 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 const int cnt[2] = {uniform(g->cnt[0]), uniform(g->cnt[1])};
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
                 if (!wait_bar(p, sh, &sh->q_full, k & 1)) break;
-                auto wait_k = [&]() { return wait_bar(p, sh, &sh->k_full[kt % kKSlots], (kt / kKSlots) & 1); };
-                auto issue_s = [&](int grp) {
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t qd = smem_desc_sw128(smem_addr(q_s + (kTwoTiles ? grp : 0) * C::kQBytes), 16, 1024);
-                        const uint64_t kd = smem_desc_sw128(smem_addr(k_s + (kt % kKSlots) * C::kSlotBytes), 16, 1024);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const int half = kk / 4, off = (kk % 4) * 32;
-                            tc_mma_16bit(s_col(grp), qd + desc_step(half * (kM * 128) + off),
-                                         kd + desc_step(half * (kTile * 128) + off), id_qk, kk > 0 ? 1u : 0u);
-                        }
-                        tc_commit(smem_addr(&sh->s_full[grp]));
-                    }
-                    __syncwarp();
-                };
-                auto release_k = [&]() {
-                    if (elect_one()) tc_commit(smem_addr(&sh->k_empty[kt % kKSlots]));
-                    ++kt;
-                };
-                // V of tile i has landed; rows past the context are zeroed
+                const bool cut = ctx < (first + n) * kTile;   // the context ends inside the last tile
+                auto wait_fill = [&](int f) { return wait_bar_one(p, sh, &sh->full[f % kSlots], (f / kSlots) & 1); };
+                auto wait_k = [&](int i) { return wait_fill(fills + C::k_fill(i)); };
                 auto wait_v = [&](int i) {
-                    if (!wait_bar(p, sh, &sh->v_full[vt % kVSlots], (vt / kVSlots) & 1)) return false;
-                    const int valid = ctx - (first + i) * kTile;
-                    if (valid < kTile) {
-                        unsigned char *v = v_s + (vt % kVSlots) * C::kSlotBytes;
-                        for (int x = lane; x < (kTile - valid) * C::kHalves * 8; x += 32) {
-                            const int row = valid + x / (C::kHalves * 8), c = x % (C::kHalves * 8);
-                            *reinterpret_cast<uint4 *>(v + (row / R) * v_box + (c / 8) * (R * 128) + (row % R) * 128 +
-                                                       (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    return true;
+                    return wait_fill(fills + C::v_fill(i, n)) &&
+                           (!cut || i != n - 1 || wait_bar_one(p, sh, &sh->v_fixed, fixed & 1));
                 };
-                auto issue_pv = [&](int grp, int j) {   // j: the group's tile
-                    if (!wait_bar(p, sh, &sh->p_full[grp], s_cnt[grp] & 1)) return false;
-                    if (j == 0 && o_cnt[grp] > 0 && !wait_bar(p, sh, &sh->o_free[grp], (o_cnt[grp] - 1) & 1)) return false;
-                    ++s_cnt[grp];
+                // the slot is free once every product issued so far has run
+                auto release = [&](int f) { tc_commit(smem_addr(&sh->empty[(fills + f) % kSlots])); };
+                auto issue_s = [&](int grp, int i) {
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t vd = smem_desc_sw128(smem_addr(v_s + (vt % kVSlots) * C::kSlotBytes), v_lbo, v_sbo);
+                    const uint64_t qd = smem_desc_sw128(smem_addr(q_s + (kTwoTiles ? grp : 0) * C::kQBytes), 16, 1024);
+                    const uint64_t kd =
+                        smem_desc_sw128(smem_addr(ring + (fills + C::k_fill(i)) % kSlots * C::kSlotBytes), 16, 1024);
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk) {
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int half = kk / 4, off = (kk % 4) * 32;
+                        tc_mma_16bit(s_col(grp), qd + desc_step(half * (kM * 128) + off),
+                                     kd + desc_step(half * (kTile * 128) + off), id_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(smem_addr(&sh->s_full[grp]));
+                };
+                // O += P V of the group's tile j, in two halves of 64 tokens as their weights appear
+                auto issue_pv = [&](int grp, int j, int i) {
+                    if (j == 0 && o_cnt[grp] > 0 && !wait_bar_one(p, sh, &sh->o_free[grp], (o_cnt[grp] - 1) & 1)) return false;
+                    const uint64_t vd =
+                        smem_desc_sw128(smem_addr(ring + (fills + C::v_fill(i, n)) % kSlots * C::kSlotBytes), v_lbo, v_sbo);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!wait_bar_one(p, sh, &sh->p_full[grp][h], (s_cnt[grp] + j) & 1)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = h * 4; kk < h * 4 + 4; ++kk) {
                             // (R is a power of two)
                             const int off = R >= 16 ? ((kk * 16) >> r_shift) * v_box + ((kk * 16) & (R - 1)) * 128 : kk * 2 * v_box;
                             tc_mma_16bit_ts(o_col(grp), s_col(grp) + kk * 8, vd + desc_step(off), id_pv,
                                             (j > 0 || kk > 0) ? 1u : 0u);
                         }
                     }
-                    __syncwarp();
+                    if (j == cnt[grp] - 1) tc_commit(smem_addr(&sh->o_full[grp]));
                     return true;
                 };
-                auto group_done = [&](int grp) {
-                    if (elect_one()) tc_commit(smem_addr(&sh->o_full[grp]));
-                    ++o_cnt[grp];
-                };
-                auto q_done = [&]() {
-                    if (elect_one()) tc_commit(smem_addr(&sh->q_empty));
-                };
-                if (n == 0) q_done();
-                if constexpr (kTwoTiles) {
-                    if (n > 0) {
-                        if (!wait_k()) break;
-#pragma unroll
-                        for (int grp = 0; grp < 2; ++grp)
-                            if (cnt[grp] > 0) issue_s(grp);
-                        release_k();
-                        if (n == 1) q_done();
+                // the products of one segment, issued by one thread: K and V are waited for ahead of the
+                // weights, so that nothing stands between a group's P V and its next S
+                auto segment = [&]() {
+                    if (n == 0) {
+                        tc_commit(smem_addr(&sh->q_empty));
+                        return true;
                     }
-                    for (int i = 0; i < n && ok; ++i) {
-                        if (!wait_v(i)) { ok = false; break; }
-                        bool have_k = false;
-#pragma unroll
-                        for (int grp = 0; grp < 2; ++grp) {
-                            if (i < cnt[grp]) {
-                                if (!issue_pv(grp, i)) { ok = false; break; }
-                                if (i == cnt[grp] - 1) group_done(grp);
-                            }
-                            if (grp == 1) if (elect_one()) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
-                            if (i + 1 < cnt[grp]) {
-                                if (!have_k && !wait_k()) { ok = false; break; }
-                                have_k = true;
-                                issue_s(grp);
+                    if constexpr (kTwoTiles) {
+                        if (!wait_k(0)) return false;
+                        if (cnt[0] > 0) issue_s(0, 0);
+                        if (cnt[1] > 0) issue_s(1, 0);
+                        release(C::k_fill(0));
+                        if (n == 1) tc_commit(smem_addr(&sh->q_empty));
+                        for (int i = 0; i < n; ++i) {
+                            if (!wait_v(i) || (i + 1 < n && !wait_k(i + 1))) return false;
+                            if (i < cnt[0] && !issue_pv(0, i, i)) return false;
+                            if (i + 1 < cnt[0]) issue_s(0, i + 1);
+                            if (i < cnt[1] && !issue_pv(1, i, i)) return false;
+                            release(C::v_fill(i, n));
+                            if (i + 1 < n) {
+                                if (i + 1 < cnt[1]) issue_s(1, i + 1);
+                                release(C::k_fill(i + 1));
+                                if (i + 2 == n) tc_commit(smem_addr(&sh->q_empty));
                             }
                         }
-                        ++vt;
-                        if (ok && i + 1 < n) {
-                            if (!have_k && !wait_k()) { ok = false; break; }
-                            release_k();
-                            if (i + 2 == n) q_done();
+                    } else {
+                        for (int i = 0; i < 2 && i < n; ++i) {
+                            if (!wait_k(i)) return false;
+                            issue_s(i, i);
+                            release(C::k_fill(i));
+                            if (i == n - 1) tc_commit(smem_addr(&sh->q_empty));
+                        }
+                        for (int i0 = 0; i0 < n; i0 += 2) {
+#pragma unroll
+                            for (int grp = 0; grp < 2; ++grp) {
+                                const int i = i0 + grp;
+                                if (i >= n) break;
+                                if (!wait_v(i) || (i + 2 < n && !wait_k(i + 2)) || !issue_pv(grp, i0 >> 1, i)) return false;
+                                release(C::v_fill(i, n));
+                                if (i + 2 < n) {
+                                    issue_s(grp, i + 2);
+                                    release(C::k_fill(i + 2));
+                                    if (i + 3 == n) tc_commit(smem_addr(&sh->q_empty));
+                                }
+                            }
                         }
                     }
-                } else {
-                    for (int i = 0; i < min(n, 2) && ok; ++i) {
-                        if (!wait_k()) { ok = false; break; }
-                        issue_s(i);
-                        release_k();
-                        if (i == n - 1) q_done();
-                    }
-                    for (int i = 0; i < n && ok; ++i) {
-                        const int grp = i & 1;
-                        if (!wait_v(i) || !issue_pv(grp, i >> 1)) { ok = false; break; }
-                        if (elect_one()) tc_commit(smem_addr(&sh->v_empty[vt % kVSlots]));
-                        ++vt;
-                        if ((i >> 1) == cnt[grp] - 1) group_done(grp);
-                        if (i + 2 < n) {
-                            if (!wait_k()) { ok = false; break; }
-                            issue_s(grp);
-                            release_k();
-                            if (i + 3 == n) q_done();
-                        }
-                    }
+                    return true;
+                };
+                bool done = true;
+                if (elect_one()) done = segment();
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, done);
+                fills += 2 * n;
+                fixed += cut && n > 0;
+#pragma unroll
+                for (int grp = 0; grp < 2; ++grp) {
+                    s_cnt[grp] += cnt[grp];
+                    o_cnt[grp] += cnt[grp] > 0;
                 }
             }
-            // every MMA this thread issued has completed once `done` arrives
-            if (lane == 0) {
+            // every MMA the issuing thread started has completed once `done` arrives
+            if (elect_one()) {
                 tc_commit(smem_addr(&sh->done));
                 if (!mbar_wait(smem_addr(&sh->done), 0)) record_status(p.status, kStatusTimeout);
             }
@@ -723,7 +789,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         }
     } else {
         // ---------------- softmax ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
@@ -761,42 +827,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     mul = 1.f;
                     up = true;
                 }
-                float mx;
-                {
-                    float a[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) a[c] = s[c];
-                    if (up) {
-#pragma unroll
-                        for (int c = 4; c < kTile; ++c) a[c & 3] = fmaxf(a[c & 3], s[c]);
-                        mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-                    } else {
-#pragma unroll
-                        for (int c = 4; c < kTile; ++c) a[c & 3] = fminf(a[c & 3], s[c]);
-                        mx = fminf(fminf(a[0], a[1]), fminf(a[2], a[3]));
-                    }
-                    mx *= mul;
-                }
+                float mx = (up ? row_max<true>(s) : row_max<false>(s)) * mul;
                 const bool need = mx > m + kSlack;
                 const float m_new = need ? mx : m;
                 const float alpha = fast_exp2(m - m_new);
                 m = m_new;
                 l *= alpha;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float p0 = fast_exp2(fmaf(s[c0 + 2 * c], mul, -m));
-                        const float p1 = fast_exp2(fmaf(s[c0 + 2 * c + 1], mul, -m));
-                        sum[c & 3] += p0 + p1;
-                        w[c] = pack16<kF16>(p0, p1);   // the weights' one rounding, to the caches' type
-                    }
-                    tmem_st16_nowait(s_col(grp) + lanes + c0 / 2, w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                // S of this tile was issued behind the group's previous P V: O is at rest here
+                // S of this tile was issued behind the group's previous P V: O is at rest until P appears
                 if (j > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
@@ -807,10 +844,31 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         tmem_st32(o_col(grp) + lanes + c, o);
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[grp]));
+                const uint64_t mul2 = pair(mul, mul), neg2 = pair(-m, -m);
+                uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+                for (int c0 = 0; c0 < kTile; c0 += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {   // 2^(s * scale - m), two at a time
+                        float e0, e1;
+                        unpair(fma2(pair(s[c0 + 2 * c], s[c0 + 2 * c + 1]), mul2, neg2), e0, e1);
+                        e0 = fast_exp2(e0);
+                        e1 = fast_exp2(e1);
+                        sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
+                        w[c] = pack16<kF16>(e0, e1);   // the weights' one rounding, to the caches' type
+                    }
+                    tmem_st16_nowait(s_col(grp) + lanes + c0 / 2, w);
+                    if (c0 & 32) {   // 64 tokens' weights are there: the products may start on them
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[grp][c0 / 64]));
+                    }
+                }
+                float a0, a1;
+                unpair(add2(sum[0], sum[1]), a0, a1);
+                l += a0 + a1;
             }
             if (!ok) break;
             // ---- epilogue ----
@@ -902,11 +960,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&sh->abort_flag)) {
-        // bounded: a slot whose second half was never started does not complete
-        const int nk = min(sh->k_issued[0], sh->k_issued[1]);
-        for (int s = 0; s < kKSlots && s < nk; ++s) mbar_wait_for(smem_addr(&sh->k_full[s]), ((nk - 1 - s) / kKSlots) & 1, 100000000ull);
-        for (int s = 0; s < kVSlots && s < sh->v_issued; ++s)
-            mbar_wait_for(smem_addr(&sh->v_full[s]), ((sh->v_issued - 1 - s) / kVSlots) & 1, 100000000ull);
+        // bounded: a slot of which one warp's half was never started does not complete
+        for (int i = 0; i < kSlots; ++i)
+            if (sh->last_fill[i] >= 0)
+                mbar_wait_for(smem_addr(&sh->full[i]), (sh->last_fill[i] / kSlots) & 1, 100000000ull);
         if (sh->q_issued) mbar_wait_for(smem_addr(&sh->q_full), (sh->q_issued - 1) & 1, 100000000ull);
     }
     __syncthreads();
