@@ -664,9 +664,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             // ---------------- MMA issue ----------------
             constexpr uint32_t id_qk = idesc_16bit_f32(kM, kTile, false, false, kF16);
             constexpr uint32_t id_pv = idesc_16bit_f32(kM, D, false, true, kF16);
-            // V boxes are [R tokens][128 bytes] per half, boxes of kHalves halves one after another
-            const uint32_t v_lbo = R * 128, v_sbo = R >= 16 ? 1024 : C::kHalves * 1024;
+            // V boxes are [R tokens][128 bytes] per half, boxes of kHalves halves one after another (R a power of two)
             const int v_box = C::kHalves * R * 128;
+            uint64_t v_off[kTile / 16];          // of the tile's 16-token steps
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+                v_off[kk] = desc_step(R >= 16 ? ((kk * 16) >> r_shift) * v_box + ((kk * 16) & (R - 1)) * 128 : kk * 2 * v_box);
+            const uint64_t q_desc = smem_desc_sw128(smem_addr(q_s), 16, 1024), k_desc = smem_desc_sw128(smem_addr(ring), 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), R * 128, R >= 16 ? 1024 : C::kHalves * 1024);
             int fills = 0, fixed = 0;            // of the segments before: ring tiles, zeroed V tiles
             int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};   // a group's tiles; its segments with any
             bool ok = true;
@@ -678,19 +683,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
                 if (!wait_bar(p, sh, &sh->q_full, k & 1)) break;
                 const bool cut = ctx < (first + n) * kTile;   // the context ends inside the last tile
-                auto wait_fill = [&](int f) { return wait_bar_one(p, sh, &sh->full[f % kSlots], (f / kSlots) & 1); };
-                auto wait_k = [&](int i) { return wait_fill(fills + C::k_fill(i)); };
-                auto wait_v = [&](int i) {
-                    return wait_fill(fills + C::v_fill(i, n)) &&
-                           (!cut || i != n - 1 || wait_bar_one(p, sh, &sh->v_fixed, fixed & 1));
+                // places in the ring: the next K and V tile's slot and phase, stepped along
+                struct Place {
+                    int slot, phase;
+                    __device__ __forceinline__ void step(int by) {
+                        slot += by;
+                        if (slot >= kSlots) {
+                            slot -= kSlots;
+                            phase ^= 1;
+                        }
+                    }
                 };
+                auto wait_at = [&](const Place &at) { return wait_bar_one(p, sh, &sh->full[at.slot], at.phase); };
                 // the slot is free once every product issued so far has run
-                auto release = [&](int f) { tc_commit(smem_addr(&sh->empty[(fills + f) % kSlots])); };
-                auto issue_s = [&](int grp, int i) {
+                auto release = [&](const Place &at) { tc_commit(smem_addr(&sh->empty[at.slot])); };
+                auto issue_s = [&](int grp, const Place &at) {
                     tc_fence_after();
-                    const uint64_t qd = smem_desc_sw128(smem_addr(q_s + (kTwoTiles ? grp : 0) * C::kQBytes), 16, 1024);
-                    const uint64_t kd =
-                        smem_desc_sw128(smem_addr(ring + (fills + C::k_fill(i)) % kSlots * C::kSlotBytes), 16, 1024);
+                    const uint64_t qd = q_desc + (kTwoTiles ? grp : 0) * desc_step(C::kQBytes);
+                    const uint64_t kd = k_desc + static_cast<uint32_t>(at.slot) * static_cast<uint32_t>(C::kSlotBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int half = kk / 4, off = (kk % 4) * 32;
@@ -700,21 +710,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     tc_commit(smem_addr(&sh->s_full[grp]));
                 };
                 // O += P V of the group's tile j, in two halves of 64 tokens as their weights appear
-                auto issue_pv = [&](int grp, int j, int i) {
+                auto issue_pv = [&](int grp, int j, const Place &at) {
+                    const uint64_t vd = v_desc + static_cast<uint32_t>(at.slot) * static_cast<uint32_t>(C::kSlotBytes >> 4);
                     if (j == 0 && o_cnt[grp] > 0 && !wait_bar_one(p, sh, &sh->o_free[grp], (o_cnt[grp] - 1) & 1)) return false;
-                    const uint64_t vd =
-                        smem_desc_sw128(smem_addr(ring + (fills + C::v_fill(i, n)) % kSlots * C::kSlotBytes), v_lbo, v_sbo);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (!wait_bar_one(p, sh, &sh->p_full[grp][h], (s_cnt[grp] + j) & 1)) return false;
                         tc_fence_after();
 #pragma unroll
-                        for (int kk = h * 4; kk < h * 4 + 4; ++kk) {
-                            // (R is a power of two)
-                            const int off = R >= 16 ? ((kk * 16) >> r_shift) * v_box + ((kk * 16) & (R - 1)) * 128 : kk * 2 * v_box;
-                            tc_mma_16bit_ts(o_col(grp), s_col(grp) + kk * 8, vd + desc_step(off), id_pv,
+                        for (int kk = h * 4; kk < h * 4 + 4; ++kk)
+                            tc_mma_16bit_ts(o_col(grp), s_col(grp) + kk * 8, vd + v_off[kk], id_pv,
                                             (j > 0 || kk > 0) ? 1u : 0u);
-                        }
                     }
                     if (j == cnt[grp] - 1) tc_commit(smem_addr(&sh->o_full[grp]));
                     return true;
@@ -726,43 +732,55 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         tc_commit(smem_addr(&sh->q_empty));
                         return true;
                     }
+                    Place kp{fills % kSlots, (fills / kSlots) & 1}, vp = kp;
+                    auto wait_fixed = [&](int i) { return !cut || i != n - 1 || wait_bar_one(p, sh, &sh->v_fixed, fixed & 1); };
                     if constexpr (kTwoTiles) {
-                        if (!wait_k(0)) return false;
-                        if (cnt[0] > 0) issue_s(0, 0);
-                        if (cnt[1] > 0) issue_s(1, 0);
-                        release(C::k_fill(0));
+                        if (!wait_at(kp)) return false;
+                        if (cnt[0] > 0) issue_s(0, kp);
+                        if (cnt[1] > 0) issue_s(1, kp);
+                        release(kp);
                         if (n == 1) tc_commit(smem_addr(&sh->q_empty));
+                        vp.step(1);
+                        kp.step(2);
                         for (int i = 0; i < n; ++i) {
-                            if (!wait_v(i) || (i + 1 < n && !wait_k(i + 1))) return false;
-                            if (i < cnt[0] && !issue_pv(0, i, i)) return false;
-                            if (i + 1 < cnt[0]) issue_s(0, i + 1);
-                            if (i < cnt[1] && !issue_pv(1, i, i)) return false;
-                            release(C::v_fill(i, n));
+                            if (!wait_at(vp) || !wait_fixed(i) || (i + 1 < n && !wait_at(kp))) return false;
+                            if (i < cnt[0] && !issue_pv(0, i, vp)) return false;
+                            if (i + 1 < cnt[0]) issue_s(0, kp);
+                            if (i < cnt[1] && !issue_pv(1, i, vp)) return false;
+                            release(vp);
                             if (i + 1 < n) {
-                                if (i + 1 < cnt[1]) issue_s(1, i + 1);
-                                release(C::k_fill(i + 1));
+                                if (i + 1 < cnt[1]) issue_s(1, kp);
+                                release(kp);
                                 if (i + 2 == n) tc_commit(smem_addr(&sh->q_empty));
                             }
+                            vp.step(2);
+                            kp.step(2);
                         }
                     } else {
                         for (int i = 0; i < 2 && i < n; ++i) {
-                            if (!wait_k(i)) return false;
-                            issue_s(i, i);
-                            release(C::k_fill(i));
+                            if (!wait_at(kp)) return false;
+                            issue_s(i, kp);
+                            release(kp);
                             if (i == n - 1) tc_commit(smem_addr(&sh->q_empty));
+                            kp.step(i == 0 ? 1 : 2);
                         }
+                        vp.step(n == 1 ? 1 : 2);
                         for (int i0 = 0; i0 < n; i0 += 2) {
 #pragma unroll
                             for (int grp = 0; grp < 2; ++grp) {
                                 const int i = i0 + grp;
                                 if (i >= n) break;
-                                if (!wait_v(i) || (i + 2 < n && !wait_k(i + 2)) || !issue_pv(grp, i0 >> 1, i)) return false;
-                                release(C::v_fill(i, n));
+                                if (!wait_at(vp) || !wait_fixed(i) || (i + 2 < n && !wait_at(kp)) ||
+                                    !issue_pv(grp, i0 >> 1, vp))
+                                    return false;
+                                release(vp);
                                 if (i + 2 < n) {
-                                    issue_s(grp, i + 2);
-                                    release(C::k_fill(i + 2));
+                                    issue_s(grp, kp);
+                                    release(kp);
                                     if (i + 3 == n) tc_commit(smem_addr(&sh->q_empty));
                                 }
+                                vp.step(i + 2 < n ? 2 : 1);
+                                kp.step(2);
                             }
                         }
                     }
