@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -891,6 +892,9 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
     if (pl.tc) {
         p.status = status_word(dev);
         if (!p.status) return PA_ERR_CUDA;
+        // masked scores are infinities before the scale: a zero scale would make them NaN; the smallest
+        // normal number gives the same weights, all ones
+        if (std::fabs(p.scale_log2) < FLT_MIN) p.scale_log2 = FLT_MIN;
         p.max_tail = pl.max_tail;
         p.tail_info = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.info_off);
         const bool contig = s.contig_stride > 0, f16 = kv_dtype == PA_F16;

@@ -5,7 +5,9 @@
 // Mathematics: O = softmax(scale Q K^T + mask) V, the softmax held as a running
 // maximum m and sum l of base-2 exponentials while 128-token K/V tiles stream
 // past. m only moves when a score passes it by more than 2^8 (then O and l are
-// rescaled): the result is the same, O is almost never touched.
+// rescaled): the result is the same, O is almost never touched. (Computing a
+// tile's first weights with the maximum so far while its own is still being found
+// was 6-12 % slower: both groups then want the exponential unit at once.)
 //
 // Rows. A row is (query token, query head); a KV head's rows are packed token
 // by token, heads_per_tile heads each, into tiles of at most 128 rows, one
@@ -53,7 +55,7 @@ constexpr int kTile = 128;           // context tokens per K/V tile
 constexpr int kSlots = 5;            // ring of K and V tiles, in the order the products take them
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 11;
-constexpr int kSegs = 2;             // published segments in flight
+constexpr int kSegs = 3;             // published segments in flight
 constexpr int kSegReaders = 11;      // MMA warp, two K warps, eight softmax warps
 constexpr float kSlack = 8.f;        // base-2 headroom before the running maximum moves
 constexpr int kMaxTail = 160;        // units of a partial wave: fewer than CTAs
@@ -91,12 +93,12 @@ struct Shared {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
-    uint64_t v_fixed;                      // a V tile's rows past the context are zeroed
-    uint64_t join_full[2];                 // one row tile: a group's maxima and sums are posted
+    uint64_t v_land;                       // the copies of a V tile that is to be mended before it counts as full
+    uint64_t join_full[2][2];              // one row tile: [segment parity][group] maxima and sums are posted
     uint64_t done;
     uint32_t tmem;
     int abort_flag;
-    int last_fill[kSlots], q_issued;       // what has been started, for the drain after a timeout
+    int last_fill[kSlots], q_issued, lands;   // what has been started, for the drain after a timeout
     Seg seg[kSegs];
     int tail_prefix[kMaxTail + 1];         // tiles of the cut wave's units, summed
     int tail_work[kMaxTail];
@@ -213,6 +215,12 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t 
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// 32 bytes of a row, a whole sector (16-byte aligned: rows of out may start anywhere that out does).
+__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t (&w)[8]) {
+    uint4 *d = reinterpret_cast<uint4 *>(dst);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
@@ -281,79 +289,41 @@ struct Scheduler {
     int tail, tail_ctas;     // units of the cut wave, CTAs that share it
     int64_t tail_tiles, a, e;   // its tiles; this CTA's remaining range
     int r;                   // unit of the cut wave that holds tile a
-    int tail_unit;           // unit of the cut wave handed out last
-    int base, before;        // resume point of the search: first sequence of a chunk, tiles before it
+    // 32 sequences at a time, one a lane: its extent, its row tiles and those before it in the chunk
+    int base, before, total; // first sequence of the chunk, row tiles before the chunk, row tiles in it
+    PrefillSeq seq;
+    int n, excl;
 };
 
-// Find row tile x at or after the scheduler's resume point (x never decreases
-// within the whole units, nor within the tail).
-__device__ __forceinline__ int sched_find(const PrefillParams &p, Scheduler &sc, int64_t x, int lane, int &tile, int &ntiles) {
-    for (; sc.base < p.num_seqs; sc.base += 32) {
-        const int b = sc.base + lane;
-        int n = 0;
-        if (b < p.num_seqs) n = (prefill_seq(p, b).qlen + p.tile_tokens - 1) / p.tile_tokens;
-        int sum = n;
+__device__ __forceinline__ void sched_chunk(const PrefillParams &p, Scheduler &sc, int lane) {
+    const int b = sc.base + lane;
+    sc.seq = PrefillSeq{0, 0, 0};
+    if (b < p.num_seqs) sc.seq = prefill_seq(p, b);
+    sc.n = (sc.seq.qlen + p.tile_tokens - 1) / p.tile_tokens;
+    int sum = sc.n;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, x < sc.before + sum);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            tile = static_cast<int>(x - sc.before) - __shfl_sync(0xffffffffu, sum - n, l);
-            ntiles = __shfl_sync(0xffffffffu, n, l);
-            return sc.base + l;
-        }
-        sc.before += __shfl_sync(0xffffffffu, sum, 31);
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
     }
-    return -1;
-}
-
-template <bool kTwoTiles>
-__device__ __forceinline__ void fill_seg(const PrefillParams &p, Seg &g, int b, int tile, int y, int t0, int t1,
-                                         int piece) {
-    const PrefillSeq s = prefill_seq(p, b);
-    const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
-    g.b = b;
-    g.tok0 = tile * p.tile_tokens;
-    g.q0 = s.q0 + g.tok0;
-    g.ntok = min(p.tile_tokens, s.qlen - g.tok0);
-    g.ctx = s.ctx;
-    g.qlen = s.qlen;
-    g.kvh = y / p.ntile;
-    g.h0 = (y % p.ntile) * p.heads_per_tile;
-    g.nh = min(p.heads_per_tile, p.group - g.h0);
-    const int tiles = unit_tiles(p, s, tile);
-    g.t0 = t0;
-    g.n = max(0, min(t1, tiles) - t0);
-    if (kTwoTiles) {   // the first row tile may see one K/V tile fewer, the second may have no tokens
-        const int first = (prefill_sees(p, s, g.tok0 + min(row_tokens, g.ntok) - 1) + kTile - 1) / kTile;
-        g.cnt[0] = max(0, min(g.n, first - t0));
-        g.cnt[1] = g.ntok > row_tokens ? g.n : 0;
-    } else {
-        g.cnt[0] = (g.n + 1) / 2;
-        g.cnt[1] = g.n / 2;
-    }
-    g.piece = piece;
+    sc.excl = sum - sc.n;
+    sc.total = __shfl_sync(0xffffffffu, sum, 31);
 }
 
 __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, int lane) {
-    int64_t x = 0;
-    for (int b = lane; b < p.num_seqs; b += 32) x += (prefill_seq(p, b).qlen + p.tile_tokens - 1) / p.tile_tokens;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     const int ys = p.num_kv_heads * p.ntile;
     const int ctas = gridDim.x;
+    int64_t x = 0;
+    for (sc.base = 0; sc.base < p.num_seqs; sc.base += 32) {
+        sched_chunk(p, sc, lane);
+        x += sc.total;
+    }
     sc.units = x * ys;
     sc.nfull = sc.units;
     sc.next = blockIdx.x;
-    sc.tail = 0;
-    sc.base = sc.before = 0;
-    sc.a = sc.e = 0;
-    sc.r = sc.tail_unit = 0;
+    sc.tail = sc.r = 0;
+    sc.a = sc.e = sc.tail_tiles = 0;
     sc.tail_ctas = 1;
-    sc.tail_tiles = 0;
     const int64_t rem = sc.units % ctas;
     // a wave that fills nine tenths of the CTAs is as good uncut, without the merge
     if (p.nsplit > 1 && rem > 0 && rem * 10 < static_cast<int64_t>(ctas) * 9) {
@@ -362,50 +332,45 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
         // tiles of the tail's row tiles [x_lo, x_hi], lanes over sequences
         const int64_t x_lo = sc.nfull / ys, x_hi = (sc.units - 1) / ys;
         int64_t before = 0;
-        for (int base = 0; base < p.num_seqs; base += 32) {
-            const int b = base + lane;
-            PrefillSeq s{};
-            int n = 0;
-            if (b < p.num_seqs) {
-                s = prefill_seq(p, b);
-                n = (s.qlen + p.tile_tokens - 1) / p.tile_tokens;
-            }
-            int sum = n;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
-            }
-            const int64_t first = before + sum - n;                 // this sequence's row tiles: first .. first + n - 1
-            const int64_t lo = first > x_lo ? first : x_lo, hi = first + n - 1 < x_hi ? first + n - 1 : x_hi;
+        for (sc.base = 0; sc.base < p.num_seqs; sc.base += 32) {
+            if (p.num_seqs > 32) sched_chunk(p, sc, lane);
+            const int64_t first = before + sc.excl;                // this sequence's row tiles: first .. first + n - 1
+            const int64_t lo = first > x_lo ? first : x_lo, hi = first + sc.n - 1 < x_hi ? first + sc.n - 1 : x_hi;
             for (int64_t t = lo; t <= hi; ++t)
-                sh->tail_work[t - x_lo] = max(1, unit_tiles(p, s, n - 1 - static_cast<int>(t - first)));
-            before += __shfl_sync(0xffffffffu, sum, 31);
+                sh->tail_work[t - x_lo] = max(1, unit_tiles(p, sc.seq, sc.n - 1 - static_cast<int>(t - first)));
+            before += sc.total;
         }
         __syncwarp();
-        int total = 0;
-        for (int r0 = 0; r0 < sc.tail; r0 += 32) {
-            const int r = r0 + lane;
-            const int w = r < sc.tail ? sh->tail_work[(sc.nfull + r) / ys - x_lo] : 0;
-            int sum = w;
+        // sums over the tail's units, lane l over units [l per, (l + 1) per)
+        const int per = (sc.tail + 31) / 32, skip = static_cast<int>(sc.nfull - x_lo * ys);
+        int mine = 0;
+        for (int r = lane * per; r < min(sc.tail, (lane + 1) * per); ++r) mine += sh->tail_work[(skip + r) / ys];
+        int sum = mine;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
-            }
-            if (r < sc.tail) sh->tail_prefix[r + 1] = total + sum;
-            total += __shfl_sync(0xffffffffu, sum, 31);
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
         }
-        if (lane == 0) sh->tail_prefix[0] = 0;
-        __syncwarp();
+        const int total = __shfl_sync(0xffffffffu, sum, 31);
         sc.tail_tiles = total;
         sc.tail_ctas = max(1, min(ctas, total / kMinPiece));
         if (static_cast<int>(blockIdx.x) < sc.tail_ctas) {
             sc.a = sc.tail_tiles * blockIdx.x / sc.tail_ctas;
             sc.e = sc.tail_tiles * (blockIdx.x + 1) / sc.tail_ctas;
-            while (sc.a < sc.e && sh->tail_prefix[sc.r + 1] <= sc.a) ++sc.r;
         }
+        int at = sum - mine, holds = 0;
+        for (int r = lane * per; r < min(sc.tail, (lane + 1) * per); ++r) {
+            sh->tail_prefix[r] = at;
+            const int end = at + sh->tail_work[(skip + r) / ys];
+            if (at <= sc.a && sc.a < end) holds = r;                // the unit of this CTA's first tile
+            at = end;
+        }
+        if (lane == 0) sh->tail_prefix[sc.tail] = total;
+        sc.r = __reduce_max_sync(0xffffffffu, holds);
+        __syncwarp();
     }
+    sc.base = sc.before = 0;
+    if (p.num_seqs > 32) sched_chunk(p, sc, lane);
     if (blockIdx.x == 0 && p.nsplit > 1) {   // for the merge
         for (int i = lane; i <= sc.tail; i += 32) p.tail_info[kTailPrefix + i] = sc.tail ? sh->tail_prefix[i] : 0;
         if (lane == 0) {
@@ -426,7 +391,6 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
         sc.next += gridDim.x;
     } else if (sc.a < sc.e) {
         while (sh->tail_prefix[sc.r + 1] <= sc.a) ++sc.r;
-        sc.tail_unit = sc.r;
         const int p0 = sh->tail_prefix[sc.r], p1 = sh->tail_prefix[sc.r + 1];
         u = sc.nfull + sc.r;
         t0 = static_cast<int>(sc.a) - p0;
@@ -437,12 +401,53 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
         if (lane == 0) g.piece = -2;
         return;
     }
-    int tile = 0, ntiles = 0;
-    const int b = sched_find(p, sc, u / ys, lane, tile, ntiles);
+    // the sequence whose row tiles hold u / ys (never before the chunk: units only go up)
+    const int64_t x = u / ys;
+    while (x >= static_cast<int64_t>(sc.before) + sc.total && sc.base + 32 < p.num_seqs) {
+        sc.before += sc.total;
+        sc.base += 32;
+        sched_chunk(p, sc, lane);
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, x < static_cast<int64_t>(sc.before) + sc.excl + sc.n);
+    const int l = hit ? __ffs(hit) - 1 : 31;
+    PrefillSeq s;
+    s.q0 = __shfl_sync(0xffffffffu, sc.seq.q0, l);
+    s.qlen = __shfl_sync(0xffffffffu, sc.seq.qlen, l);
+    s.ctx = __shfl_sync(0xffffffffu, sc.seq.ctx, l);
+    const int ntiles = __shfl_sync(0xffffffffu, sc.n, l);
+    const int from = static_cast<int>(x - sc.before) - __shfl_sync(0xffffffffu, sc.excl, l);
+    if (lane != 0) return;
     // within a sequence the last row tile first: the longest work of a causal mask starts first
-    if (lane == 0) {
-        if (b < 0) g.piece = -2;
-        else fill_seg<kTwoTiles>(p, g, b, ntiles - 1 - tile, static_cast<int>(u % ys), t0, t1, piece);
+    const int tile = ntiles - 1 - from, y = static_cast<int>(u - x * ys);
+    const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
+    g.b = sc.base + l;
+    g.tok0 = tile * p.tile_tokens;
+    g.q0 = s.q0 + g.tok0;
+    g.ntok = min(p.tile_tokens, s.qlen - g.tok0);
+    g.ctx = s.ctx;
+    g.qlen = s.qlen;
+    g.kvh = y / p.ntile;
+    g.h0 = (y - g.kvh * p.ntile) * p.heads_per_tile;
+    g.nh = min(p.heads_per_tile, p.group - g.h0);
+    const int tiles = unit_tiles(p, s, tile);
+    g.t0 = t0;
+    g.n = max(0, min(t1, tiles) - t0);
+    if (kTwoTiles) {   // the first row tile may see one K/V tile fewer, the second may have no tokens
+        const int first = (prefill_sees(p, s, g.tok0 + min(row_tokens, g.ntok) - 1) + kTile - 1) / kTile;
+        g.cnt[0] = max(0, min(g.n, first - t0));
+        g.cnt[1] = g.ntok > row_tokens ? g.n : 0;
+    } else {
+        g.cnt[0] = (g.n + 1) / 2;
+        g.cnt[1] = g.n / 2;
+    }
+    g.piece = piece;
+    if (piece >= 0 && t0 == 0) {   // a cut unit, for the merge
+        int *d = p.tail_info + kTailUnits + sc.r * 8;
+        d[0] = g.q0;
+        d[1] = g.ntok;
+        d[2] = g.kvh;
+        d[3] = g.h0;
+        d[4] = g.nh;
     }
 }
 
@@ -495,16 +500,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             mbar_init(smem_addr(&sh->p_full[g][1]), 4);
             mbar_init(smem_addr(&sh->o_full[g]), 1);
             mbar_init(smem_addr(&sh->o_free[g]), kTwoTiles ? 4 : 8);
-            mbar_init(smem_addr(&sh->join_full[g]), 4);
+            mbar_init(smem_addr(&sh->join_full[0][g]), 4);
+            mbar_init(smem_addr(&sh->join_full[1][g]), 4);
         }
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_addr(&sh->seg_full[i]), 1);
             mbar_init(smem_addr(&sh->seg_empty[i]), kSegReaders);
         }
         mbar_init(smem_addr(&sh->done), 1);
-        mbar_init(smem_addr(&sh->v_fixed), 1);
+        mbar_init(smem_addr(&sh->v_land), 1);
         sh->abort_flag = 0;
-        sh->q_issued = 0;
+        sh->q_issued = sh->lands = 0;
         mbar_fence_init();
     } else if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(&sh->tmem), 512u);
@@ -514,7 +520,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     tc_fence_after();
     const uint32_t tmem = uniform(sh->tmem);
     grid_dependency_wait();
-    // tensor-memory columns: S (and P) of group g at 128 g, O at 256 + 128 g
+    // tensor-memory columns: S of group g at 128 g, P in its place, O at 256 + 128 g
     auto s_col = [&](int g) { return tmem + g * 128; };
     auto o_col = [&](int g) { return tmem + 256 + g * 128; };
     const int R = box_tokens(p), r_shift = 31 - __clz(R);                    // powers of two, like the block size
@@ -528,22 +534,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             sched_init(p, sh, sc, lane);
             const uint64_t policy = l2_policy_evict_normal(), q_policy = l2_policy_evict_first();
             const int q_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
-            int fills = 0;                       // of the segments before
-            for (int k = 0;; ++k) {
-                Seg *g = &sh->seg[k % kSegs];
-                if (k >= kSegs && !wait_bar(p, sh, &sh->seg_empty[k % kSegs], ((k / kSegs) - 1) & 1)) break;
-                sched_next<kTwoTiles>(p, sh, sc, *g, lane);
+            // segment k's readers have all begun it before segment k + kSegs takes its place
+            auto publish = [&](int k) {
+                if (k >= kSegs && !wait_bar(p, sh, &sh->seg_empty[k % kSegs], ((k / kSegs) - 1) & 1)) return false;
+                sched_next<kTwoTiles>(p, sh, sc, sh->seg[k % kSegs], lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_full[k % kSegs]));
+                return true;
+            };
+            int fills = 0, lands = 0;            // of the segments before: ring tiles, mended V tiles
+            publish(0);
+            for (int k = 0;; ++k) {
+                const Seg *g = &sh->seg[k % kSegs];
                 if (g->piece == -2) break;
-                if (lane == 0 && g->piece >= 0 && g->t0 == 0) {   // a cut unit, for the merge
-                    int *d = p.tail_info + kTailUnits + sc.tail_unit * 8;
-                    d[0] = g->q0;
-                    d[1] = g->ntok;
-                    d[2] = g->kvh;
-                    d[3] = g->h0;
-                    d[4] = g->nh;
-                }
                 if (k > 0 && !wait_bar(p, sh, &sh->q_empty, (k - 1) & 1)) break;
                 const int b = uniform(g->b), ctx = uniform(g->ctx), kvh = uniform(g->kvh), n = uniform(g->n),
                           first = uniform(g->t0), h0 = uniform(g->h0), q0 = uniform(g->q0);
@@ -561,6 +564,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     sh->q_issued = k + 1;
                 }
                 __syncwarp();
+                // the K warps run into the next segment while this one's V still comes
+                if (!publish(k + 1)) break;
                 BlockIds ids{-1, 0};
                 const int nblk = (ctx + p.block_size - 1) >> bs_shift;
                 bool ok = true;
@@ -570,13 +575,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         ok = false;
                         break;
                     }
-                    const int boxes = (min(ctx - t0, kTile) + R - 1) >> r_shift;
+                    const int boxes = (min(ctx - t0, kTile) + R - 1) >> r_shift, valid = ctx - t0;
                     const uint32_t full = smem_addr(&sh->full[slot]);
+                    // where the context ends inside the tile, its copies land on a barrier of this warp's own
+                    const bool mend = valid < kTile;
+                    const uint32_t land = mend ? smem_addr(&sh->v_land) : full;
                     const uint32_t dst = smem_addr(ring + slot * C::kSlotBytes);
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
-                        mbar_arrive(full);
-                        sh->last_fill[slot] = f;
+                        mbar_arrive_expect_tx(land, static_cast<uint32_t>(boxes * C::kHalves * R * 128));
+                        if (mend) {
+                            sh->lands = lands + 1;
+                        } else {
+                            mbar_arrive(full);
+                            sh->last_fill[slot] = f;
+                        }
                     }
                     __syncwarp();
                     for (int j = 0; j < boxes; ++j) {
@@ -589,16 +601,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                             at = tok & (p.block_size - 1);
                         }
                         if (elect_one())
-                            tma_load_5d(dst + j * (C::kHalves * R * 128), &tmap_v, 0, at, 0, kvh, blk, full, policy);
+                            tma_load_5d(dst + j * (C::kHalves * R * 128), &tmap_v, 0, at, 0, kvh, blk, land, policy);
                         __syncwarp();
                     }
-                    const int valid = ctx - t0;
-                    if (valid < kTile) {   // the context ends inside the tile: zero its other rows once it has landed
-                        if (!wait_bar(p, sh, &sh->full[slot], (f / kSlots) & 1)) {
+                    if (mend) {   // zero the rows past the context; then the tile is full
+                        if (!wait_bar(p, sh, &sh->v_land, lands & 1)) {
                             ok = false;
                             break;
                         }
-                        unsigned char *v = ring + slot * C::kSlotBytes;
+                        ++lands;
+                        unsigned char *v = ring + slot * C::kSlotBytes;   // boxes of [half][R tokens][128 bytes]
                         for (int x = lane; x < (kTile - valid) * C::kHalves * 8; x += 32) {
                             const int row = valid + x / (C::kHalves * 8), c = x % (C::kHalves * 8);
                             *reinterpret_cast<uint4 *>(v + (row >> r_shift) * (C::kHalves * R * 128) + (c / 8) * (R * 128) +
@@ -606,7 +618,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&sh->v_fixed));
+                        if (lane == 0) {
+                            mbar_arrive(full);
+                            mbar_arrive(full);
+                        }
                     }
                 }
                 if (!ok) break;
@@ -672,17 +687,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 v_off[kk] = desc_step(R >= 16 ? ((kk * 16) >> r_shift) * v_box + ((kk * 16) & (R - 1)) * 128 : kk * 2 * v_box);
             const uint64_t q_desc = smem_desc_sw128(smem_addr(q_s), 16, 1024), k_desc = smem_desc_sw128(smem_addr(ring), 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), R * 128, R >= 16 ? 1024 : C::kHalves * 1024);
-            int fills = 0, fixed = 0;            // of the segments before: ring tiles, zeroed V tiles
+            int fills = 0;                       // ring tiles of the segments before
             int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};   // a group's tiles; its segments with any
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const Seg *g = &sh->seg[k % kSegs];
                 if (!wait_bar(p, sh, &sh->seg_full[k % kSegs], (k / kSegs) & 1) || g->piece == -2) break;
-                const int n = uniform(g->n), ctx = uniform(g->ctx), first = uniform(g->t0);
+                const int n = uniform(g->n);
                 const int cnt[2] = {uniform(g->cnt[0]), uniform(g->cnt[1])};
                 if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
                 if (!wait_bar(p, sh, &sh->q_full, k & 1)) break;
-                const bool cut = ctx < (first + n) * kTile;   // the context ends inside the last tile
                 // places in the ring: the next K and V tile's slot and phase, stepped along
                 struct Place {
                     int slot, phase;
@@ -733,7 +747,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         return true;
                     }
                     Place kp{fills % kSlots, (fills / kSlots) & 1}, vp = kp;
-                    auto wait_fixed = [&](int i) { return !cut || i != n - 1 || wait_bar_one(p, sh, &sh->v_fixed, fixed & 1); };
                     if constexpr (kTwoTiles) {
                         if (!wait_at(kp)) return false;
                         if (cnt[0] > 0) issue_s(0, kp);
@@ -743,7 +756,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         vp.step(1);
                         kp.step(2);
                         for (int i = 0; i < n; ++i) {
-                            if (!wait_at(vp) || !wait_fixed(i) || (i + 1 < n && !wait_at(kp))) return false;
+                            if (!wait_at(vp) || (i + 1 < n && !wait_at(kp))) return false;
                             if (i < cnt[0] && !issue_pv(0, i, vp)) return false;
                             if (i + 1 < cnt[0]) issue_s(0, kp);
                             if (i < cnt[1] && !issue_pv(1, i, vp)) return false;
@@ -770,7 +783,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                             for (int grp = 0; grp < 2; ++grp) {
                                 const int i = i0 + grp;
                                 if (i >= n) break;
-                                if (!wait_at(vp) || !wait_fixed(i) || (i + 2 < n && !wait_at(kp)) ||
+                                if (!wait_at(vp) || (i + 2 < n && !wait_at(kp)) ||
                                     !issue_pv(grp, i0 >> 1, vp))
                                     return false;
                                 release(vp);
@@ -791,7 +804,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 __syncwarp();
                 ok = __all_sync(0xffffffffu, done);
                 fills += 2 * n;
-                fixed += cut && n > 0;
 #pragma unroll
                 for (int grp = 0; grp < 2; ++grp) {
                     s_cnt[grp] += cnt[grp];
@@ -813,6 +825,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
         const int rt = row / p.heads_per_tile, rh = row - rt * p.heads_per_tile;
         const float sl2 = p.scale_log2;
+        const bool up = sl2 >= 0.f;
         int s_cnt = 0, o_cnt = 0, o_other = 0;   // tiles; segments in which this / the other group had any
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -836,25 +849,45 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 const int t0 = (first + (kTwoTiles ? j : 2 * j + grp)) * kTile;
                 float s[kTile];
                 tmem_ld128(s_col(grp) + lanes, s);
-                float mul = sl2;
-                bool up = sl2 >= 0.f;
-                if (t0 + kTile > whole) {   // scaled here, so that -inf is the mask whatever the scale
+                if (t0 + kTile > whole) {     // (the scale is never zero: infinity times it is the mask)
                     const int valid = sees - t0;
+                    const float never = up ? -INFINITY : INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c) s[c] = c < valid ? s[c] * sl2 : -INFINITY;
-                    mul = 1.f;
-                    up = true;
+                    for (int c = 0; c < kTile; ++c) s[c] = c < valid ? s[c] : never;
                 }
-                float mx = (up ? row_max<true>(s) : row_max<false>(s)) * mul;
-                const bool need = mx > m + kSlack;
-                const float m_new = need ? mx : m;
-                const float alpha = fast_exp2(m - m_new);
-                m = m_new;
-                l *= alpha;
-                // S of this tile was issued behind the group's previous P V: O is at rest until P appears
-                if (j > 0 && __any_sync(0xffffffffu, need)) {
+                uint64_t sum[2] = {0, 0};
+                auto weights = [&](int half) {   // 2^(s * scale - m), two at a time
+                    const uint64_t mul2 = pair(sl2, sl2), neg2 = pair(-m, -m);
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
+                    for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            float e0, e1;
+                            unpair(fma2(pair(s[c0 + 2 * c], s[c0 + 2 * c + 1]), mul2, neg2), e0, e1);
+                            e0 = fast_exp2(e0);
+                            e1 = fast_exp2(e1);
+                            sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
+                            w[c] = pack16<kF16>(e0, e1);   // the weights' one rounding, to the caches' type
+                        }
+                        tmem_st16_nowait(s_col(grp) + lanes + c0 / 2, w);
+                    }
+                };
+                auto hand_over = [&](int half) {   // 64 tokens' weights are there: the products may start on them
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[grp][half]));
+                };
+                const float mx = (up ? row_max<true>(s) : row_max<false>(s)) * sl2;
+                const bool need = mx > m + kSlack;
+                if (__any_sync(0xffffffffu, need)) {
+                    const float m_new = need ? mx : m, alpha = fast_exp2(m - m_new);
+                    m = m_new;
+                    l *= alpha;
+                    // S of this tile was issued behind the group's previous P V: O is at rest until P appears
+#pragma unroll 1
+                    for (int c = 0; c < D && j > 0; c += 32) {
                         float o[32];
                         tmem_ld32(o_col(grp) + lanes + c, o);
 #pragma unroll
@@ -862,28 +895,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         tmem_st32(o_col(grp) + lanes + c, o);
                     }
                 }
-                const uint64_t mul2 = pair(mul, mul), neg2 = pair(-m, -m);
-                uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {   // 2^(s * scale - m), two at a time
-                        float e0, e1;
-                        unpair(fma2(pair(s[c0 + 2 * c], s[c0 + 2 * c + 1]), mul2, neg2), e0, e1);
-                        e0 = fast_exp2(e0);
-                        e1 = fast_exp2(e1);
-                        sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
-                        w[c] = pack16<kF16>(e0, e1);   // the weights' one rounding, to the caches' type
-                    }
-                    tmem_st16_nowait(s_col(grp) + lanes + c0 / 2, w);
-                    if (c0 & 32) {   // 64 tokens' weights are there: the products may start on them
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[grp][c0 / 64]));
-                    }
-                }
+                weights(0);
+                hand_over(0);
+                weights(1);
+                hand_over(1);
                 float a0, a1;
                 unpair(add2(sum[0], sum[1]), a0, a1);
                 l += a0 + a1;
@@ -895,8 +910,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 join->m[k & 1][grp][row] = m;
                 join->l[k & 1][grp][row] = l;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh->join_full[grp]));
-                if (!wait_bar(p, sh, &sh->join_full[grp ^ 1], k & 1)) break;
+                if (lane == 0) mbar_arrive(smem_addr(&sh->join_full[k & 1][grp]));
+                if (!wait_bar(p, sh, &sh->join_full[k & 1][grp ^ 1], (k >> 1) & 1)) break;
                 const float mo = join->m[k & 1][grp ^ 1][row], lo = join->l[k & 1][grp ^ 1][row];
                 const float M = fmaxf(m, mo);
                 wa = cnt > 0 ? fast_exp2(m - M) : 0.f;
@@ -913,7 +928,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             // one row tile: each group writes half of the columns, from both groups' O
             constexpr int kCols = kTwoTiles ? D : D / 2;
             const int col0 = kTwoTiles ? 0 : grp * kCols;
-#pragma unroll
+            // (not unrolled: code that runs once a unit costs its fetch from memory)
+#pragma unroll 1
             for (int c = 0; c < kCols; c += 32) {
                 float o[32];
                 if (cnt > 0) {
@@ -944,22 +960,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 #pragma unroll
                     for (int e = 0; e < 32; ++e) dst[e * kM] = o[e];
                 } else if (live) {
-                    if (p.out_type == 0) {
-                        float *dst = static_cast<float *>(p.out) + orow * D + col0 + c;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    } else {
+                    if (p.out_type == (kF16 ? 2 : 1)) {
                         uint16_t *dst = static_cast<uint16_t *>(p.out) + orow * D + col0 + c;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                w[x] = p.out_type == 1 ? pack_bf16x2(o[e + 2 * x], o[e + 2 * x + 1])
-                                                       : pack_f16x2(o[e + 2 * x], o[e + 2 * x + 1]);
-                            *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int x = 0; x < 8; ++x) w[x] = pack16<kF16>(o[e + 2 * x], o[e + 2 * x + 1]);
+                            store_32_bytes(dst + e, w);
                         }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) store_pair_as(p.out, p.out_type, orow * D + col0 + c + e, o[e], o[e + 1]);
                     }
                 }
             }
@@ -982,6 +994,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (int i = 0; i < kSlots; ++i)
             if (sh->last_fill[i] >= 0)
                 mbar_wait_for(smem_addr(&sh->full[i]), (sh->last_fill[i] / kSlots) & 1, 100000000ull);
+        if (sh->lands) mbar_wait_for(smem_addr(&sh->v_land), (sh->lands - 1) & 1, 100000000ull);
         if (sh->q_issued) mbar_wait_for(smem_addr(&sh->q_full), (sh->q_issued - 1) & 1, 100000000ull);
     }
     __syncthreads();

@@ -151,6 +151,27 @@ def test_large_ragged_batch():
             c.check(c.run(True, ws), True)
 
 
+@pytest.mark.parametrize("shape", [(186, 1, 700, 4, 8, 64, 128), (77, 4, 2000, 4, 4, 128, 128), (300, 2, 200, 2, 4, 64, 16),
+                                   (95, 30, 2000, 1, 2, 128, 64)])
+def test_many_short_pieces_a_cta(shape):
+    """Far more sequences than CTAs, each of a few tiles: a CTA's producers run segments ahead of its products.
+    The same bits every time."""
+    n, q_hi, past, hkv, g, d, bs = shape
+    rng = np.random.default_rng(n)
+    q = rng.integers(0, q_hi + 1, n)
+    q[0] = q_hi
+    ctx = q + rng.integers(0, past + 1, n)
+    for dt in ("fp16", "bf16"):
+        c = Case(q.tolist(), ctx.tolist(), hkv * g, hkv, d, bs, dt, seed=24)
+        for causal in (True, False):
+            for ws in (None, c.workspace()):
+                out = c.run(causal, ws)
+                c.check(out, causal)
+                for _ in range(10):
+                    assert torch.equal(c.run(causal, ws), out)
+    assert pa.pa_device_status() == 0
+
+
 def test_long_prompt_and_long_context():
     """Many tiles per CTA, the whole pipeline's depth; 65,536 tokens of context."""
     c = Case([2000, 1], [2000, 2000], 8, 1, 128, 16, "bf16", seed=17)
