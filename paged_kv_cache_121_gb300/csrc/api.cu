@@ -857,7 +857,7 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
     const PrefillPlan pl = plan_prefill(s, kv_dtype, sms, workspace != nullptr || workspace_bytes != 0);
     if (pl.total && (!workspace || workspace_bytes < pl.total || !aligned16(workspace))) return PA_ERR_WORKSPACE;
     const int64_t ytiles = static_cast<int64_t>(s.num_kv_heads) * pl.ntile;
-    if (pl.tiles > INT32_MAX || ytiles > 65535) return PA_ERR_UNSUPPORTED;
+    if (pl.tiles * ytiles > INT32_MAX || ytiles > 65535) return PA_ERR_UNSUPPORTED;
     PrefillParams p;
     std::memset(&p, 0, sizeof p);
     p.query = query;

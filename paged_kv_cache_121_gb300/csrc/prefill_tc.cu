@@ -52,15 +52,15 @@ namespace {
 
 constexpr int kM = 128;              // rows of a row tile: tensor-memory lanes
 constexpr int kTile = 128;           // context tokens per K/V tile
-constexpr int kSlots = 5;            // ring of K and V tiles, in the order the products take them
+constexpr int kMaxSlots = 13;        // of the ring of K and V tiles, in the order the products take them
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 11;
 constexpr int kSegs = 3;             // published segments in flight
 constexpr int kSegReaders = 11;      // MMA warp, two K warps, eight softmax warps
 constexpr float kSlack = 8.f;        // base-2 headroom before the running maximum moves
 constexpr int kMaxTail = 160;        // units of a partial wave: fewer than CTAs
-// p.tail_info: units of the cut wave, CTAs that share it | their tiles' prefix sums | unit descriptors
-constexpr int kTailPrefix = 2, kTailUnits = kTailPrefix + kMaxTail + 1, kTailInts = kTailUnits + 8 * kMaxTail;
+// p.tail_info: units of the cut wave, CTAs that share it, its tiles | prefix sums of the tiles | unit descriptors
+constexpr int kTailPrefix = 3, kTailUnits = kTailPrefix + kMaxTail + 1, kTailInts = kTailUnits + 8 * kMaxTail;
 constexpr int kMinPiece = 4;         // tiles a CTA takes of a cut wave, at least
 
 template <int D, bool kTwoTiles>
@@ -70,6 +70,8 @@ struct Cfg {
     static constexpr int kQBytes = kHalves * kM * 128;      // one row tile
     static constexpr int kSlotBytes = kHalves * kTile * 128;
     static constexpr int kRingOff = kGroupsQ * kQBytes;
+    static constexpr int kSlots = ((kTwoTiles ? 224 : 220) * 1024 - kRingOff) / kSlotBytes;   // as many as fit
+    static_assert(kSlots >= 5 && kSlots <= kMaxSlots, "ring");
     static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
     // Place in the ring's order of tile i of a segment's n. Two row tiles: K0 V0 K1 V1 ...;
     // one, whose first two score tiles come before any weights: K0 K1 V0 K2 V1 ... V(n-1).
@@ -89,7 +91,7 @@ struct Seg {
 };
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots];  // K: one arrival of each K warp; V: two of its warp
+    uint64_t full[kMaxSlots], empty[kMaxSlots];  // K: one arrival of each K warp; V: two of its warp
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -98,7 +100,7 @@ struct Shared {
     uint64_t done;
     uint32_t tmem;
     int abort_flag;
-    int last_fill[kSlots], q_issued, lands;   // what has been started, for the drain after a timeout
+    int last_fill[kMaxSlots], q_issued, lands;   // what has been started, for the drain after a timeout
     Seg seg[kSegs];
     int tail_prefix[kMaxTail + 1];         // tiles of the cut wave's units, summed
     int tail_work[kMaxTail];
@@ -283,17 +285,23 @@ __device__ __forceinline__ int unit_tiles(const PrefillParams &p, const PrefillS
 // ---------------------------------------------------------------------------
 // The schedule (one warp): segments of this CTA, in order.
 // ---------------------------------------------------------------------------
-struct Scheduler {
-    int64_t units, nfull;    // all units; units taken whole
-    int64_t next;            // next whole unit of this CTA
-    int tail, tail_ctas;     // units of the cut wave, CTAs that share it
-    int64_t tail_tiles, a, e;   // its tiles; this CTA's remaining range
+struct Scheduler {           // (the host keeps the batch's units below 2^31)
+    int units, nfull;        // all units; units taken whole
+    int next;                // next whole unit of this CTA
+    int tail, a, e;          // units of the cut wave; this CTA's remaining range of its tiles
     int r;                   // unit of the cut wave that holds tile a
     // 32 sequences at a time, one a lane: its extent, its row tiles and those before it in the chunk
     int base, before, total; // first sequence of the chunk, row tiles before the chunk, row tiles in it
     PrefillSeq seq;
     int n, excl;
 };
+
+// The cut wave's tiles over the CTAs that share it: the first tiles % ctas take one more.
+__device__ __forceinline__ int range_begin(int c, int tiles, int ctas) { return c * (tiles / ctas) + min(c, tiles % ctas); }
+__device__ __forceinline__ int range_owner(int x, int tiles, int ctas) {
+    const int q = tiles / ctas, more = tiles % ctas, edge = more * (q + 1);
+    return x < edge ? x / (q + 1) : more + (x - edge) / q;   // (q >= 1: every CTA has a tile)
+}
 
 __device__ __forceinline__ void sched_chunk(const PrefillParams &p, Scheduler &sc, int lane) {
     const int b = sc.base + lane;
@@ -313,36 +321,33 @@ __device__ __forceinline__ void sched_chunk(const PrefillParams &p, Scheduler &s
 __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, int lane) {
     const int ys = p.num_kv_heads * p.ntile;
     const int ctas = gridDim.x;
-    int64_t x = 0;
+    int rows = 0;
     for (sc.base = 0; sc.base < p.num_seqs; sc.base += 32) {
         sched_chunk(p, sc, lane);
-        x += sc.total;
+        rows += sc.total;
     }
-    sc.units = x * ys;
-    sc.nfull = sc.units;
+    sc.units = sc.nfull = rows * ys;
     sc.next = blockIdx.x;
-    sc.tail = sc.r = 0;
-    sc.a = sc.e = sc.tail_tiles = 0;
-    sc.tail_ctas = 1;
-    const int64_t rem = sc.units % ctas;
+    sc.tail = sc.r = sc.a = sc.e = 0;
+    int tail_ctas = 1, tail_tiles = 0;
+    const int rem = sc.units % ctas;
     // a wave that fills nine tenths of the CTAs is as good uncut, without the merge
-    if (p.nsplit > 1 && rem > 0 && rem * 10 < static_cast<int64_t>(ctas) * 9) {
+    if (p.nsplit > 1 && rem > 0 && rem * 10 < ctas * 9) {
         sc.nfull = sc.units - rem;
-        sc.tail = static_cast<int>(rem);
+        sc.tail = rem;
         // tiles of the tail's row tiles [x_lo, x_hi], lanes over sequences
-        const int64_t x_lo = sc.nfull / ys, x_hi = (sc.units - 1) / ys;
-        int64_t before = 0;
+        const int x_lo = sc.nfull / ys, x_hi = (sc.units - 1) / ys;
+        int before = 0;
         for (sc.base = 0; sc.base < p.num_seqs; sc.base += 32) {
             if (p.num_seqs > 32) sched_chunk(p, sc, lane);
-            const int64_t first = before + sc.excl;                // this sequence's row tiles: first .. first + n - 1
-            const int64_t lo = first > x_lo ? first : x_lo, hi = first + sc.n - 1 < x_hi ? first + sc.n - 1 : x_hi;
-            for (int64_t t = lo; t <= hi; ++t)
-                sh->tail_work[t - x_lo] = max(1, unit_tiles(p, sc.seq, sc.n - 1 - static_cast<int>(t - first)));
+            const int first = before + sc.excl;                    // this sequence's row tiles: first .. first + n - 1
+            for (int t = max(first, x_lo); t <= min(first + sc.n - 1, x_hi); ++t)
+                sh->tail_work[t - x_lo] = max(1, unit_tiles(p, sc.seq, sc.n - 1 - (t - first)));
             before += sc.total;
         }
         __syncwarp();
         // sums over the tail's units, lane l over units [l per, (l + 1) per)
-        const int per = (sc.tail + 31) / 32, skip = static_cast<int>(sc.nfull - x_lo * ys);
+        const int per = (sc.tail + 31) / 32, skip = sc.nfull - x_lo * ys;
         int mine = 0;
         for (int r = lane * per; r < min(sc.tail, (lane + 1) * per); ++r) mine += sh->tail_work[(skip + r) / ys];
         int sum = mine;
@@ -351,12 +356,11 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
             const int o = __shfl_up_sync(0xffffffffu, sum, d);
             if (lane >= d) sum += o;
         }
-        const int total = __shfl_sync(0xffffffffu, sum, 31);
-        sc.tail_tiles = total;
-        sc.tail_ctas = max(1, min(ctas, total / kMinPiece));
-        if (static_cast<int>(blockIdx.x) < sc.tail_ctas) {
-            sc.a = sc.tail_tiles * blockIdx.x / sc.tail_ctas;
-            sc.e = sc.tail_tiles * (blockIdx.x + 1) / sc.tail_ctas;
+        tail_tiles = __shfl_sync(0xffffffffu, sum, 31);
+        tail_ctas = max(1, min(ctas, tail_tiles / kMinPiece));
+        if (static_cast<int>(blockIdx.x) < tail_ctas) {
+            sc.a = range_begin(blockIdx.x, tail_tiles, tail_ctas);
+            sc.e = range_begin(blockIdx.x + 1, tail_tiles, tail_ctas);
         }
         int at = sum - mine, holds = 0;
         for (int r = lane * per; r < min(sc.tail, (lane + 1) * per); ++r) {
@@ -365,7 +369,7 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
             if (at <= sc.a && sc.a < end) holds = r;                // the unit of this CTA's first tile
             at = end;
         }
-        if (lane == 0) sh->tail_prefix[sc.tail] = total;
+        if (lane == 0) sh->tail_prefix[sc.tail] = tail_tiles;
         sc.r = __reduce_max_sync(0xffffffffu, holds);
         __syncwarp();
     }
@@ -375,7 +379,8 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
         for (int i = lane; i <= sc.tail; i += 32) p.tail_info[kTailPrefix + i] = sc.tail ? sh->tail_prefix[i] : 0;
         if (lane == 0) {
             p.tail_info[0] = sc.tail;
-            p.tail_info[1] = sc.tail_ctas;
+            p.tail_info[1] = tail_ctas;
+            p.tail_info[2] = tail_tiles;
         }
     }
 }
@@ -384,8 +389,7 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
 template <bool kTwoTiles>
 __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, Scheduler &sc, Seg &g, int lane) {
     const int ys = p.num_kv_heads * p.ntile;
-    int64_t u;
-    int t0 = 0, t1 = INT_MAX, piece = -1;
+    int u, t0 = 0, t1 = INT_MAX, piece = -1;
     if (sc.next < sc.nfull) {
         u = sc.next;
         sc.next += gridDim.x;
@@ -393,8 +397,8 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
         while (sh->tail_prefix[sc.r + 1] <= sc.a) ++sc.r;
         const int p0 = sh->tail_prefix[sc.r], p1 = sh->tail_prefix[sc.r + 1];
         u = sc.nfull + sc.r;
-        t0 = static_cast<int>(sc.a) - p0;
-        t1 = static_cast<int>(sc.e < p1 ? sc.e : p1) - p0;
+        t0 = sc.a - p0;
+        t1 = min(sc.e, p1) - p0;
         if (t0 > 0 || t1 < p1 - p0) piece = static_cast<int>(blockIdx.x) + sc.r;
         sc.a = p0 + t1;
     } else {
@@ -402,23 +406,23 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
         return;
     }
     // the sequence whose row tiles hold u / ys (never before the chunk: units only go up)
-    const int64_t x = u / ys;
-    while (x >= static_cast<int64_t>(sc.before) + sc.total && sc.base + 32 < p.num_seqs) {
+    const int x = u / ys;
+    while (x >= sc.before + sc.total && sc.base + 32 < p.num_seqs) {
         sc.before += sc.total;
         sc.base += 32;
         sched_chunk(p, sc, lane);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, x < static_cast<int64_t>(sc.before) + sc.excl + sc.n);
+    const unsigned hit = __ballot_sync(0xffffffffu, x < sc.before + sc.excl + sc.n);
     const int l = hit ? __ffs(hit) - 1 : 31;
     PrefillSeq s;
     s.q0 = __shfl_sync(0xffffffffu, sc.seq.q0, l);
     s.qlen = __shfl_sync(0xffffffffu, sc.seq.qlen, l);
     s.ctx = __shfl_sync(0xffffffffu, sc.seq.ctx, l);
     const int ntiles = __shfl_sync(0xffffffffu, sc.n, l);
-    const int from = static_cast<int>(x - sc.before) - __shfl_sync(0xffffffffu, sc.excl, l);
+    const int from = x - sc.before - __shfl_sync(0xffffffffu, sc.excl, l);
     if (lane != 0) return;
     // within a sequence the last row tile first: the longest work of a causal mask starts first
-    const int tile = ntiles - 1 - from, y = static_cast<int>(u - x * ys);
+    const int tile = ntiles - 1 - from, y = u - x * ys;
     const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
     g.b = sc.base + l;
     g.tok0 = tile * p.tile_tokens;
@@ -475,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ PrefillParams p) {
     using C = Cfg<D, kTwoTiles>;
+    constexpr int kSlots = C::kSlots;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1015,32 +1020,45 @@ prefill_tc_merge_kernel(const __grid_constant__ PrefillParams p, int row_tiles) 
     grid_dependency_wait();
     grid_dependents_launch();
     const int r = blockIdx.x, rt = blockIdx.y, c0 = blockIdx.z * kMergeCols, row = threadIdx.x;
-    const int *info = p.tail_info;
-    const int tail = info[0];
+    // one round trip for the layout, one for the pieces: every load that may be needed at once
+    const int *info = p.tail_info, *d = info + kTailUnits + r * 8;
+    const int tail = info[0], ctas = info[1], tiles = info[2], p0 = info[kTailPrefix + r], p1 = info[kTailPrefix + r + 1];
+    const int q0 = d[0], ntok = d[1], kvh = d[2], h0 = d[3], nh = d[4];
     if (r >= tail) return;
-    const int64_t ctas = info[1], tiles = info[kTailPrefix + tail];
-    const int64_t p0 = info[kTailPrefix + r], p1 = info[kTailPrefix + r + 1];
-    // CTA c took tiles [c tiles / ctas, (c + 1) tiles / ctas): tile x belongs to ((x + 1) ctas - 1) / tiles
-    const int first = static_cast<int>(((p0 + 1) * ctas - 1) / tiles), last = static_cast<int>((p1 * ctas - 1) / tiles);
+    const int first = range_owner(p0, tiles, ctas), last = range_owner(p1 - 1, tiles, ctas);
     if (first == last) return;   // taken whole: written by its CTA
-    const int *d = info + kTailUnits + r * 8;
     const int row_tokens = p.tile_tokens / row_tiles;
     const int t = row / p.heads_per_tile, h = row - t * p.heads_per_tile, tok = rt * row_tokens + t;
-    if (t >= row_tokens || tok >= d[1] || h >= d[4]) return;
+    if (t >= row_tokens || tok >= ntok || h >= nh) return;
     float M = -1e30f, l = 0.f, o[kMergeCols];
 #pragma unroll
     for (int e = 0; e < kMergeCols; ++e) o[e] = 0.f;
-    for (int c = first; c <= last; ++c) M = fmaxf(M, p.part_max[(static_cast<int64_t>(c + r) * row_tiles + rt) * kM + row]);
-    for (int c = first; c <= last; ++c) {
-        const int64_t piece = static_cast<int64_t>(c + r) * row_tiles + rt;
-        const float w = fast_exp2(p.part_max[piece * kM + row] - M);
-        l = fmaf(w, p.part_sum[piece * kM + row], l);
-        const float *src = p.part_out + (piece * p.head_dim + c0) * kM + row;
+    for (int c = first; c <= last; c += 2) {   // two pieces at a time, folded into a running maximum
+        float m[2], s[2], x[2][kMergeCols];
 #pragma unroll
-        for (int e = 0; e < kMergeCols; ++e) o[e] = fmaf(w, src[e * kM], o[e]);
+        for (int k = 0; k < 2; ++k) {
+            m[k] = -1e30f;
+            s[k] = 0.f;
+            if (c + k > last) continue;
+            const int64_t piece = static_cast<int64_t>(c + k + r) * row_tiles + rt;
+            m[k] = p.part_max[piece * kM + row];
+            s[k] = p.part_sum[piece * kM + row];
+            const float *src = p.part_out + (piece * p.head_dim + c0) * kM + row;
+#pragma unroll
+            for (int e = 0; e < kMergeCols; ++e) x[k][e] = src[e * kM];
+        }
+        const float Mn = fmaxf(M, fmaxf(m[0], m[1])), a = fast_exp2(M - Mn), w0 = fast_exp2(m[0] - Mn),
+                    w1 = c + 1 <= last ? fast_exp2(m[1] - Mn) : 0.f;
+        M = Mn;
+        l = l * a + s[0] * w0 + s[1] * w1;
+#pragma unroll
+        for (int e = 0; e < kMergeCols; ++e) {
+            o[e] = fmaf(x[0][e], w0, o[e] * a);
+            if (c + 1 <= last) o[e] = fmaf(x[1][e], w1, o[e]);
+        }
     }
     const float inv = l > 0.f ? 1.f / l : l;
-    const int64_t at = (static_cast<int64_t>(d[0] + tok) * p.num_heads + d[2] * p.group + d[3] + h) * p.head_dim + c0;
+    const int64_t at = (static_cast<int64_t>(q0 + tok) * p.num_heads + kvh * p.group + h0 + h) * p.head_dim + c0;
 #pragma unroll
     for (int e = 0; e < kMergeCols; e += 2) store_pair_as(p.out, p.out_type, at + e, o[e] * inv, o[e + 1] * inv);
 }
