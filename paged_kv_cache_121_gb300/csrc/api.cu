@@ -755,13 +755,17 @@ struct PrefillShape {
 constexpr int kPrefillSimtCtasPerSm = 2;      // CTA slots the CUDA-core kernel's split fills
 constexpr int kPrefillSimtMinSplit = 256;     // tokens a piece, at least
 constexpr int kPrefillSimtMaxSplits = 16;
+constexpr int kPrefillRowsHeads = 8;          // KV heads of a few-rows CTA, at most
+constexpr int kPrefillRowsMinHeads = 4;       //   and at least, for that kernel to be taken
 
 // A wave's units are cut between CTAs only below this many waves: above, an idle
 // tail is under a tenth of the work and the pieces' traffic is not worth it.
 constexpr int kPrefillCutWaves = 6;
 
 struct PrefillPlan {
-    bool tc;                  // tensor-core kernel (else CUDA-core)
+    bool rows;                // few rows a KV head: mma.sync, equal tile ranges per CTA
+    int heads_per_cta;        //   KV heads of a CTA
+    bool tc;                  // tcgen05 kernel (else CUDA-core)
     bool tall;                // tc: two row tiles a unit, else one; CUDA-core: 64-row tiles, else 16
     int heads_per_tile, ntile, tile_tokens;
     int64_t tiles;            // upper bound of the batch's row tiles (the lengths are on the device)
@@ -790,7 +794,24 @@ pa_status check_prefill(const PrefillShape &s, pa_dtype out_dtype, pa_dtype q_dt
 PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool have_workspace) {
     PrefillPlan pl{};
     const int group = s.num_heads / s.num_kv_heads;
-    pl.tc = is16(kv_dtype) && prefill_tc_supported(s.head_dim, s.block_size, s.contig_stride > 0);
+    const bool contig = s.contig_stride > 0, pow2 = (s.block_size & (s.block_size - 1)) == 0;
+    // At most 16 rows a KV head, and enough KV heads to keep a CTA's warps busy (with one or two the
+    // tcgen05 kernel's CTAs, one KV head each, stream more): bound by the cache's bytes
+    pl.heads_per_cta = decode_mma_heads_per_cta(s.num_kv_heads, kPrefillRowsHeads);
+    pl.rows = is16(kv_dtype) && have_workspace && static_cast<int64_t>(s.max_query) * group <= prefill_rows_max() &&
+              pl.heads_per_cta >= kPrefillRowsMinHeads && s.num_seqs <= kPrefillRowsMaxSeqs &&
+              (contig || (s.block_size >= 16 && pow2)) &&
+              static_cast<int64_t>(s.num_seqs) * cdiv64(s.max_ctx, 16) < (int64_t(1) << 30);
+    if (pl.rows) {
+        pl.ctas = std::max(1, sms / (s.num_kv_heads / pl.heads_per_cta));
+        const size_t rows = static_cast<size_t>(2) * pl.ctas * s.num_kv_heads * prefill_rows_max();
+        pl.max_off = align256(rows * s.head_dim * sizeof(float));
+        pl.sum_off = pl.max_off + align256(rows * sizeof(float));
+        pl.info_off = pl.sum_off + align256(rows * sizeof(float));
+        pl.total = pl.info_off + align256(static_cast<size_t>(s.num_seqs + 1) * sizeof(int));
+        return pl;
+    }
+    pl.tc = is16(kv_dtype) && prefill_tc_supported(s.head_dim, s.block_size, contig);
     int rows;
     if (pl.tc) {
         rows = prefill_tc_rows();
@@ -889,6 +910,20 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
     p.tile_tokens = pl.tile_tokens;
     p.nsplit = pl.nsplit;
     p.scale_log2 = scale * kLog2e;
+    if (pl.rows) {
+        p.status = status_word(dev);
+        if (!p.status) return PA_ERR_CUDA;
+        p.heads_per_cta = pl.heads_per_cta;
+        p.tail_info = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.info_off);
+        const bool contig = s.contig_stride > 0, f16 = kv_dtype == PA_F16;
+        const int64_t blocks = contig ? 1 : s.num_blocks;
+        const int64_t tokens = contig ? static_cast<int64_t>(s.num_seqs) * s.contig_stride : s.block_size;
+        CUtensorMap tk, tv;
+        if ((st = make_cache_map(&tk, k_cache, blocks, tokens, s.num_kv_heads, s.head_dim, 16, pl.heads_per_cta, 0, f16)) != PA_OK ||
+            (st = make_cache_map(&tv, v_cache, blocks, tokens, s.num_kv_heads, s.head_dim, 16, pl.heads_per_cta, 0, f16)) != PA_OK)
+            return st;
+        return launch_prefill_rows(p, f16, tk, tv, pl.ctas, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     if (pl.tc) {
         p.status = status_word(dev);
         if (!p.status) return PA_ERR_CUDA;

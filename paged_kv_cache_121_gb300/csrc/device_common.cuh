@@ -186,7 +186,8 @@ struct PrefillParams {
     int nsplit;                   // prefill_simt: pieces a context is cut into; prefill_tc: 2 where the last
                                   //   wave's units may be cut, else 1
     int max_tail;                 // prefill_tc: units the cut wave can have
-    int *tail_info;               // prefill_tc: its layout, written for the merge
+    int *tail_info;               // prefill_tc: its layout, prefill_rows: the tiles' prefix sums, for the merge
+    int heads_per_cta;            // prefill_rows: KV heads (consumer warps) per CTA
     float scale_log2;
 };
 

@@ -93,6 +93,14 @@ int prefill_tc_box_tokens(int block_size, bool contiguous);
 size_t prefill_tc_info_bytes();
 cudaError_t launch_prefill_tc(const PrefillParams &p, bool two_tiles, bool f16, const CUtensorMap &tmap_k,
                               const CUtensorMap &tmap_v, const CUtensorMap &tmap_q, int ctas, cudaStream_t stream);
+// At most 16 rows a KV head (prefill_rows.cu): ctas CTAs per group of
+// p.heads_per_cta KV heads; tmap_k / tmap_v: cache maps of 16 tokens, all halves,
+// heads_per_cta heads. The merge is launched too. Workspace: 2 ctas slots of
+// num_kv_heads x 16 rows, and [num_seqs + 1] prefix sums (p.tail_info).
+constexpr int kPrefillRowsMaxSeqs = 2048;   // the prefix sums live in shared memory
+int prefill_rows_max();
+cudaError_t launch_prefill_rows(const PrefillParams &p, bool f16, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                int ctas, cudaStream_t stream);
 // Arguments of a decode call (mirrors pa_decode, dtypes as pa_dtype values).
 struct DecodeCall {
     void *out;

@@ -151,6 +151,32 @@ def test_large_ragged_batch():
             c.check(c.run(True, ws), True)
 
 
+FEW = [   # query lengths, context lengths, Hq, Hkv, D, block size (0: contiguous)
+    ([1], [1], 8, 8, 64, 16), ([4] * 16, [4164 - 3 * i for i in range(16)], 32, 8, 128, 16),
+    ([3, 0, 1, 2, 0, 3], [3, 9, 0, 1, 40, 700], 20, 4, 128, 32), ([2, 1, 2], [1, 0, 2], 32, 8, 64, 64),
+    ([16, 1, 7], [300, 15, 17], 6, 6, 128, 256), ([1] * 70, [(37 * i) % 900 for i in range(70)], 16, 16, 64, 0),
+    ([4, 2], [1500, 31], 16, 4, 64, 0), ([2] * 200, [(71 * i) % 333 for i in range(200)], 40, 5, 64, 16),
+    ([1, 1], [16, 65536], 32, 8, 128, 16),
+]
+
+
+@pytest.mark.parametrize("case", range(len(FEW)))
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_few_rows(case, dt):
+    """At most 16 rows a KV head: with a workspace the ranges are cut between CTAs, pieces of a sequence joined;
+    causal rows that see nothing of a piece; empty sequences and contexts."""
+    q, ctx, hq, hkv, d, bs = FEW[case]
+    c = Case(q, ctx, hq, hkv, d, bs, dt, seed=40 + case, lead=2, trail=3)
+    for causal in ((True, False) if bs else (False,)):
+        ws = c.workspace()
+        out = c.run(causal, ws)
+        c.check(out, causal)
+        assert torch.equal(c.run(causal, c.workspace(fill=0)), out)
+        c.check(c.run(causal, None), causal)
+        c.check(c.run(causal, ws, out_dtype=torch.float32), causal)
+    assert pa.pa_device_status() == 0
+
+
 @pytest.mark.parametrize("shape", [(186, 1, 700, 4, 8, 64, 128), (77, 4, 2000, 4, 4, 128, 128), (300, 2, 200, 2, 4, 64, 16),
                                    (95, 30, 2000, 1, 2, 128, 64)])
 def test_many_short_pieces_a_cta(shape):
