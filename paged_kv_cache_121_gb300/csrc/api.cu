@@ -761,6 +761,9 @@ constexpr int kPrefillRowsMinHeads = 4;       //   and at least, for that kernel
 // A wave's units are cut between CTAs only below this many waves: above, an idle
 // tail is under a tenth of the work and the pieces' traffic is not worth it.
 constexpr int kPrefillCutWaves = 6;
+// From this many waves CTAs draw units from a counter (a 4-byte memset ahead of the
+// kernel) instead of taking every C-th: ragged units would leave CTAs behind.
+constexpr int kPrefillDrawWaves = 2;
 
 struct PrefillPlan {
     bool rows;                // few rows a KV head: mma.sync, equal tile ranges per CTA
@@ -772,7 +775,8 @@ struct PrefillPlan {
     int ctas;                 // tc: the persistent grid
     int nsplit;               // CUDA-core: pieces of a context; tc: 2 where the last wave may be cut
     int max_tail;             // tc: units the cut wave can have
-    size_t max_off, sum_off, info_off, total;   // workspace: partial outputs, maxima, sums, tail layout
+    bool draw;                // tc: CTAs draw their units from a counter
+    size_t max_off, sum_off, info_off, counter_off, total;   // workspace: partial outputs, maxima, sums, layout
 };
 
 pa_status check_prefill(const PrefillShape &s, pa_dtype out_dtype, pa_dtype q_dtype, pa_dtype kv_dtype, float scale) {
@@ -835,6 +839,8 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
         const int64_t slots = std::min(sms, prefill_tc_max_ctas());
         const bool cut = have_workspace && units < slots * kPrefillCutWaves && s.max_ctx > 2 * prefill_tc_tile();
         pl.ctas = static_cast<int>(cut ? slots : std::min(slots, std::max<int64_t>(units, 1)));
+        pl.draw = have_workspace && units >= slots * kPrefillDrawWaves;
+        if (pl.draw) pl.total = align256(sizeof(int));
         if (!cut) return pl;
         pl.nsplit = 2;
         pl.max_tail = static_cast<int>(std::min(units, slots));
@@ -843,7 +849,8 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
         pl.max_off = align256(pieces * s.head_dim * sizeof(float));
         pl.sum_off = pl.max_off + align256(pieces * sizeof(float));
         pl.info_off = pl.sum_off + align256(pieces * sizeof(float));
-        pl.total = pl.info_off + align256(prefill_tc_info_bytes());
+        pl.counter_off = pl.info_off + align256(prefill_tc_info_bytes());
+        pl.total = pl.counter_off + align256(sizeof(int));
         return pl;
     }
     const int64_t slots = static_cast<int64_t>(sms) * kPrefillSimtCtasPerSm;
@@ -932,6 +939,10 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
         if (std::fabs(p.scale_log2) < FLT_MIN) p.scale_log2 = FLT_MIN;
         p.max_tail = pl.max_tail;
         p.tail_info = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.info_off);
+        if (pl.draw) {
+            p.counter = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.counter_off);
+            if (cudaMemsetAsync(p.counter, 0, sizeof(int), as_stream(stream)) != cudaSuccess) return PA_ERR_CUDA;
+        }
         const bool contig = s.contig_stride > 0, f16 = kv_dtype == PA_F16;
         // contiguous states [B, stride, Hkv, D] are mapped as one block of B * stride tokens
         const int64_t blocks = contig ? 1 : s.num_blocks;
