@@ -820,7 +820,10 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
     if (pl.tc) {
         rows = prefill_tc_rows();
     } else {
-        pl.tall = static_cast<int64_t>(s.max_query) * group > prefill_simt_rows(false);
+        // 64-row tiles where a sequence has more than 16 rows and such tiles fill the SMs
+        const int64_t all_rows = static_cast<int64_t>(s.num_tokens) * group;
+        pl.tall = static_cast<int64_t>(s.max_query) * group > prefill_simt_rows(false) &&
+                  all_rows * s.num_kv_heads >= static_cast<int64_t>(sms) * prefill_simt_rows(true);
         rows = prefill_simt_rows(pl.tall);
     }
     pl.heads_per_tile = std::min(group, rows);

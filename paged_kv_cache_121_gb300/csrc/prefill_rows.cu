@@ -38,12 +38,17 @@ __device__ __forceinline__ int seq_tiles(const PrefillParams &p, const PrefillSe
     return max(1, (prefill_sees(p, s, s.qlen - 1) + kTT - 1) / kTT);
 }
 
-// P[b] = tiles of sequences 0 .. b - 1, P[B] = all of them. All threads.
-__device__ void rows_prefix(const PrefillParams &p, int *P, int *scratch) {
+// P[b] = tiles of sequences 0 .. b - 1, P[B] = all of them, and ctx[b]. All threads.
+__device__ void rows_prefix(const PrefillParams &p, int *P, int *ctx, int *scratch) {
     const int B = p.num_seqs, nt = blockDim.x;
     const int per = (B + nt - 1) / nt, b0 = static_cast<int>(threadIdx.x) * per;
     int sum = 0;
-    for (int b = b0; b < min(B, b0 + per); ++b) sum += seq_tiles(p, prefill_seq(p, b));
+    for (int b = b0; b < min(B, b0 + per); ++b) {
+        const PrefillSeq s = prefill_seq(p, b);
+        ctx[b] = s.ctx;
+        P[b] = seq_tiles(p, s);   // (its count, until the sums are known)
+        sum += P[b];
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = sum;
 #pragma unroll
@@ -56,9 +61,9 @@ __device__ void rows_prefix(const PrefillParams &p, int *P, int *scratch) {
     int run = incl - sum;
     for (int w = 0; w < warp; ++w) run += scratch[w];
     for (int b = b0; b < min(B, b0 + per); ++b) {
+        const int n = P[b];
         P[b] = run;
-        if (per > 1) run += seq_tiles(p, prefill_seq(p, b));
-        else run += sum;
+        run += n;
     }
     if (threadIdx.x == static_cast<unsigned>(nt - 1)) P[B] = run;   // the last thread's running sum is the total
     __syncthreads();
@@ -134,6 +139,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
     const int v_off = stage_bytes / 2;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kRingBytes);   // full[kMaxStages], empty[kMaxStages]
     int *P = reinterpret_cast<int *>(bars + 2 * kMaxStages);            // [num_seqs + 1]
+    int *ctx = P + p.num_seqs + 1;                                      // [num_seqs]
     __shared__ int s_scratch[32];
     __shared__ int s_abort;
     __shared__ int s_issued;
@@ -152,7 +158,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
         mbar_fence_init();
     }
     grid_dependency_wait();
-    rows_prefix(p, P, s_scratch);
+    rows_prefix(p, P, ctx, s_scratch);
     const int W = P[B];
     if (c == 0 && hgrp == 0)   // for the merge
         for (int i = threadIdx.x; i <= B; i += blockDim.x) p.tail_info[i] = P[i];
@@ -172,7 +178,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             off = -1;   // nothing to load
             if (i < ntiles) {
                 const int g = start + i, b = rows_seq_of(P, B, g), tok = (g - P[b]) * kTT;
-                if (tok < prefill_seq(p, b).ctx) {
+                if (tok < ctx[b]) {
                     if (contig) {
                         off = b * p.contig_stride + tok;
                     } else {
@@ -324,11 +330,11 @@ prefill_rows_merge_kernel(const __grid_constant__ PrefillParams p, int ctas) {
     constexpr int E = D / 32;
     const int b = blockIdx.x, lane = threadIdx.x & 31;
     const int w = blockIdx.y * 4 + (threadIdx.x >> 5), kvh = w >> 4, r = w & 15;
+    const PrefillSeq s = prefill_seq(p, b);   // (written before the grid that this one waits for began)
     grid_dependency_wait();
     grid_dependents_launch();
     const int *P = p.tail_info;
     const int pb = P[b], pe = P[b + 1], W = P[p.num_seqs];
-    const PrefillSeq s = prefill_seq(p, b);
     if (pe == pb || kvh >= p.num_kv_heads || r >= s.qlen * p.group) return;
     const int C = min(ctas, W), c0 = rows_owner(pb, W, C), c1 = rows_owner(pe - 1, W, C);
     if (c0 == c1) return;   // held whole: written by its CTA
@@ -377,10 +383,10 @@ cudaError_t launch_rows(const PrefillParams &p, const CUtensorMap &tk, const CUt
     auto kern = prefill_rows_kernel<D, kF16>;
     const size_t fixed = 1024 + kRingBytes + 2 * kMaxStages * sizeof(uint64_t);
     static unsigned long long done = 0;
-    cudaError_t e = ensure_smem_limit(kern, fixed + (kPrefillRowsMaxSeqs + 1) * sizeof(int), done);
+    cudaError_t e = ensure_smem_limit(kern, fixed + (2 * kPrefillRowsMaxSeqs + 1) * sizeof(int), done);
     if (e != cudaSuccess) return e;
     const dim3 grid(ctas, p.num_kv_heads / p.heads_per_cta);
-    e = launch_kernel(kern, grid, dim3(32 * (p.heads_per_cta + 1)), fixed + (p.num_seqs + 1) * sizeof(int), stream, 1u,
+    e = launch_kernel(kern, grid, dim3(32 * (p.heads_per_cta + 1)), fixed + (2 * p.num_seqs + 1) * sizeof(int), stream, 1u,
                       tk, tv, p);
     if (e != cudaSuccess) return e;
     return launch_kernel(prefill_rows_merge_kernel<D>, dim3(p.num_seqs, p.num_kv_heads * 4), dim3(128), 0, stream, 1u, p,

@@ -11,9 +11,11 @@
 // context through shared memory in tiles of 32 tokens, every operand as fp32.
 // 256 threads as 16 x 16: a thread holds RT rows x 2 keys of the scores and RT
 // rows x D / 16 dims of O in registers; the 16 threads of a row sit in one
-// half-warp, so the softmax reductions are shuffles. Bound: the fp32 pipe and
-// the shared-memory loads that feed it. RT = 1 where a sequence has at most 16
-// rows (a few tokens): a taller tile would multiply rows that are not there.
+// half-warp, so the softmax reductions are shuffles. The next tile is fetched
+// while one is computed. Bound: the fp32 pipe and the shared-memory loads that
+// feed it; for small batches latency, so RT = 1 where a sequence has at most 16
+// rows (a taller tile would multiply rows that are not there) or 64-row tiles
+// would not fill the SMs (three prompts of 12 to 47 tokens: 10.3 -> 6.6 us).
 // Contexts are cut into pieces (partials through the workspace, merged after)
 // when there are fewer tiles than CTA slots.
 #include "device_common.cuh"
@@ -83,20 +85,6 @@ prefill_simt_kernel(const __grid_constant__ PrefillParams p) {
     const int nh = min(p.heads_per_tile, p.group - h0);
     const int rows = ntok * nh;                                   // row r: token tok0 + r / nh, head h0 + r % nh
 
-    // the rows' queries, scaled to base-2 scores
-    for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-            const int64_t row = static_cast<int64_t>(s.q0 + tok0 + r / nh) * p.num_heads + kvh * p.group + h0 + r % nh;
-            v = load4(static_cast<const T *>(p.query) + row * D + c);
-            v.x *= p.scale_log2;
-            v.y *= p.scale_log2;
-            v.z *= p.scale_log2;
-            v.w *= p.scale_log2;
-        }
-        *reinterpret_cast<float4 *>(qs + r * C::kStride + c) = v;
-    }
     int sees[RT];
     float m[RT], l[RT];
     float4 o[RT][D / 64];
@@ -117,37 +105,53 @@ prefill_simt_kernel(const __grid_constant__ PrefillParams p) {
 
     const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * D;
     const int lr = tid >> 3, lc = (tid & 7) * 4;                  // this thread's row of the tile, first column
-    for (int t = t_begin; t < t_end; ++t) {
-        __syncthreads();
-        {
-            const int tok = t * kKeys + lr;
-            int64_t at = -1;                                       // row of the cache; -1: not read, zeros
-            if (tok < s.ctx) {
-                if (p.contig_stride > 0) {
-                    at = static_cast<int64_t>(b) * p.contig_stride + tok;
-                } else {
-                    const int blk = p.block_tables[static_cast<int64_t>(b) * p.max_blocks + tok / p.block_size];
-                    if (blk >= 0 && blk < p.num_blocks) at = static_cast<int64_t>(blk) * p.block_size + tok % p.block_size;
-                }
-            }
-            const T *kr = static_cast<const T *>(p.k_cache) + at * row_elems + kvh * D + lc;
-            const T *vr = static_cast<const T *>(p.v_cache) + at * row_elems + kvh * D + lc;
-            float4 kx[D / 32], vx[D / 32];
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                kx[c] = vx[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (at >= 0) {
-                    kx[c] = load4(kr + c * 32);
-                    vx[c] = load4(vr + c * 32);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                *reinterpret_cast<float4 *>(ks + lr * C::kStride + lc + c * 32) = kx[c];
-                *reinterpret_cast<float4 *>(vs + lr * C::kStride + lc + c * 32) = vx[c];
+    float4 kx[D / 32], vx[D / 32];                                // the next tile's, on its way while one is computed
+    auto fetch = [&](int t) {
+        const int tok = t * kKeys + lr;
+        int64_t at = -1;                                           // row of the cache; -1: not read, zeros
+        if (t < t_end && tok < s.ctx) {
+            if (p.contig_stride > 0) {
+                at = static_cast<int64_t>(b) * p.contig_stride + tok;
+            } else {
+                const int blk = p.block_tables[static_cast<int64_t>(b) * p.max_blocks + tok / p.block_size];
+                if (blk >= 0 && blk < p.num_blocks) at = static_cast<int64_t>(blk) * p.block_size + tok % p.block_size;
             }
         }
+        const T *kr = static_cast<const T *>(p.k_cache) + at * row_elems + kvh * D + lc;
+        const T *vr = static_cast<const T *>(p.v_cache) + at * row_elems + kvh * D + lc;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            kx[c] = vx[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at >= 0) {
+                kx[c] = load4(kr + c * 32);
+                vx[c] = load4(vr + c * 32);
+            }
+        }
+    };
+    fetch(t_begin);
+    // the rows' queries, scaled to base-2 scores
+    for (int i = tid; i < C::kRows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            const int64_t row = static_cast<int64_t>(s.q0 + tok0 + r / nh) * p.num_heads + kvh * p.group + h0 + r % nh;
+            v = load4(static_cast<const T *>(p.query) + row * D + c);
+            v.x *= p.scale_log2;
+            v.y *= p.scale_log2;
+            v.z *= p.scale_log2;
+            v.w *= p.scale_log2;
+        }
+        *reinterpret_cast<float4 *>(qs + r * C::kStride + c) = v;
+    }
+    for (int t = t_begin; t < t_end; ++t) {
         __syncthreads();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            *reinterpret_cast<float4 *>(ks + lr * C::kStride + lc + c * 32) = kx[c];
+            *reinterpret_cast<float4 *>(vs + lr * C::kStride + lc + c * 32) = vx[c];
+        }
+        __syncthreads();
+        fetch(t + 1);
         float sc[RT][2];
 #pragma unroll
         for (int i = 0; i < RT; ++i) sc[i][0] = sc[i][1] = 0.f;
