@@ -90,12 +90,11 @@ def _on_current_device(*tensors) -> None:
             raise ValueError("tensors must be on the current CUDA device")
 
 
-def _token_stride(t: torch.Tensor, name: str) -> int:
-    """Token stride of a [tokens, heads, head_dim] view whose heads and dims are contiguous."""
-    T, h, d = t.shape
+def _token_stride(t: torch.Tensor, T: int, h: int, d: int) -> int:
+    """Token stride of a [T, h, d] view whose heads and dims are contiguous."""
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
-        raise ValueError(f"{name}: heads and dims must be contiguous")
+        raise ValueError("heads and dims must be contiguous")
     return st if T > 1 else h * d
 
 
@@ -130,7 +129,7 @@ def pa_rope(out, x, positions, inv_freq, layout=PA_ROPE_HALF, factor=1.0, transp
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and dtype")
     rot = _rope_vectors(positions, inv_freq, T)
-    so, sx = _token_stride(out, "out"), _token_stride(x, "x")
+    so, sx = _token_stride(out, T, h, d), _token_stride(x, T, h, d)
     _on_current_device(out, x, positions, inv_freq)
     _check(_lib.load().pa_rope(out.data_ptr(), so, x.data_ptr(), sx, _ptr(positions), _ptr(inv_freq), T, h, d, rot,
                                layout, factor, bool(transpose), _dtype(x), _stream(stream)), "pa_rope")
@@ -154,8 +153,8 @@ def pa_rope_and_cache(query_out, query, key, value, k_cache, v_cache, slot_mappi
     if not (dt == v_cache.dtype == query.dtype == query_out.dtype == key.dtype == value.dtype):
         raise TypeError("query, key, value and the caches must have one dtype")
     rot = _rope_vectors(positions, inv_freq, T)
-    so, sq = _token_stride(query_out, "query_out"), _token_stride(query, "query")
-    sk, sv = _token_stride(key, "key"), _token_stride(value, "value")
+    so, sq = _token_stride(query_out, T, hq, d), _token_stride(query, T, hq, d)
+    sk, sv = _token_stride(key, T, hkv, d), _token_stride(value, T, hkv, d)
     _on_current_device(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq)
     _check(_lib.load().pa_rope_and_cache(
         query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv, _ptr(k_cache),

@@ -942,10 +942,6 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
         if (std::fabs(p.scale_log2) < FLT_MIN) p.scale_log2 = FLT_MIN;
         p.max_tail = pl.max_tail;
         p.tail_info = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.info_off);
-        if (pl.draw) {
-            p.counter = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.counter_off);
-            if (cudaMemsetAsync(p.counter, 0, sizeof(int), as_stream(stream)) != cudaSuccess) return PA_ERR_CUDA;
-        }
         const bool contig = s.contig_stride > 0, f16 = kv_dtype == PA_F16;
         // contiguous states [B, stride, Hkv, D] are mapped as one block of B * stride tokens
         const int64_t blocks = contig ? 1 : s.num_blocks;
@@ -953,10 +949,15 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
         const int box = prefill_tc_box_tokens(s.block_size, contig);
         CUtensorMap tk, tv, tq;
         if ((st = make_cache_map(&tk, k_cache, blocks, tokens, s.num_kv_heads, s.head_dim, box, 1, 1, f16)) != PA_OK ||
-            (st = make_cache_map(&tv, v_cache, blocks, tokens, s.num_kv_heads, s.head_dim, box, 1, 0, f16)) != PA_OK ||
+            (st = make_cache_map(&tv, v_cache, blocks, tokens, s.num_kv_heads, s.head_dim, box, 1,
+                                 prefill_tc_v_box_halves(s.head_dim, s.block_size, contig), f16)) != PA_OK ||
             (st = make_query_group_map(&tq, query, s.num_tokens, s.num_kv_heads, p.group, s.head_dim,
                                        pl.tall ? pl.tile_tokens / 2 : pl.tile_tokens, f16, pl.heads_per_tile)) != PA_OK)
             return st;
+        if (pl.draw) {
+            p.counter = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.counter_off);
+            if (cudaMemsetAsync(p.counter, 0, sizeof(int), as_stream(stream)) != cudaSuccess) return PA_ERR_CUDA;
+        }
         return launch_prefill_tc(p, pl.tall, f16, tk, tv, tq, pl.ctas, as_stream(stream)) == cudaSuccess ? PA_OK
                                                                                                        : PA_ERR_CUDA;
     }

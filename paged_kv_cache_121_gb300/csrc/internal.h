@@ -82,14 +82,15 @@ cudaError_t launch_rope(RopeParams &p, int type, int sms, cudaStream_t stream);
 int prefill_simt_rows(bool tall);
 cudaError_t launch_prefill_simt(const PrefillParams &p, int kv_type, bool tall, dim3 grid, cudaStream_t stream);
 // Several query tokens a sequence on tcgen05 (prefill_tc.cu), persistent over
-// `ctas` CTAs. tmap_k / tmap_v: cache maps of box_tokens tokens, one half / all
-// halves of one head; tmap_q: the query as make_query_map lays it out. With
+// `ctas` CTAs. tmap_k / tmap_v: cache maps of box_tokens tokens of one head, one half /
+// v_box_halves halves; tmap_q: the query as make_query_map lays it out. With
 // p.nsplit > 1 the merge is launched too.
 bool prefill_tc_supported(int head_dim, int block_size, bool contiguous);
 int prefill_tc_rows();        // rows of a row tile
 int prefill_tc_tile();        // context tokens of a K/V tile
 int prefill_tc_max_ctas();
 int prefill_tc_box_tokens(int block_size, bool contiguous);
+int prefill_tc_v_box_halves(int head_dim, int block_size, bool contiguous);   // halves in one box of V
 size_t prefill_tc_info_bytes();
 cudaError_t launch_prefill_tc(const PrefillParams &p, bool two_tiles, bool f16, const CUtensorMap &tmap_k,
                               const CUtensorMap &tmap_v, const CUtensorMap &tmap_q, int ctas, cudaStream_t stream);

@@ -29,7 +29,7 @@
 //    tensor pipe in issue order.
 //  * warps 9, 10: K tiles, 64 tokens each; warp 11: the schedule, Q and V
 //    tiles. TMA boxes, one per cache block (at most 64 tokens); K one box per
-//    64-dim half, V both halves in one. A thread starts a box every ~50 ns, so
+//    64-dim half, V too where blocks are long, else both halves in one. A thread starts a box every ~50 ns, so
 //    blocks of 16 need three issuing warps.
 //
 // Schedule: whole units, each CTA drawing the next as it goes (with a workspace and
@@ -336,8 +336,9 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
     sc.tail = sc.r = sc.a = sc.e = 0;
     int tail_ctas = 1, tail_tiles = 0;
     const int rem = sc.units % ctas;
-    // a wave that fills nine tenths of the CTAs is as good uncut, without the merge
-    if (p.nsplit > 1 && rem > 0 && rem * 10 < ctas * 9) {
+    // a wave that fills nine tenths of the CTAs is as good uncut, without the merge (and a query_start that
+    // breaks its contract may describe more units than the workspace was sized for)
+    if (p.nsplit > 1 && rem > 0 && rem * 10 < ctas * 9 && rem <= p.max_tail) {
         sc.nfull = sc.units - rem;
         sc.tail = rem;
         // tiles of the tail's row tiles [x_lo, x_hi], lanes over sequences
@@ -481,12 +482,17 @@ __device__ __forceinline__ int block_id(const PrefillParams &p, BlockIds &c, int
     return __shfl_sync(0xffffffffu, c.id, blk - c.first);
 }
 
-template <int D, bool kTwoTiles, bool kF16>
+template <int D, bool kTwoTiles, bool kF16, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ PrefillParams p) {
     using C = Cfg<D, kTwoTiles>;
     constexpr int kSlots = C::kSlots;
+    // V in shared memory. kWide (boxes of 32 tokens or more): [half][token][128 bytes], one box a half. Else
+    // (16 or 8, half as many boxes): boxes of [half][token][128 bytes] one after another. In either the
+    // 16-token steps of the products are a constant apart, which the MMA issue depends on.
+    constexpr int kVBoxHalves = kWide ? 1 : C::kHalves;
+    constexpr int kVStep = kVBoxHalves * 16 * 128;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -612,8 +618,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                             blk = block_id(p, ids, b, tok >> bs_shift, nblk, lane);
                             at = tok & (p.block_size - 1);
                         }
-                        if (elect_one())
-                            tma_load_5d(dst + j * (C::kHalves * R * 128), &tmap_v, 0, at, 0, kvh, blk, land, policy);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int h = 0; h < C::kHalves; h += kVBoxHalves)
+                                tma_load_5d(dst + h * (kTile * 128) + j * (kVBoxHalves * R * 128), &tmap_v, 0, at, h, kvh, blk,
+                                            land, policy);
+                        }
                         __syncwarp();
                     }
                     if (mend) {   // zero the rows past the context; then the tile is full
@@ -622,11 +632,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                             break;
                         }
                         ++lands;
-                        unsigned char *v = ring + slot * C::kSlotBytes;   // boxes of [half][R tokens][128 bytes]
+                        unsigned char *v = ring + slot * C::kSlotBytes;
                         for (int x = lane; x < (kTile - valid) * C::kHalves * 8; x += 32) {
                             const int row = valid + x / (C::kHalves * 8), c = x % (C::kHalves * 8);
-                            *reinterpret_cast<uint4 *>(v + (row >> r_shift) * (C::kHalves * R * 128) + (c / 8) * (R * 128) +
-                                                       (row & (R - 1)) * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            const int at = kWide ? (c / 8) * (kTile * 128) + row * 128
+                                                 : (row >> r_shift) * (C::kHalves * R * 128) + (c / 8) * (R * 128) + (row & (R - 1)) * 128;
+                            *reinterpret_cast<uint4 *>(v + at + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -691,14 +702,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             // ---------------- MMA issue ----------------
             constexpr uint32_t id_qk = idesc_16bit_f32(kM, kTile, false, false, kF16);
             constexpr uint32_t id_pv = idesc_16bit_f32(kM, D, false, true, kF16);
-            // V boxes are [R tokens][128 bytes] per half, boxes of kHalves halves one after another (R a power of two)
-            const int v_box = C::kHalves * R * 128;
-            uint64_t v_off[kTile / 16];          // of the tile's 16-token steps
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-                v_off[kk] = desc_step(R >= 16 ? ((kk * 16) >> r_shift) * v_box + ((kk * 16) & (R - 1)) * 128 : kk * 2 * v_box);
             const uint64_t q_desc = smem_desc_sw128(smem_addr(q_s), 16, 1024), k_desc = smem_desc_sw128(smem_addr(ring), 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), R * 128, R >= 16 ? 1024 : C::kHalves * 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), kWide ? kTile * 128 : R * 128, kWide || R >= 16 ? 1024 : C::kHalves * 1024);
             int fills = 0;                       // ring tiles of the segments before
             int s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};   // a group's tiles; its segments with any
             bool ok = true;
@@ -745,7 +750,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         tc_fence_after();
 #pragma unroll
                         for (int kk = h * 4; kk < h * 4 + 4; ++kk)
-                            tc_mma_16bit_ts(o_col(grp), s_col(grp) + kk * 8, vd + v_off[kk], id_pv,
+                            tc_mma_16bit_ts(o_col(grp), s_col(grp) + kk * 8, vd + desc_step(kk * kVStep), id_pv,
                                             (j > 0 || kk > 0) ? 1u : 0u);
                     }
                     if (j == cnt[grp] - 1) tc_commit(smem_addr(&sh->o_full[grp]));
@@ -1070,10 +1075,10 @@ prefill_tc_merge_kernel(const __grid_constant__ PrefillParams p, int row_tiles) 
     for (int e = 0; e < kMergeCols; e += 2) store_pair_as(p.out, p.out_type, at + e, o[e] * inv, o[e + 1] * inv);
 }
 
-template <int D, bool kTwoTiles, bool kF16>
+template <int D, bool kTwoTiles, bool kF16, bool kWide>
 cudaError_t launch_impl(const PrefillParams &p, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tq,
                         int ctas, cudaStream_t stream) {
-    auto kern = prefill_tc_kernel<D, kTwoTiles, kF16>;
+    auto kern = prefill_tc_kernel<D, kTwoTiles, kF16, kWide>;
     constexpr size_t smem = smem_bytes<D, kTwoTiles>();
     static unsigned long long done = 0;
     cudaError_t e = ensure_smem_limit(kern, smem, done);
@@ -1085,11 +1090,11 @@ cudaError_t launch_impl(const PrefillParams &p, const CUtensorMap &tk, const CUt
                          row_tiles);
 }
 
-template <int D, bool kTwoTiles>
+template <int D, bool kTwoTiles, bool kWide>
 cudaError_t launch_type(const PrefillParams &p, bool f16, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tq, int ctas, cudaStream_t stream) {
-    return f16 ? launch_impl<D, kTwoTiles, true>(p, tk, tv, tq, ctas, stream)
-               : launch_impl<D, kTwoTiles, false>(p, tk, tv, tq, ctas, stream);
+    return f16 ? launch_impl<D, kTwoTiles, true, kWide>(p, tk, tv, tq, ctas, stream)
+               : launch_impl<D, kTwoTiles, false, kWide>(p, tk, tv, tq, ctas, stream);
 }
 
 }  // namespace
@@ -1102,15 +1107,21 @@ int prefill_tc_rows() { return kM; }
 int prefill_tc_tile() { return kTile; }
 int prefill_tc_max_ctas() { return kMaxTail; }
 int prefill_tc_box_tokens(int block_size, bool contiguous) { return contiguous || block_size > 64 ? 64 : block_size; }
+int prefill_tc_v_box_halves(int head_dim, int block_size, bool contiguous) {
+    return prefill_tc_box_tokens(block_size, contiguous) >= 32 ? 1 : head_dim / 64;
+}
 size_t prefill_tc_info_bytes() { return kTailInts * sizeof(int); }
 
 cudaError_t launch_prefill_tc(const PrefillParams &p, bool two_tiles, bool f16, const CUtensorMap &tk,
                               const CUtensorMap &tv, const CUtensorMap &tq, int ctas, cudaStream_t stream) {
-    if (p.head_dim == 128)
-        return two_tiles ? launch_type<128, true>(p, f16, tk, tv, tq, ctas, stream)
-                         : launch_type<128, false>(p, f16, tk, tv, tq, ctas, stream);
-    return two_tiles ? launch_type<64, true>(p, f16, tk, tv, tq, ctas, stream)
-                     : launch_type<64, false>(p, f16, tk, tv, tq, ctas, stream);
+    if (p.head_dim == 64)   // one half: either layout is the wide one
+        return two_tiles ? launch_type<64, true, true>(p, f16, tk, tv, tq, ctas, stream)
+                         : launch_type<64, false, true>(p, f16, tk, tv, tq, ctas, stream);
+    if (prefill_tc_v_box_halves(p.head_dim, p.block_size, p.contig_stride > 0) == 1)
+        return two_tiles ? launch_type<128, true, true>(p, f16, tk, tv, tq, ctas, stream)
+                         : launch_type<128, false, true>(p, f16, tk, tv, tq, ctas, stream);
+    return two_tiles ? launch_type<128, true, false>(p, f16, tk, tv, tq, ctas, stream)
+                     : launch_type<128, false, false>(p, f16, tk, tv, tq, ctas, stream);
 }
 
 }  // namespace pa
