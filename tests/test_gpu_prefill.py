@@ -131,6 +131,23 @@ def test_lengths_past_the_bounds_are_cut():
     assert pa.pa_device_status() == 0
 
 
+def test_query_start_that_overlaps_stays_in_bounds():
+    """Sequences that claim the same tokens again and again: more units than the batch's tokens can hold. The
+    result is unspecified; nothing outside out and the workspace is written."""
+    for hkv, q in ((2, 60), (2, 200), (4, 3)):
+        c = Case([q] + [0] * 79, [700] * 80, 4 * hkv, hkv, 64, 16, "bf16", seed=13)
+        starts = np.zeros(81, np.int32)
+        starts[1::2] = q
+        c.start_d.copy_(torch.from_numpy(starts))
+        need = c.workspace().numel()
+        big = torch.full((need + (32 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+        out = torch.full((q + 64, 4 * hkv, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        c.run(True, big[:need], out=out[:q])
+        torch.cuda.synchronize()
+        assert bool((big[need:] == 0x5A).all()) and bool((out[q:] == 5.0).all())
+    assert pa.pa_device_status() == 0
+
+
 def test_single_tokens_agree_with_decode():
     """Query lengths of one: pa_decode's result."""
     c = Case([1] * 6, [1, 17, 300, 1029, 64, 555], 32, 8, 128, 16, "bf16", seed=14)
