@@ -37,14 +37,14 @@ def _check(status: int, where: str) -> None:
         raise PAError(status, where)
 
 
+_DTYPES = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float16: PA_F16}
+
+
 def _dtype(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return PA_F32
-    if t.dtype == torch.bfloat16:
-        return PA_BF16
-    if t.dtype == torch.float16:
-        return PA_F16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -84,7 +84,7 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None
 
 def _on_current_device(*tensors) -> None:
     """The kernels run on a stream of the current device: every tensor has to live there."""
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else 0
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else 0   # (on the CPU every device id is -1)
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError("tensors must be on the current CUDA device")
@@ -241,24 +241,23 @@ def pa_prefill_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, hea
                                                      block_size, max_query_len, max_context_len, kv_dtype))
 
 
-def _prefill_args(out, query, k, v, lens, query_start, workspace):
+def _prefill_args(out, query, k, v, lens, query_start, workspace, tables):
     """Checks pa_prefill and pa_cross_attention share; returns the workspace's bytes."""
-    T, hq, d = query.shape
     if out.shape != query.shape:
         raise ValueError("out must have query's shape")
-    if k.dim() != 4 or v.shape != k.shape or k.shape[3] != d:
+    if k.dim() != 4 or v.shape != k.shape or k.shape[3] != query.shape[2]:
         raise ValueError("keys and values are [blocks or sequences, tokens, num_kv_heads, head_dim], both alike")
-    if query.dtype != k.dtype or v.dtype != k.dtype:
+    if not (query.dtype == k.dtype == v.dtype):
         raise TypeError("query, keys and values must have one dtype")
     if lens.dtype != torch.int32 or query_start.dtype != torch.int32:
         raise TypeError("lengths and query_start must be int32")
     if lens.dim() != 1 or query_start.shape != (lens.shape[0] + 1,):
         raise ValueError("query_start must be [num_seqs + 1]")
-    _on_current_device(out, query, k, v, lens, query_start)
     if workspace is None:
+        _on_current_device(out, query, k, v, lens, query_start, tables)
         return 0
-    _on_current_device(workspace, out)
-    return workspace.numel() * workspace.element_size()
+    _on_current_device(out, query, k, v, lens, query_start, tables, workspace)
+    return workspace.nbytes
 
 
 def pa_prefill(out, query, k_cache, v_cache, block_tables, context_lens, query_start, max_query_len, max_context_len,
@@ -269,10 +268,9 @@ def pa_prefill(out, query, k_cache, v_cache, block_tables, context_lens, query_s
     its ``context_lens[b]`` tokens. ``causal``: token i sees the context up to
     itself; else all of it. ``workspace``: a uint8 tensor of at least
     :func:`pa_prefill_workspace_size` bytes, or None (contexts are not split)."""
-    ws_bytes = _prefill_args(out, query, k_cache, v_cache, context_lens, query_start, workspace)
     if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != context_lens.shape[0]:
         raise TypeError("block_tables must be int32 [num_seqs, max_blocks]")
-    _on_current_device(block_tables)
+    ws_bytes = _prefill_args(out, query, k_cache, v_cache, context_lens, query_start, workspace, block_tables)
     nb, bs, hkv, d = k_cache.shape
     T, hq, _ = query.shape
     _check(_lib.load().pa_prefill(_ptr(out), _dtype(out), _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache),
@@ -289,7 +287,7 @@ def pa_cross_attention(out, query, k, v, state_lens, query_start, max_query_len,
     ``state_lens[b]`` of an encoder's states ``k``, ``v`` [B, S, Hkv, D], into
     ``out`` [T, Hq, D]. ``workspace`` as for :func:`pa_prefill`, sized with
     block_size 16."""
-    ws_bytes = _prefill_args(out, query, k, v, state_lens, query_start, workspace)
+    ws_bytes = _prefill_args(out, query, k, v, state_lens, query_start, workspace, query_start)
     if k.shape[0] != state_lens.shape[0]:
         raise ValueError("keys and values are [num_seqs, max_states, num_kv_heads, head_dim]")
     n, states, hkv, d = k.shape
