@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libpa.so")
 
 SOURCES = ["api.cu", "decode_mma.cu", "decode_balanced.cu", "prefix_mma.cu", "prefix_tc.cu", "decode_simt.cu", "cache_ops.cu", "rope.cu", "prefill_simt.cu", "prefill_tc.cu", "prefill_rows.cu",
            "decode_static.cu", "health.cu", "block_manager.cpp"]
-HEADERS = ["device_common.cuh", "mma_tile.cuh", "tcgen05.cuh", "internal.h"]
+HEADERS = ["device_common.cuh", "mma_tile.cuh", "tcgen05.cuh", "prompt_common.cuh", "internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -15,6 +15,7 @@
 #include "../../include/pa.h"
 #include "device_common.cuh"
 #include "internal.h"
+#include "prompt_common.cuh"
 
 namespace pa {
 

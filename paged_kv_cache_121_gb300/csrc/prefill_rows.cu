@@ -18,9 +18,9 @@
 // however ragged the batch. A CTA's first and last segment may be pieces of a
 // sequence: they go to the workspace, slots 2 c and 2 c + 1 of CTA c, and the
 // merge joins them; sequences held whole are written by their CTA.
-#include "device_common.cuh"
 #include "internal.h"
 #include "mma_tile.cuh"
+#include "prompt_common.cuh"
 
 namespace pa {
 

@@ -18,8 +18,8 @@
 // would not fill the SMs (three prompts of 12 to 47 tokens: 10.3 -> 6.6 us).
 // Contexts are cut into pieces (partials through the workspace, merged after)
 // when there are fewer tiles than CTA slots.
-#include "device_common.cuh"
 #include "internal.h"
+#include "prompt_common.cuh"
 
 namespace pa {
 

@@ -47,8 +47,8 @@
 // and frees its tensor memory.
 #include <climits>
 
-#include "device_common.cuh"
 #include "internal.h"
+#include "prompt_common.cuh"
 #include "tcgen05.cuh"
 
 namespace pa {

@@ -25,8 +25,8 @@
 // CTA takes fewer heads of a token, so that a step's latency is one item's.
 #include <cmath>
 
-#include "device_common.cuh"
 #include "internal.h"
+#include "prompt_common.cuh"
 
 namespace pa {
 
