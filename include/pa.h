@@ -333,10 +333,14 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
  *                 host-side upper bounds; what lies past them is not attended
  *                 and the rows of a longer query are undefined.
  *   workspace     at least pa_prefill_workspace_size() bytes, 16-byte aligned,
- *                 or NULL / 0 bytes: then no context is split between CTAs,
- *                 which costs time where there are few query tokens. Its
+ *                 or NULL / 0 bytes: then no context is split between CTAs
+ *                 and the tensor-core kernels balance less, which costs time
+ *                 where there are few query tokens or ragged lengths. Its
  *                 contents need no initialisation. Calls that share a
- *                 workspace must not overlap on the GPU.
+ *                 workspace must not overlap on the GPU. The size does not
+ *                 grow with every argument (small batches are cut into pieces,
+ *                 large ones are not): one buffer for several shapes is as
+ *                 large as the largest of their sizes.
  *   Supported: as pa_decode (head_dim 64 or 128, blocks of 1 to 256, q and kv
  *   of one dtype, any out dtype, num_heads a multiple of num_kv_heads).
  *   Scores, softmax statistics and output sums are held in fp32; 16-bit caches

@@ -743,6 +743,11 @@ bool rope_view_ok(const void *ptr, int64_t stride, int heads, int head_dim, pa_d
            stride >= static_cast<int64_t>(heads) * head_dim;
 }
 
+// Rotated in place, a row has to be where it was read from.
+bool rope_in_place_ok(const void *out, int64_t out_stride, const void *x, int64_t x_stride, int num_tokens) {
+    return out != x || out_stride == x_stride || num_tokens == 1;
+}
+
 // ---------------------------------------------------------------------------
 // Several query tokens a sequence: prompts, chunks of prompts, verified drafts
 // (paged, causal or not), and cross attention (contiguous states)
@@ -1477,7 +1482,8 @@ PA_API pa_status pa_rope(void *out, int64_t out_stride, const void *x, int64_t x
     if (num_tokens == 0) return PA_OK;
     if (!out || !x || !positions || !inv_freq) return PA_ERR_INVALID_ARG;
     if (!rope_view_ok(out, out_stride, num_heads, head_dim, dtype) ||
-        !rope_view_ok(x, x_stride, num_heads, head_dim, dtype) || !aligned_to(positions, 4) ||
+        !rope_view_ok(x, x_stride, num_heads, head_dim, dtype) ||
+        !rope_in_place_ok(out, out_stride, x, x_stride, num_tokens) || !aligned_to(positions, 4) ||
         !aligned_to(inv_freq, 8))
         return PA_ERR_INVALID_ARG;
     int dev;
@@ -1518,6 +1524,7 @@ PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, co
         return PA_ERR_INVALID_ARG;
     if (!rope_view_ok(query_out, query_out_stride, num_heads, head_dim, dtype) ||
         !rope_view_ok(query, query_stride, num_heads, head_dim, dtype) ||
+        !rope_in_place_ok(query_out, query_out_stride, query, query_stride, num_tokens) ||
         !rope_view_ok(key, key_stride, num_kv_heads, head_dim, dtype) ||
         !rope_view_ok(value, value_stride, num_kv_heads, head_dim, dtype) || !aligned16(k_cache) ||
         !aligned16(v_cache) || !aligned_to(slot_mapping, 8) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))

@@ -90,6 +90,15 @@ def test_argument_checks_return_before_launch():
     assert append(hkv=1, D=6, rot=6) == pa.PA_ERR_UNSUPPORTED   # a slot is not whole 16-byte vectors
 
 
+def test_in_place_needs_one_stride():
+    """Rows rotated in place but at another stride would overwrite rows that are still to be read."""
+    lib = pa.load_library()
+    P = 4096
+    assert lib.pa_rope(P, 1024, P, 512, P, P, 4, 4, 128, 128, 0, 1.0, 0, 1, None) == pa.PA_ERR_INVALID_ARG
+    assert lib.pa_rope_and_cache(P, 512, P, 768, P, 256, P, 256, P, P, P, P, P, 4, 4, 8, 16, 2, 128, 128, 0, 1.0, 1,
+                                 None) == pa.PA_ERR_INVALID_ARG
+
+
 def test_binding_refuses_mismatched_tensors():
     T, H, D = 4, 2, 64
     x = torch.zeros(T, H, D)
