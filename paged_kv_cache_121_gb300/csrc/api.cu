@@ -767,6 +767,9 @@ constexpr int kPrefillRowsMinHeads = 4;       //   and at least, for that kernel
 // A wave's units are cut between CTAs only below this many waves: above, an idle
 // tail is under a tenth of the work and the pieces' traffic is not worth it.
 constexpr int kPrefillCutWaves = 6;
+// ... and only for contexts of this many tiles, few units (a quarter of the CTAs or fewer) / more: below, the
+// merge's launch (3.3 us) costs more than the shorter wave saves. One row tile: a tile takes about half as long.
+constexpr int kPrefillCutTiles[2][2] = {{24, 48}, {12, 24}};   // [two row tiles][more units]
 // From this many waves CTAs draw units from a counter (a 4-byte memset ahead of the
 // kernel) instead of taking every C-th: ragged units would leave CTAs behind.
 constexpr int kPrefillDrawWaves = 2;
@@ -846,7 +849,8 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
     const int64_t units = pl.tiles * s.num_kv_heads * pl.ntile;
     if (pl.tc) {
         const int64_t slots = std::min(sms, prefill_tc_max_ctas());
-        const bool cut = have_workspace && units < slots * kPrefillCutWaves && s.max_ctx > 2 * prefill_tc_tile();
+        const bool cut = have_workspace && units < slots * kPrefillCutWaves &&
+                         cdiv64(s.max_ctx, prefill_tc_tile()) >= kPrefillCutTiles[pl.tall][units * 4 > slots];
         pl.ctas = static_cast<int>(cut ? slots : std::min(slots, std::max<int64_t>(units, 1)));
         pl.draw = have_workspace && units >= slots * kPrefillDrawWaves;
         if (pl.draw) pl.total = align256(sizeof(int));

@@ -35,8 +35,10 @@
 // Schedule: whole units, each CTA drawing the next as it goes (with a workspace and
 // more than two waves of units; else CTA c takes c, c + C, ...): the CTAs then work
 // on neighbouring units, which share their K and V, at any time. Where the host
-// allows, the units of the last partial wave are cut into equal ranges of tiles over
-// all CTAs, pieces of a unit going to the workspace for the merge kernel. (All units
+// allows, the units of the last partial wave are cut where that pays: into pieces of
+// units, one a CTA, or equal ranges of tiles over all CTAs; pieces of a unit go to the
+// workspace for the merge kernel. (192 units of 64 tiles at head_dim 128: 196 us whole,
+// 157 in pieces, 154 in ranges; 272 units of 12 tiles: 51 whole, 71 in ranges. All units
 // cut into one contiguous range a CTA, measured: 64 ragged chunks 609 us against
 // 450, four 4,100-token prompts 517 against 396: each CTA then streams a K and V of
 // its own, and ranges of many short units take longer.)
@@ -64,9 +66,15 @@ constexpr int kSegs = 3;             // published segments in flight
 constexpr int kSegReaders = 11;      // MMA warp, two K warps, eight softmax warps
 constexpr float kSlack = 8.f;        // base-2 headroom before the running maximum moves
 constexpr int kMaxTail = 160;        // units of a partial wave: fewer than CTAs
-// p.tail_info: units of the cut wave, CTAs that share it, its tiles | prefix sums of the tiles | unit descriptors
-constexpr int kTailPrefix = 3, kTailUnits = kTailPrefix + kMaxTail + 1, kTailInts = kTailUnits + 8 * kMaxTail;
+// p.tail_info: units of the cut wave, then eight ints a unit: first query token, query tokens, KV head, first
+// head, heads, first and last CTA that holds a piece of it
+constexpr int kTailUnits = 8, kTailInts = kTailUnits + 8 * kMaxTail;
 constexpr int kMinPiece = 4;         // tiles a CTA takes of a cut wave, at least
+// What a cut wave's pieces cost (written and read again, up to 128 KB each at head_dim 128), in tiles of its
+// length: one for every so many pieces. Measured over 8 to 352 units of 8 to 128 tiles, both head dims: cuts
+// by this rule run at 0.95 (U 272, 128 tiles) to 4 times (U 8) the speed of uncut waves, most of them above 1.
+template <bool kTwoTiles>
+constexpr int kPiecesPerTile = kTwoTiles ? 10 : 6;
 
 template <int D, bool kTwoTiles>
 struct Cfg {
@@ -323,6 +331,7 @@ __device__ __forceinline__ void sched_chunk(const PrefillParams &p, Scheduler &s
     sc.total = __shfl_sync(0xffffffffu, sum, 31);
 }
 
+template <bool kTwoTiles>
 __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, int lane) {
     const int ys = p.num_kv_heads * p.ntile;
     const int ctas = gridDim.x;
@@ -334,11 +343,9 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
     sc.units = sc.nfull = rows * ys;
     sc.next = blockIdx.x;
     sc.tail = sc.r = sc.a = sc.e = 0;
-    int tail_ctas = 1, tail_tiles = 0;
     const int rem = sc.units % ctas;
-    // a wave that fills nine tenths of the CTAs is as good uncut, without the merge (and a query_start that
-    // breaks its contract may describe more units than the workspace was sized for)
-    if (p.nsplit > 1 && rem > 0 && rem * 10 < ctas * 9 && rem <= p.max_tail) {
+    // (a query_start that breaks its contract may describe more units than the workspace was sized for)
+    if (p.nsplit > 1 && rem > 0 && rem <= p.max_tail) {
         sc.nfull = sc.units - rem;
         sc.tail = rem;
         // tiles of the tail's row tiles [x_lo, x_hi], lanes over sequences
@@ -352,43 +359,96 @@ __device__ void sched_init(const PrefillParams &p, Shared *sh, Scheduler &sc, in
             before += sc.total;
         }
         __syncwarp();
-        // sums over the tail's units, lane l over units [l per, (l + 1) per)
-        const int per = (sc.tail + 31) / 32, skip = sc.nfull - x_lo * ys;
-        int mine = 0;
-        for (int r = lane * per; r < min(sc.tail, (lane + 1) * per); ++r) mine += sh->tail_work[(skip + r) / ys];
-        int sum = mine;
+        // lane l holds units [l per, (l + 1) per): their tiles
+        const int per = (sc.tail + 31) / 32, skip = sc.nfull - x_lo * ys, r0 = lane * per;
+        constexpr int kPer = (kMaxTail + 31) / 32;
+        int w[kPer], mine = 0, most = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
+        for (int i = 0; i < kPer; ++i) {
+            w[i] = i < per && r0 + i < sc.tail ? sh->tail_work[(skip + r0 + i) / ys] : 0;
+            mine += w[i];
+            most = max(most, w[i]);
         }
-        tail_tiles = __shfl_sync(0xffffffffu, sum, 31);
-        tail_ctas = max(1, min(ctas, tail_tiles / kMinPiece));
-        if (static_cast<int>(blockIdx.x) < tail_ctas) {
-            sc.a = range_begin(blockIdx.x, tail_tiles, tail_ctas);
-            sc.e = range_begin(blockIdx.x + 1, tail_tiles, tail_ctas);
+        const int tiles = __reduce_add_sync(0xffffffffu, mine);
+        most = __reduce_max_sync(0xffffffffu, most);
+        // the shortest length to which units can be cut with one piece a CTA
+        auto pieces = [&](int len) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) n += (w[i] + len - 1) / len;
+            return n;
+        };
+        const int even = (tiles + ctas - 1) / ctas;
+        int len = max(even, kMinPiece), hi = max(most, len);       // (the units themselves are at most ctas)
+        while (len < hi) {
+            const int mid = (len + hi) / 2;
+            if (static_cast<int>(__reduce_add_sync(0xffffffffu, pieces(mid))) <= ctas) hi = mid;
+            else len = mid + 1;
         }
-        int at = sum - mine, holds = 0;
-        for (int r = lane * per; r < min(sc.tail, (lane + 1) * per); ++r) {
-            sh->tail_prefix[r] = at;
-            const int end = at + sh->tail_work[(skip + r) / ys];
-            if (at <= sc.a && sc.a < end) holds = r;                // the unit of this CTA's first tile
-            at = end;
+        // tiles saved, less what the pieces cost: units cut into pieces, one a CTA, or equal ranges of tiles that
+        // run across units (shorter, but up to two more pieces a CTA), or neither
+        const int cuts_all = __reduce_add_sync(0xffffffffu, pieces(len));
+        const int by_pieces = most - len - (cuts_all > sc.tail ? cuts_all : 0) / kPiecesPerTile<kTwoTiles>,
+                  by_ranges = most - even - (sc.tail + ctas) / kPiecesPerTile<kTwoTiles>;
+        const bool ranges = by_ranges > by_pieces;
+        if (max(by_ranges, by_pieces) <= 0) {
+            sc.nfull = sc.units;
+            sc.tail = 0;
+        } else {
+            const int tail_ctas = max(1, min(ctas, tiles / kMinPiece)), c = blockIdx.x;
+            if (ranges && c < tail_ctas) {
+                sc.a = range_begin(c, tiles, tail_ctas);
+                sc.e = range_begin(c + 1, tiles, tail_ctas);
+            }
+            const int cuts = pieces(len);
+            int at = mine, first = cuts;                           // tiles, pieces before this lane's units
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, at, d), q = __shfl_up_sync(0xffffffffu, first, d);
+                if (lane >= d) {
+                    at += o;
+                    first += q;
+                }
+            }
+            at -= mine;
+            first -= cuts;
+            int holds = -1, a = 0, e = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (w[i] == 0) continue;
+                const int r = r0 + i, n = (w[i] + len - 1) / len, j = c - first;
+                sh->tail_prefix[r] = at;
+                if (ranges ? at <= sc.a && sc.a < at + w[i] : j >= 0 && j < n) {   // holds this CTA's (first) piece
+                    holds = r;
+                    if (!ranges) {
+                        a = at + range_begin(j, w[i], n);
+                        e = at + range_begin(j + 1, w[i], n);
+                    }
+                }
+                if (c == 0) {                                      // for the merge
+                    int *d = p.tail_info + kTailUnits + r * 8;
+                    d[5] = ranges ? range_owner(at, tiles, tail_ctas) : first;
+                    d[6] = ranges ? range_owner(at + w[i] - 1, tiles, tail_ctas) : first + n - 1;
+                }
+                at += w[i];
+                first += n;
+            }
+            if (lane == 0) sh->tail_prefix[sc.tail] = tiles;
+            const unsigned who = __ballot_sync(0xffffffffu, holds >= 0);
+            if (who) {
+                const int l = __ffs(who) - 1;
+                sc.r = __shfl_sync(0xffffffffu, holds, l);
+                if (!ranges) {
+                    sc.a = __shfl_sync(0xffffffffu, a, l);
+                    sc.e = __shfl_sync(0xffffffffu, e, l);
+                }
+            }
+            __syncwarp();
         }
-        if (lane == 0) sh->tail_prefix[sc.tail] = tail_tiles;
-        sc.r = __reduce_max_sync(0xffffffffu, holds);
-        __syncwarp();
     }
     sc.base = sc.before = 0;
     if (p.num_seqs > 32) sched_chunk(p, sc, lane);
-    if (blockIdx.x == 0 && p.nsplit > 1) {   // for the merge
-        for (int i = lane; i <= sc.tail; i += 32) p.tail_info[kTailPrefix + i] = sc.tail ? sh->tail_prefix[i] : 0;
-        if (lane == 0) {
-            p.tail_info[0] = sc.tail;
-            p.tail_info[1] = tail_ctas;
-            p.tail_info[2] = tail_tiles;
-        }
-    }
+    if (blockIdx.x == 0 && p.nsplit > 1 && lane == 0) p.tail_info[0] = sc.tail;   // for the merge
 }
 
 // The next segment of this CTA into g (lane 0 writes it).
@@ -549,7 +609,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         if (warp == kVWarp) {
             // ---------------- the schedule, Q and V ----------------
             Scheduler sc;
-            sched_init(p, sh, sc, lane);
+            sched_init<kTwoTiles>(p, sh, sc, lane);
             const uint64_t policy = l2_policy_evict_normal(), q_policy = l2_policy_evict_first();
             const int q_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
             // segment k's readers have all begun it before segment k + kSegs takes its place
@@ -1028,20 +1088,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 constexpr int kMergeCols = 16;
 
 __global__ void __launch_bounds__(kM)
-prefill_tc_merge_kernel(const __grid_constant__ PrefillParams p, int row_tiles) {
+prefill_tc_merge_kernel(const __grid_constant__ PrefillParams p, int row_tiles, int ctas) {
     grid_dependency_wait();
     grid_dependents_launch();
     const int r = blockIdx.x, rt = blockIdx.y, c0 = blockIdx.z * kMergeCols, row = threadIdx.x;
     // one round trip for the layout, one for the pieces: every load that may be needed at once
-    const int *info = p.tail_info, *d = info + kTailUnits + r * 8;
-    const int tail = info[0], ctas = info[1], tiles = info[2], p0 = info[kTailPrefix + r], p1 = info[kTailPrefix + r + 1];
-    const int q0 = d[0], ntok = d[1], kvh = d[2], h0 = d[3], nh = d[4];
-    if (r >= tail) return;
-    const int first = range_owner(p0, tiles, ctas), last = range_owner(p1 - 1, tiles, ctas);
-    if (first == last) return;   // taken whole: written by its CTA
+    const int *d = p.tail_info + kTailUnits + r * 8;
+    const int tail = p.tail_info[0], q0 = d[0], ntok = d[1], kvh = d[2], h0 = d[3], nh = d[4], first = d[5], last = d[6];
+    // (first == last: taken whole and written by its CTA; the bounds hold unless a wait of the kernel before ran out)
+    if (r >= tail || first >= last || first < 0 || last >= ctas) return;
     const int row_tokens = p.tile_tokens / row_tiles;
     const int t = row / p.heads_per_tile, h = row - t * p.heads_per_tile, tok = rt * row_tokens + t;
-    if (t >= row_tokens || tok >= ntok || h >= nh) return;
+    if (t >= row_tokens || tok >= ntok || h >= nh || q0 < 0 || q0 + tok >= p.num_tokens || kvh < 0 ||
+        kvh >= p.num_kv_heads || h0 < 0 || h0 + h >= p.group)
+        return;
     float M = -1e30f, l = 0.f, o[kMergeCols];
 #pragma unroll
     for (int e = 0; e < kMergeCols; ++e) o[e] = 0.f;
@@ -1087,7 +1147,7 @@ cudaError_t launch_impl(const PrefillParams &p, const CUtensorMap &tk, const CUt
     if (p.nsplit <= 1) return cudaSuccess;
     const int row_tiles = kTwoTiles ? 2 : 1;
     return launch_kernel(prefill_tc_merge_kernel, dim3(p.max_tail, row_tiles, D / kMergeCols), dim3(kM), 0, stream, 1u, p,
-                         row_tiles);
+                         row_tiles, ctas);
 }
 
 template <int D, bool kTwoTiles, bool kWide>
