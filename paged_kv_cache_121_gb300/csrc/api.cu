@@ -770,8 +770,9 @@ constexpr int kPrefillCutWaves = 6;
 // ... and only for contexts of this many tiles, few units (a quarter of the CTAs or fewer) / more: below, the
 // merge's launch (3.3 us) costs more than the shorter wave saves. One row tile: a tile takes about half as long.
 constexpr int kPrefillCutTiles[2][2] = {{24, 48}, {12, 24}};   // [two row tiles][more units]
-// From this many waves CTAs draw units from a counter (a 4-byte memset ahead of the
-// kernel) instead of taking every C-th: ragged units would leave CTAs behind.
+// From this many waves CTAs draw units from a counter (set to zero by a small kernel
+// ahead, which also orders the sequences) instead of taking every C-th: ragged units
+// would leave CTAs behind.
 constexpr int kPrefillDrawWaves = 2;
 
 struct PrefillPlan {
@@ -853,7 +854,9 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
                          cdiv64(s.max_ctx, prefill_tc_tile()) >= kPrefillCutTiles[pl.tall][units * 4 > slots];
         pl.ctas = static_cast<int>(cut ? slots : std::min(slots, std::max<int64_t>(units, 1)));
         pl.draw = have_workspace && units >= slots * kPrefillDrawWaves;
-        if (pl.draw) pl.total = align256(sizeof(int));
+        // the counter and the order of the sequences
+        const size_t draw_bytes = align256((1 + std::min(s.num_seqs, kPrefillOrderSeqs)) * sizeof(int));
+        if (pl.draw) pl.total = draw_bytes;
         if (!cut) return pl;
         pl.nsplit = 2;
         pl.max_tail = static_cast<int>(std::min(units, slots));
@@ -863,7 +866,7 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
         pl.sum_off = pl.max_off + align256(pieces * sizeof(float));
         pl.info_off = pl.sum_off + align256(pieces * sizeof(float));
         pl.counter_off = pl.info_off + align256(prefill_tc_info_bytes());
-        pl.total = pl.counter_off + align256(sizeof(int));
+        pl.total = pl.counter_off + draw_bytes;
         return pl;
     }
     const int64_t slots = static_cast<int64_t>(sms) * kPrefillSimtCtasPerSm;
@@ -966,7 +969,7 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
             return st;
         if (pl.draw) {
             p.counter = reinterpret_cast<int *>(static_cast<char *>(workspace) + pl.counter_off);
-            if (cudaMemsetAsync(p.counter, 0, sizeof(int), as_stream(stream)) != cudaSuccess) return PA_ERR_CUDA;
+            if (s.num_seqs > 1 && s.num_seqs <= kPrefillOrderSeqs) p.order = p.counter + 1;
         }
         return launch_prefill_tc(p, pl.tall, f16, tk, tv, tq, pl.ctas, as_stream(stream)) == cudaSuccess ? PA_OK
                                                                                                        : PA_ERR_CUDA;

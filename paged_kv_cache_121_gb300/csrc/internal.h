@@ -92,6 +92,7 @@ int prefill_tc_max_ctas();
 int prefill_tc_box_tokens(int block_size, bool contiguous);
 int prefill_tc_v_box_halves(int head_dim, int block_size, bool contiguous);   // halves in one box of V
 size_t prefill_tc_info_bytes();
+constexpr int kPrefillOrderSeqs = 256;      // sequences that are ordered by length, at most, a thread each
 cudaError_t launch_prefill_tc(const PrefillParams &p, bool two_tiles, bool f16, const CUtensorMap &tmap_k,
                               const CUtensorMap &tmap_v, const CUtensorMap &tmap_q, int ctas, cudaStream_t stream);
 // At most 16 rows a KV head (prefill_rows.cu): ctas CTAs per group of

@@ -305,6 +305,7 @@ struct Scheduler {           // (the host keeps the batch's units below 2^31)
     int r;                   // unit of the cut wave that holds tile a
     // 32 sequences at a time, one a lane: its extent, its row tiles and those before it in the chunk
     int base, before, total; // first sequence of the chunk, row tiles before the chunk, row tiles in it
+    int b;                   // this lane's sequence (p.order: longest contexts first)
     PrefillSeq seq;
     int n, excl;
 };
@@ -317,9 +318,12 @@ __device__ __forceinline__ int range_owner(int x, int tiles, int ctas) {
 }
 
 __device__ __forceinline__ void sched_chunk(const PrefillParams &p, Scheduler &sc, int lane) {
-    const int b = sc.base + lane;
+    sc.b = sc.base + lane;
     sc.seq = PrefillSeq{0, 0, 0};
-    if (b < p.num_seqs) sc.seq = prefill_seq(p, b);
+    if (sc.b < p.num_seqs) {
+        if (p.order) sc.b = p.order[sc.b];
+        sc.seq = prefill_seq(p, sc.b);
+    }
     sc.n = (sc.seq.qlen + p.tile_tokens - 1) / p.tile_tokens;
     int sum = sc.n;
 #pragma unroll
@@ -486,13 +490,13 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
     s.q0 = __shfl_sync(0xffffffffu, sc.seq.q0, l);
     s.qlen = __shfl_sync(0xffffffffu, sc.seq.qlen, l);
     s.ctx = __shfl_sync(0xffffffffu, sc.seq.ctx, l);
-    const int ntiles = __shfl_sync(0xffffffffu, sc.n, l);
+    const int ntiles = __shfl_sync(0xffffffffu, sc.n, l), b = __shfl_sync(0xffffffffu, sc.b, l);
     const int from = x - sc.before - __shfl_sync(0xffffffffu, sc.excl, l);
     if (lane != 0) return;
     // within a sequence the last row tile first: the longest work of a causal mask starts first
     const int tile = ntiles - 1 - from, y = u - x * ys;
     const int row_tokens = kTwoTiles ? p.tile_tokens / 2 : p.tile_tokens;
-    g.b = sc.base + l;
+    g.b = b;
     g.tok0 = tile * p.tile_tokens;
     g.q0 = s.q0 + g.tok0;
     g.ntok = min(p.tile_tokens, s.qlen - g.tok0);
@@ -1082,6 +1086,36 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 }
 
 // ---------------------------------------------------------------------------
+// Ahead of a launch whose CTAs draw their units: the counter, and the order in
+// which the sequences' units are drawn, longest contexts first, so that the
+// last ones are short (64 ragged chunks: 436 us in the batch's order, 415 so; at
+// head_dim 64 405 and 365; 1,000 sequences of up to 100 tokens 482 and 499, so
+// only batches of at most kPrefillOrderSeqs are ordered: the CTAs go through the
+// list themselves). One CTA, a thread a sequence, which counts those that go
+// before its own.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPrefillOrderSeqs)
+prefill_order_kernel(const __grid_constant__ PrefillParams p) {
+    __shared__ alignas(16) int tiles[kPrefillOrderSeqs];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int b = threadIdx.x, n = p.num_seqs;
+    int mine = -1;
+    if (b < n) mine = (prefill_seq(p, b).ctx + kTile - 1) / kTile;
+    tiles[b] = mine;
+    __syncthreads();
+    if (b == 0) *p.counter = 0;
+    if (b >= n) return;
+    int rank = 0;
+    for (int j = 0; j < n; j += 4) {   // (the block is whole warps: the entries past n are there, and -1)
+        const int4 t = *reinterpret_cast<const int4 *>(tiles + j);
+        rank += (t.x > mine || (t.x == mine && j < b)) + (t.y > mine || (t.y == mine && j + 1 < b)) +
+                (t.z > mine || (t.z == mine && j + 2 < b)) + (t.w > mine || (t.w == mine && j + 3 < b));
+    }
+    p.order[rank] = b;
+}
+
+// ---------------------------------------------------------------------------
 // The cut wave's pieces joined: one CTA per (unit, row tile, 16 columns), a
 // thread per row; piece weights 2^(m_i - M).
 // ---------------------------------------------------------------------------
@@ -1143,6 +1177,12 @@ cudaError_t launch_impl(const PrefillParams &p, const CUtensorMap &tk, const CUt
     static unsigned long long done = 0;
     cudaError_t e = ensure_smem_limit(kern, smem, done);
     if (e != cudaSuccess) return e;
+    if (p.order) {
+        const int threads = (p.num_seqs + 31) / 32 * 32;
+        if ((e = launch_kernel(prefill_order_kernel, dim3(1), dim3(threads), 0, stream, 1u, p)) != cudaSuccess) return e;
+    } else if (p.counter) {
+        if ((e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream)) != cudaSuccess) return e;
+    }
     if ((e = launch_kernel(kern, dim3(ctas), dim3(kThreads), smem, stream, 1u, tk, tv, tq, p)) != cudaSuccess) return e;
     if (p.nsplit <= 1) return cudaSuccess;
     const int row_tiles = kTwoTiles ? 2 : 1;

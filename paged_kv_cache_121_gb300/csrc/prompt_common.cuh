@@ -51,7 +51,8 @@ struct PrefillParams {
                                   //   wave's units may be cut, else 1
     int max_tail;                 // prefill_tc: units the cut wave can have
     int *tail_info;               // prefill_tc: its layout, prefill_rows: the tiles' prefix sums, for the merge
-    int *counter;                 // prefill_tc: units drawn so far beyond one a CTA (zero at launch), or null
+    int *counter;                 // prefill_tc: units drawn so far beyond one a CTA, or null (set to zero ahead)
+    int *order;                   // prefill_tc: the sequences, longest context first, or null (batch order)
     int heads_per_cta;            // prefill_rows: KV heads (consumer warps) per CTA
     float scale_log2;
 };

@@ -353,3 +353,38 @@ def test_prompt_then_steps_then_cross():
     c = Case([4, 1, 9], [40, 77, 13], hq, hkv, d, 0, "bf16", seed=23)
     c.check(c.run(False, c.workspace()), False)
     assert pa.pa_device_status() == 0
+
+
+WAVES = [   # (query, context) lengths, Hq, Hkv, D, block size (0: contiguous), causal: how the last wave is given out
+    ([256] * 5, [4096, 4000, 3000, 4096, 100], 8, 8, 64, 0, False),         # few units: cut into pieces, one a CTA
+    ([256] * 9, [4096] * 9, 8, 8, 128, 0, False),                          # as many pieces as CTAs, nearly
+    ([200] * 10, [7700 - 300 * i for i in range(10)], 8, 8, 64, 64, True),  # more units than half the CTAs: ranges
+    ([100] * 4, [6200, 6100, 17, 6200], 8, 8, 64, 0, False),               # one row tile a unit
+    ([100] * 10, [130 * 128] * 10, 8, 8, 64, 0, False),                    #   and ranges of them
+    ([256] * 16, [1500] * 16, 8, 8, 64, 0, False),                         # short contexts: not cut
+    ([60, 1, 300] * 11, [60, 700, 2000] * 11, 16, 8, 64, 32, True),        # drawn, longest contexts first
+    ([12] * 300, [12 + (i * 7) % 90 for i in range(300)], 8, 8, 64, 16, True),     # more than are ordered
+    ([12] * 256, [12 + (i * 7) % 90 for i in range(256)], 8, 8, 64, 16, True),     # as many
+]
+
+
+@pytest.mark.parametrize("i", range(len(WAVES)))
+def test_last_wave_and_order(i):
+    """However the units reach the CTAs: right, and the same bits on every run, from any workspace, in a graph."""
+    q, ctx, hq, hkv, d, bs, causal = WAVES[i]
+    c = Case(q, ctx, hq, hkv, d, bs, "bf16", seed=40 + i)
+    ws = c.workspace()
+    got = c.run(causal, ws)
+    c.check(got, causal)
+    assert torch.equal(c.run(causal, c.workspace(fill=0x11)), got)
+    out = torch.full_like(got, 5.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(causal, ws, out=out)
+        c.run(causal, ws, out=out)
+    for _ in range(3):
+        out.fill_(5.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
+    assert pa.pa_device_status() == 0
