@@ -15,7 +15,8 @@
 // while one is computed. Bound: the fp32 pipe and the shared-memory loads that
 // feed it; for small batches latency, so RT = 1 where a sequence has at most 16
 // rows (a taller tile would multiply rows that are not there) or 64-row tiles
-// would not fill the SMs (three prompts of 12 to 47 tokens: 10.3 -> 6.6 us).
+// would not fill the SMs (three prompts of 12 to 47 tokens: 10.3 -> 6.0 us with
+// the tile fetched ahead).
 // Contexts are cut into pieces (partials through the workspace, merged after)
 // when there are fewer tiles than CTA slots.
 #include "internal.h"
