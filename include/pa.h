@@ -317,7 +317,8 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
  * pa_reshape_and_cache wrote them).
  *
  *   query, out    [num_tokens, num_heads, head_dim], the sequences' query
- *                 tokens one sequence after the other
+ *                 tokens one sequence after the other; out must not
+ *                 overlap query or the caches
  *   query_start   [num_seqs + 1] int32, not decreasing: sequence b owns tokens
  *                 query_start[b] .. query_start[b + 1] - 1. Rows before
  *                 query_start[0] or at or past query_start[num_seqs] are left

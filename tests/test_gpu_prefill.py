@@ -388,3 +388,19 @@ def test_last_wave_and_order(i):
         torch.cuda.synchronize()
         assert torch.equal(out, got)
     assert pa.pa_device_status() == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("q, ctx", [([300, 7, 0, 130], [100, 700, 0, 1000]), ([2, 1, 3], [1, 900, 3]), ([70], [40])])
+def test_loose_host_bounds(dt, q, ctx):
+    """max_query_len and max_context_len are upper bounds: far larger ones (another kernel, other tiles, more
+    workspace) give right results too, rows that see nothing among them."""
+    c = Case(q, ctx, 8, 2, 128, 16, dt, seed=60)
+    c.max_q, c.max_ctx = 5000, c.tables.shape[1] * 16
+    for ws in (None, c.workspace()):
+        c.check(c.run(True, ws), True)
+    c = Case(q, ctx, 8, 2, 64, 0, dt, seed=61, max_states=3000)
+    c.max_q, c.max_ctx = 1000, 3000
+    for ws in (None, c.workspace()):
+        c.check(c.run(False, ws), False)
+    assert pa.pa_device_status() == 0
