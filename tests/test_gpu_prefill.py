@@ -404,3 +404,19 @@ def test_loose_host_bounds(dt, q, ctx):
     for ws in (None, c.workspace()):
         c.check(c.run(False, ws), False)
     assert pa.pa_device_status() == 0
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q, ws", [(4, True), (100, False), (300, False), (300, True)])
+def test_output_at_any_16_bytes(out_dtype, q, ws):
+    """out is 16-byte aligned, no more; what lies beside it stays as it was."""
+    c = Case([q, 1, q // 2], [q + 500, 1, q + 2000], 16, 4, 64, 16, "bf16", seed=70)
+    ws = c.workspace() if ws else None
+    want = c.run(True, ws, out_dtype=out_dtype)
+    c.check(want, True)
+    pad = 16 // want.element_size()
+    flat = torch.full((want.numel() + 2 * pad + 64,), 5.0, dtype=out_dtype, device="cuda")
+    out = flat[pad:pad + want.numel()].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    assert torch.equal(c.run(True, ws, out=out), want)
+    assert bool((flat[:pad] == 5.0).all()) and bool((flat[pad + want.numel():] == 5.0).all())
