@@ -34,10 +34,11 @@
 //
 // Bound: the tensor pipe, 76 % busy on long contexts (ncu; the rest is the hand-over
 // between products and softmax, and the start and end of a unit). Measured on
-// GB300, head_dim 128, causal: 2,048 tokens behind 30,720, 64 / 8 heads, 1,237 to
-// 1,295 us by GPU (1,640 - 1,720 TFLOP/s, where cuBLAS sustains 1,697); four prompts
-// of 4,100, 32 / 8 heads, 390 us (1,410); 64 chunks of 1 to 512 behind up to 3,584,
-// 415 us (1,220). The outputs' stores are 5 % of the prompts' time.
+// GB300, head_dim 128, causal: 2,048 tokens behind 30,720, 64 / 8 heads, 1,220 to
+// 1,290 us by GPU (1,650 - 1,750 TFLOP/s, where cuBLAS sustains 1,697); four prompts
+// of 4,100, 32 / 8 heads, 378 us (1,460); 64 chunks of 1 to 512 behind up to 3,584,
+// 408 us (1,240). A tile takes 2,520 cycles (its products 2,048), a change of unit
+// 4,500 to 5,500.
 //
 // Schedule: whole units, each CTA drawing the next as it goes (with a workspace and
 // more than two waves of units; else CTA c takes c, c + C, ...): the CTAs then work
@@ -1112,7 +1113,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 // ---------------------------------------------------------------------------
 // Ahead of a launch whose CTAs draw their units: the counter, and the order in
 // which the sequences' units are drawn, longest contexts first, so that the
-// last ones are short (64 ragged chunks: 436 us in the batch's order, 415 so; at
+// last ones are short (64 ragged chunks: 436 us in the batch's order, 415 so then; at
 // head_dim 64 405 and 365; 1,000 sequences of up to 100 tokens 482 and 499, so
 // only batches of at most kPrefillOrderSeqs are ordered: the CTAs go through the
 // list themselves). One CTA, a thread a sequence, which counts those that go
