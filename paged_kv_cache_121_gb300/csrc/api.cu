@@ -770,8 +770,8 @@ constexpr int kPrefillCutWaves = 6;
 // ... and only for contexts of this many tiles, few units (a quarter of the CTAs or fewer) / more: below, the
 // merge's launch (3.3 us) costs more than the shorter wave saves. One row tile: a tile takes about half as long.
 constexpr int kPrefillCutTiles[2][2] = {{24, 48}, {12, 24}};   // [two row tiles][more units]
-// From this many waves CTAs draw units from a counter (set to zero by a small kernel
-// ahead, which also orders the sequences) instead of taking every C-th: ragged units
+// From this many waves CTAs draw units from a counter (set to zero ahead, by the kernel
+// that orders the sequences or by a memset) instead of taking every C-th: ragged units
 // would leave CTAs behind.
 constexpr int kPrefillDrawWaves = 2;
 
@@ -851,6 +851,7 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
     if (pl.tc) {
         const int64_t slots = std::min(sms, prefill_tc_max_ctas());
         const bool cut = have_workspace && units < slots * kPrefillCutWaves &&
+                         s.max_ctx < (1 << 30) &&   // (a wave's tiles are summed in 32 bits)
                          cdiv64(s.max_ctx, prefill_tc_tile()) >= kPrefillCutTiles[pl.tall][units * 4 > slots];
         pl.ctas = static_cast<int>(cut ? slots : std::min(slots, std::max<int64_t>(units, 1)));
         pl.draw = have_workspace && units >= slots * kPrefillDrawWaves;
@@ -1568,7 +1569,8 @@ PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, co
 
 PA_API size_t pa_prefill_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
                                         int block_size, int max_query_len, int max_context_len, pa_dtype kv_dtype) {
-    const PrefillShape s{num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, INT32_MAX / 256, 1,
+    const int64_t blocks = block_size > 0 ? std::max<int64_t>(cdiv64(max_context_len, block_size), 1) : 1;
+    const PrefillShape s{num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, static_cast<int>(blocks), 1,
                          max_query_len, max_context_len, 0};
     if (check_prefill(s, PA_F32, kv_dtype, kv_dtype, 1.f) != PA_OK || num_seqs == 0 || num_tokens == 0) return 0;
     int dev;

@@ -420,3 +420,9 @@ def test_output_at_any_16_bytes(out_dtype, q, ws):
     assert out.data_ptr() % 32 == 16
     assert torch.equal(c.run(True, ws, out=out), want)
     assert bool((flat[:pad] == 5.0).all()) and bool((flat[pad + want.numel():] == 5.0).all())
+
+
+def test_workspace_size_of_long_contexts():
+    """The size does not depend on how many blocks a context takes: 10 million tokens in blocks of 1 and of 16."""
+    sizes = [pa.pa_prefill_workspace_size(1, 64, 8, 8, 64, bs, 64, 10_000_000, pa.PA_F32) for bs in (1, 16)]
+    assert sizes[0] == sizes[1] > 0
