@@ -36,9 +36,9 @@
 // between products and softmax, and the start and end of a unit). Measured on
 // GB300, head_dim 128, causal: 2,048 tokens behind 30,720, 64 / 8 heads, 1,220 to
 // 1,290 us by GPU (1,650 - 1,750 TFLOP/s, where cuBLAS sustains 1,697); four prompts
-// of 4,100, 32 / 8 heads, 378 us (1,460); 64 chunks of 1 to 512 behind up to 3,584,
-// 408 us (1,240). A tile takes 2,520 cycles (its products 2,048), a change of unit
-// 4,500 to 5,500.
+// of 4,100, 32 / 8 heads, 370 us (1,490); 64 chunks of 1 to 512 behind up to 3,584,
+// 399 us (1,270). A tile takes about 2,500 cycles (its products 2,048), a change of
+// unit 4,500 to 5,500 (both stamped before the last step, which took 2 % off).
 //
 // Schedule: whole units, each CTA drawing the next as it goes (with a workspace and
 // more than two waves of units; else CTA c takes c, c + C, ...): the CTAs then work
