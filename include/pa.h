@@ -542,7 +542,9 @@ PA_API pa_status pa_device_status(int *status, int clear, void *stream);
  * is armed for a copy that is never issued, so the consumer's bounded wait
  * runs out after timeout_us microseconds instead of the kernels' 2 s. The
  * CTA then records PA_ERR_TIMEOUT in the device status word, stops and
- * returns, as a decode kernel would; no copy is ever in flight. Afterwards
+ * returns, as a decode kernel would; no copy is ever in flight. A second wait,
+ * completed after half of the consumer's lanes have given up, checks that a
+ * warp's lanes agree on the outcome (PA_ERR_CUDA if not). Afterwards
  * pa_device_status reports PA_ERR_TIMEOUT (and clears it if asked), and the
  * device stays usable. The status word is shared: do not run this beside
  * decode calls whose status you mean to read. (Not a step of the pages'

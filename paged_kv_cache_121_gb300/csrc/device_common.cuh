@@ -20,7 +20,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s: far above any legal wait
 
 enum DecodeMode : int { kModeFinal = 0, kModeSplitK = 1 };
-enum StatusCode : int { kStatusTimeout = 5 };
+enum StatusCode : int { kStatusTimeout = 5, kStatusCuda = 6 };
 
 // Everything a decode launch needs; passed by value.
 // Two kernels that read nothing of each other's output (the shared-prefix
@@ -260,6 +260,25 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uin
 // The kernels' wait: bounded by kWaitLimitNs.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return mbar_wait_for(bar, parity, kWaitLimitNs);
+}
+
+// The wait of a whole converged warp: the answer is the same in all its lanes.
+// (Lanes that gave up at different times would part, and the others would wait
+// for them without a limit at the warp's next full-mask step.) Past the limit
+// the timeout is recorded and the CTA's abort flag raised; with the flag up
+// nothing is waited for any more.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int *status, int *abort_flag,
+                                               uint64_t limit_ns = kWaitLimitNs) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (!ok && !*reinterpret_cast<volatile int *>(abort_flag)) {
+        ok = mbar_wait_for(bar, parity, limit_ns);
+        if (!ok) {
+            record_status(status, kStatusTimeout);
+            *reinterpret_cast<volatile int *>(abort_flag) = 1;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 // ---------------------------------------------------------------------------

@@ -13,6 +13,11 @@
 // seeing it, stops; the drain's own bounded wait gives up too (it records
 // the same code), and the CTA returns. No copy is in flight at any point,
 // so nothing lands in shared memory after the CTA has gone.
+//
+// The consumer is a whole warp, whose lanes have to agree on the outcome. Half
+// of them are given four times the limit, and the producer completes the phase
+// once the others have given up: had each lane its own answer, the patient ones
+// would go on alone. A warp that does not agree is recorded as PA_ERR_CUDA.
 #include "../../include/pa.h"
 #include "device_common.cuh"
 #include "internal.h"
@@ -22,14 +27,15 @@ namespace pa {
 namespace {
 
 __global__ void __launch_bounds__(64, 1) wait_timeout_check_kernel(int *status, unsigned long long limit_ns) {
-    __shared__ __align__(8) uint64_t bars[2];   // the stage's full and empty barriers
-    __shared__ int s_abort;
+    __shared__ __align__(8) uint64_t bars[3];   // a stage's full and empty barriers; one the warp has to agree on
+    __shared__ int s_abort, s_gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t full = smem_addr(&bars[0]), empty = smem_addr(&bars[1]);
+    const uint32_t full = smem_addr(&bars[0]), empty = smem_addr(&bars[1]), late = smem_addr(&bars[2]);
     if (threadIdx.x == 0) {
         mbar_init(full, 1);
         mbar_init(empty, 1);
-        s_abort = 0;
+        mbar_init(late, 1);
+        s_abort = s_gave_up = 0;
         mbar_fence_init();
     }
     __syncthreads();
@@ -44,14 +50,22 @@ __global__ void __launch_bounds__(64, 1) wait_timeout_check_kernel(int *status, 
                 s_abort = 1;
             }
         }
-    } else if (lane == 0) {
-        // consumer: the decode kernels' wait for a stage to fill
-        if (!mbar_wait_for(full, 0, limit_ns)) {
-            record_status(status, kStatusTimeout);
-            s_abort = 1;
-        } else {
-            mbar_arrive(empty);
+    } else {
+        // consumer: the kernels' wait for a stage to fill
+        if (mbar_wait_warp(full, 0, status, &s_abort, limit_ns) && lane == 0) mbar_arrive(empty);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0) {
+            const uint64_t t0 = global_timer_ns();
+            while (!*reinterpret_cast<volatile int *>(&s_gave_up) && global_timer_ns() - t0 < 2 * limit_ns) {
+            }
+            mbar_arrive(late);   // the phase completes after half of the lanes have given up
         }
+    } else {
+        const bool ok = mbar_wait_warp(late, 0, status, &s_gave_up, lane < 16 ? limit_ns : 4 * limit_ns);
+        const unsigned went_on = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0 && status && went_on != 0u && went_on != 0xffffffffu) atomicExch(status, kStatusCuda);
     }
     __syncthreads();
     // drain: the last phase the producer armed (bounded as well)

@@ -250,8 +250,8 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             const bool whole = P[b] >= start && seg_end <= end;
             rows_epilogue<D>(p, st, s, kvh, whole ? -1 : 2 * c + (start >= P[b] ? 0 : 1), lane);
         };
+        bool ok = true;
         for (int i = 0; i < ntiles; ++i) {
-            if (*reinterpret_cast<volatile int *>(&s_abort)) break;
             const int g = start + i;
             if (!open || g >= seg_end) {
                 if (open) {
@@ -283,11 +283,8 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 }
             }
             const int sg = i % nstages, k = i / nstages;
-            if (!mbar_wait(smem_addr(&bars[sg]), k & 1)) {
-                record_status(p.status, kStatusTimeout);
-                s_abort = 1;
-                break;
-            }
+            ok = mbar_wait_warp(smem_addr(&bars[sg]), k & 1, p.status, &s_abort);
+            if (!ok) break;
             unsigned char *kst = smem + sg * stage_bytes + warp * kHeadStride;   // this head
             const uint32_t kbase = smem_addr(kst);
             const int t0 = (g - P[b]) * kTT, valid = min(kTT, s.ctx - t0);
@@ -307,7 +304,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&bars[kMaxStages + sg]));
         }
-        if (open && !*reinterpret_cast<volatile int *>(&s_abort)) close();
+        if (open && ok) close();
     }
 
     grid_dependents_launch();

@@ -136,19 +136,9 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<128, true>() <= 227 * 1024 && smem_bytes<128, false>() <= 227 * 1024, "shared memory of a CTA");
 
-// A whole warp waits; the answer is the same in all its lanes (a warp whose
-// lanes gave up at different times would part at its next warp-wide step).
+// A whole warp waits.
 __device__ __forceinline__ bool wait_bar(const PrefillParams &p, Shared *sh, uint64_t *bar, uint32_t parity) {
-    bool ok = mbar_try_wait(smem_addr(bar), parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    if (!ok && !*reinterpret_cast<volatile int *>(&sh->abort_flag)) {
-        ok = mbar_wait(smem_addr(bar), parity);
-        if (!ok) {
-            record_status(p.status, kStatusTimeout);
-            *reinterpret_cast<volatile int *>(&sh->abort_flag) = 1;
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
+    return mbar_wait_warp(smem_addr(bar), parity, p.status, &sh->abort_flag);
 }
 
 // The same for a single thread (the MMA issuer inside a segment).
