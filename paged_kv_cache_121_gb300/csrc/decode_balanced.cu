@@ -316,7 +316,6 @@ decode_balanced_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         int len = 0, seg_end = 0;
         bool open = false;
         for (int i = 0; i < ntiles; ++i) {
-            if (*reinterpret_cast<volatile int *>(&s_abort)) break;
             const int g = start + i;
             if (!open || g >= seg_end) {
                 if (open) {   // the previous sequence's segment is done
@@ -347,11 +346,7 @@ decode_balanced_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 }
             }
             const int s = i % nstages, k = i / nstages;
-            if (!mbar_wait(smem_addr(&bars[s]), k & 1)) {
-                record_status(p.status, kStatusTimeout);
-                s_abort = 1;
-                break;
-            }
+            if (!mbar_wait_warp(smem_addr(&bars[s]), k & 1, p.status, &s_abort)) break;
             unsigned char *kst = smem + s * stage_bytes + warp * kHeadStride;   // this head
             const uint32_t kbase = smem_addr(kst);
             const int valid = min(kTT, len - (g - P[b]) * kTT);

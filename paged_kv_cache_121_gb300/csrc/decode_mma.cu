@@ -444,13 +444,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const float sl2 = p.scale_log2;
 
         for (int i = 0; i < ntiles; ++i) {
-            if (*reinterpret_cast<volatile int *>(&s_abort)) break;
             const int s = i % nstages, k = i / nstages;
-            if (!mbar_wait(smem_addr(&bars[s]), k & 1)) {
-                record_status(p.status, kStatusTimeout);
-                s_abort = 1;
-                break;
-            }
+            if (!mbar_wait_warp(smem_addr(&bars[s]), k & 1, p.status, &s_abort)) break;
             unsigned char *kst = smem + s * stage_bytes + warp * kHeadStride;   // this head (rows: its dims)
             const uint32_t kbase = smem_addr(kst);
             const uint32_t vbase = kbase + v_off;

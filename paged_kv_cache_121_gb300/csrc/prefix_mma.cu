@@ -171,13 +171,8 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const float sl2 = p.scale_log2;
 
         for (int i = 0; i < ntiles; ++i) {
-            if (*reinterpret_cast<volatile int *>(&s_abort)) break;
             const int s = i % nstages, k = i / nstages;
-            if (!mbar_wait(smem_addr(&bars[s]), k & 1)) {
-                record_status(p.status, kStatusTimeout);
-                s_abort = 1;
-                break;
-            }
+            if (!mbar_wait_warp(smem_addr(&bars[s]), k & 1, p.status, &s_abort)) break;
             const uint32_t kbase = smem_addr(smem + s * stage_bytes);
             const int t0 = tok_begin + i * TT;
             const int valid0 = min(TT, max(0, len0 - t0)), valid1 = min(TT, max(0, len1 - t0));

@@ -123,12 +123,16 @@ int TcCfg<D, kGroups>::max_ring_bytes() {
 // than the instructions themselves at N = 64.
 __host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
 
+// A single thread's wait, and a whole warp's.
 __device__ __forceinline__ bool tc_wait(const PrefixParams &p, TcBars *bars, uint64_t *bar, uint32_t parity) {
     if (*reinterpret_cast<volatile int *>(&bars->abort_flag)) return false;
     if (mbar_wait(smem_addr(bar), parity)) return true;
     record_status(p.status, kStatusTimeout);
     bars->abort_flag = 1;
     return false;
+}
+__device__ __forceinline__ bool tc_wait_warp(const PrefixParams &p, TcBars *bars, uint64_t *bar, uint32_t parity) {
+    return mbar_wait_warp(smem_addr(bar), parity, p.status, &bars->abort_flag);
 }
 
 // Barrier among the softmax warps only (named barrier 1).
@@ -342,7 +346,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         bool ok = g < ngrp;
         for (int i = 0; i < ntiles && ok; ++i) {
             const int b = i & 1;
-            if (!tc_wait(p, bars, &bars->s_full[g][b], (i >> 1) & 1)) { ok = false; break; }
+            if (!tc_wait_warp(p, bars, &bars->s_full[g][b], (i >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
             float s[kTcTile];
             tmem_ld64(tmem + lane_off + C::s_col(g, b), s);
@@ -397,7 +401,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             if (i >= 1) {
                 // the previous tile's P.V has read the P buffer and landed in O
-                if (!tc_wait(p, bars, &bars->pv_done[g], (i - 1) & 1)) { ok = false; break; }
+                if (!tc_wait_warp(p, bars, &bars->pv_done[g], (i - 1) & 1)) { ok = false; break; }
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, need)) {   // rescale O
 #pragma unroll
@@ -424,10 +428,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         // ---- epilogue: O / l in split form at partition `chunk` ----
         // every row group's last P.V done: P buffers and ring are free for staging
-        if (ok && ntiles > 0 && !tc_wait(p, bars, &bars->pv_done[g], (ntiles - 1) & 1)) ok = false;
+        if (ok && ntiles > 0 && !tc_wait_warp(p, bars, &bars->pv_done[g], (ntiles - 1) & 1)) ok = false;
         softmax_warps_sync(32 * C::kSoftmaxWarps);
         tc_fence_after();
-        if (g < ngrp && !*reinterpret_cast<volatile int *>(&bars->abort_flag)) {
+        const bool aborted = *reinterpret_cast<volatile int *>(&bars->abort_flag) != 0;
+        if (!__any_sync(0xffffffffu, !ok || aborted)) {   // (warp-uniform: the loads below are warp-wide)
             const float inv = l > 0.f ? 1.f / l : 0.f;
             unsigned char *box0 = stage_out + g * C::kOutBytes + R * 128;
 #pragma unroll
