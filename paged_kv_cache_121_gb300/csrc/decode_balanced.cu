@@ -358,6 +358,7 @@ decode_balanced_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         *reinterpret_cast<uint4 *>(kst + v_off + hh * kHalfStride + row * 128 + (e % 8) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                 }
+                fence_proxy_async_smem();   // (a later tile is copied over these rows)
                 __syncwarp();
             }
             warp_tile_attention<D, kTT, true, kF16>(st, qa, kbase, kbase + v_off, kHalfStride, tok_off, valid, valid,

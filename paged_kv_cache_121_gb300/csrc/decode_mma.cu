@@ -351,6 +351,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap tmap_k,
             } else if (live) {
                 for (uint32_t o = 0; o < grp_bytes; o += 16)
                     *reinterpret_cast<uint4 *>(smem + s * stage_bytes + dst_lane + o) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();   // (a later token is copied over the row)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(full);   // after the zeroed rows: the phase covers them

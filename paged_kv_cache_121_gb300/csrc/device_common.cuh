@@ -220,6 +220,12 @@ __device__ __forceinline__ void mbar_fence_init() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// This thread's ordinary accesses to shared memory come before the later ones of the asynchronous
+// proxy (TMA and bulk copies, the tensor cores' reads) that a barrier orders behind this thread.
+__device__ __forceinline__ void fence_proxy_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
