@@ -814,6 +814,7 @@ PrefillPlan plan_prefill(const PrefillShape &s, pa_dtype kv_dtype, int sms, bool
     pl.heads_per_cta = decode_mma_heads_per_cta(s.num_kv_heads, kPrefillRowsHeads);
     pl.rows = is16(kv_dtype) && have_workspace && static_cast<int64_t>(s.max_query) * group <= prefill_rows_max() &&
               pl.heads_per_cta >= kPrefillRowsMinHeads && s.num_seqs <= kPrefillRowsMaxSeqs &&
+              s.num_kv_heads <= kPrefillRowsMaxKvHeads &&
               (contig || (s.block_size >= 16 && pow2)) &&
               static_cast<int64_t>(s.num_seqs) * cdiv64(s.max_ctx, 16) < (int64_t(1) << 30);
     if (pl.rows) {

@@ -100,6 +100,7 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, bool two_tiles, bool f16, 
 // heads_per_cta heads. The merge is launched too. Workspace: 2 ctas slots of
 // num_kv_heads x 16 rows, and [num_seqs + 1] prefix sums (p.tail_info).
 constexpr int kPrefillRowsMaxSeqs = 2048;   // the prefix sums live in shared memory
+constexpr int kPrefillRowsMaxKvHeads = 65535 / 4;   // the merge's grid.y: four rows a CTA, 16 a KV head
 int prefill_rows_max();
 cudaError_t launch_prefill_rows(const PrefillParams &p, bool f16, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                 int ctas, cudaStream_t stream);

@@ -398,7 +398,9 @@ int prefill_rows_max() { return 16; }
 
 cudaError_t launch_prefill_rows(const PrefillParams &p, bool f16, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                                 cudaStream_t stream) {
-    if (p.num_seqs > kPrefillRowsMaxSeqs || p.heads_per_cta < 1 || p.heads_per_cta > kMaxHeads) return cudaErrorInvalidValue;
+    if (p.num_seqs > kPrefillRowsMaxSeqs || p.num_kv_heads > kPrefillRowsMaxKvHeads || p.heads_per_cta < 1 ||
+        p.heads_per_cta > kMaxHeads)
+        return cudaErrorInvalidValue;
     if (p.head_dim == 128)
         return f16 ? launch_rows<128, true>(p, tk, tv, ctas, stream) : launch_rows<128, false>(p, tk, tv, ctas, stream);
     return f16 ? launch_rows<64, true>(p, tk, tv, ctas, stream) : launch_rows<64, false>(p, tk, tv, ctas, stream);
