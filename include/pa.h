@@ -141,8 +141,10 @@ PA_API pa_status pa_rope_frequencies(double *inv_freq, float *factor, int rotary
  *   positions   [num_tokens] int32. A negative position marks padding:
  *               nothing of that token is written.
  *   inv_freq    [rotary_dim / 2] 64-bit, device memory, 8-byte aligned. The
- *               angle is reduced modulo a turn in integers: it is as exact
- *               at position 2^31 - 1 as at position 1.
+ *               angle is reduced modulo a turn in integers, from a frequency
+ *               held to 2^-65 of a turn: at position 2^31 - 1 it is off by
+ *               less than 4e-10 rad before it is rounded to fp32 (for
+ *               frequencies up to one radian a position).
  *   transpose   1: sin negated -- the gradient with respect to x of the
  *               rotation, applied to out's gradient.
  *   rotary_dim even, at most head_dim; head_dim at most 256; all three

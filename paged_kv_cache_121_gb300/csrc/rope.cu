@@ -11,9 +11,10 @@
 // fraction of a full turn (2^64 = one turn), multiplied by the position in
 // integers modulo 2^64 -- the reduction modulo a turn costs nothing and is
 // exact -- and only the reduced angle is rounded to fp32, as half turns, for
-// sincospif. The error is 2^-65 of a turn a position plus one fp32 rounding,
-// whatever the position; an fp32 product position * inv_freq would be off by
-// 0.004 rad at position 65,536 already. No 64-bit floating point runs.
+// sincospif. The fraction is rounded to nearest, so the angle is off by at most
+// 2^-65 of a turn a position (plus 2^-72 a position and radian of inv_freq, from
+// the constant 2 / pi) and one fp32 rounding; an fp32 product position * inv_freq
+// would be off by 0.004 rad at position 65,536 already. No 64-bit floating point runs.
 //
 // Bound: HBM (every element read and written once; a rotation is 6 flops a
 // pair). So: 16-byte vectors; a thread takes the two vectors that hold its
@@ -99,8 +100,9 @@ __device__ __forceinline__ float half_turns(double inv_freq, int position) {
     const int s = 54 - e;
     uint64_t turn = 0;
     if (s >= 128) turn = 0;
-    else if (s >= 64) turn = hi >> (s - 64);
-    else if (s > 0) turn = (hi << (64 - s)) | (lo >> s);
+    else if (s > 64) turn = (hi >> (s - 64)) + ((hi >> (s - 65)) & 1);      // (rounded: the last bit shifted out)
+    else if (s == 64) turn = hi + (lo >> 63);
+    else if (s > 0) turn = ((hi << (64 - s)) | (lo >> s)) + ((lo >> (s - 1)) & 1);
     else if (s > -64) turn = lo << -s;
     uint64_t phase = turn * static_cast<uint64_t>(static_cast<int64_t>(position));
     if (bits >> 63) phase = 0 - phase;
