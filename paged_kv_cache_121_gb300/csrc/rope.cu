@@ -221,7 +221,7 @@ cudaError_t launch_rope_vec(RopeParams &p, int sms, cudaStream_t stream) {
     const int rows = few ? slots : slots * kUnroll;
     p.heads_per_cta = heads < rows ? heads : rows;
     p.tokens_per_cta = rows / p.heads_per_cta;
-    const dim3 grid(static_cast<unsigned>((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta),
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.num_tokens) + p.tokens_per_cta - 1) / p.tokens_per_cta),
                     static_cast<unsigned>((heads + p.heads_per_cta - 1) / p.heads_per_cta));
     const size_t smem = static_cast<size_t>(p.tokens_per_cta) * (p.rotary_dim / 2) * sizeof(float2);
     return p.interleaved ? launch_kernel(rope_kernel<T, V, true>, grid, dim3(threads), smem, stream, 1u, p)
