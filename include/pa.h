@@ -334,7 +334,8 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
  *                 nothing is all zeros.
  *   max_query_len, max_context_len
  *                 host-side upper bounds; what lies past them is not attended
- *                 and the rows of a longer query are undefined.
+ *                 (the causal mask still counts from the context's length as
+ *                 given) and the rows of a longer query are undefined.
  *   workspace     at least pa_prefill_workspace_size() bytes, 16-byte aligned,
  *                 or NULL / 0 bytes: then no context is split between CTAs
  *                 and the tensor-core kernels balance less, which costs time

@@ -104,7 +104,7 @@ struct Cfg {
 struct Seg {
     int b, q0;            // sequence; first query token of the unit (in the batch)
     int tok0, ntok;       // the same within the sequence; query tokens of the unit
-    int ctx, qlen;
+    int ctx, past;        // context tokens; PrefillSeq::past
     int kvh, h0, nh;      // KV head; first query head of its group, heads here
     int t0, n;
     int cnt[2];           // tiles each softmax group takes
@@ -337,7 +337,7 @@ __device__ __forceinline__ int range_owner(int x, int tiles, int ctas) {
 
 __device__ __forceinline__ void sched_chunk(const PrefillParams &p, Scheduler &sc, int lane) {
     sc.b = sc.base + lane;
-    sc.seq = PrefillSeq{0, 0, 0};
+    sc.seq = PrefillSeq{0, 0, 0, 0};
     if (sc.b < p.num_seqs) {
         if (p.order) sc.b = p.order[sc.b];
         sc.seq = prefill_seq(p, sc.b);
@@ -508,6 +508,7 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
     s.q0 = __shfl_sync(0xffffffffu, sc.seq.q0, l);
     s.qlen = __shfl_sync(0xffffffffu, sc.seq.qlen, l);
     s.ctx = __shfl_sync(0xffffffffu, sc.seq.ctx, l);
+    s.past = __shfl_sync(0xffffffffu, sc.seq.past, l);
     const int ntiles = __shfl_sync(0xffffffffu, sc.n, l), b = __shfl_sync(0xffffffffu, sc.b, l);
     const int from = x - sc.before - __shfl_sync(0xffffffffu, sc.excl, l);
     if (lane != 0) return;
@@ -519,7 +520,7 @@ __device__ __forceinline__ void sched_next(const PrefillParams &p, Shared *sh, S
     g.q0 = s.q0 + g.tok0;
     g.ntok = min(p.tile_tokens, s.qlen - g.tok0);
     g.ctx = s.ctx;
-    g.qlen = s.qlen;
+    g.past = s.past;
     g.kvh = y / p.ntile;
     g.h0 = (y - g.kvh * p.ntile) * p.heads_per_tile;
     g.nh = min(p.heads_per_tile, p.group - g.h0);
@@ -934,7 +935,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             const int tok = (kTwoTiles ? grp * row_tokens : 0) + rt;            // query token within the unit
             const bool live = rt < row_tokens && tok < g->ntok && rh < g->nh;
             // rows that are not there need no masking but the context's end: their outputs are never stored
-            const int sees = !live || !p.causal ? g->ctx : max(0, g->ctx - g->qlen + g->tok0 + tok + 1);
+            const int sees = !live || !p.causal ? g->ctx : max(0, min(g->ctx, g->past + g->tok0 + tok + 1));
             const int64_t orow = static_cast<int64_t>(q0 + tok) * p.num_heads + g->kvh * p.group + g->h0 + rh;
             const int other = kTwoTiles ? 0 : g->cnt[grp ^ 1];
             __syncwarp();

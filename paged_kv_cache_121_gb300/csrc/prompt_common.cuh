@@ -62,18 +62,22 @@ struct PrefillParams {
 struct PrefillSeq {
     int q0, qlen;   // first query token, query tokens
     int ctx;        // context tokens
+    int past;       // context tokens ahead of the first query token, of the lengths as given: what the
+                    //   causal mask counts from, wherever the context is cut (negative: leading rows see nothing)
 };
 
 __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams &p, int b) {
     PrefillSeq s;
     s.q0 = p.query_start[b];
-    int64_t n = static_cast<int64_t>(p.query_start[b + 1]) - s.q0;
+    const int64_t given = static_cast<int64_t>(p.query_start[b + 1]) - s.q0;
+    int64_t n = given;
     if (s.q0 < 0 || s.q0 > p.num_tokens) n = 0;
     n = n < p.num_tokens - s.q0 ? n : p.num_tokens - s.q0;
     n = n < p.max_query ? n : p.max_query;
     s.qlen = n > 0 ? static_cast<int>(n) : 0;
     const int64_t cap = p.contig_stride > 0 ? p.contig_stride : static_cast<int64_t>(p.max_blocks) * p.block_size;
     int64_t c = p.context_lens[b];
+    s.past = s.qlen > 0 ? static_cast<int>((c > 0 ? c : 0) - given) : 0;   // (given >= qlen >= 1: fits)
     c = c < cap ? c : cap;
     c = c < p.max_ctx ? c : p.max_ctx;
     s.ctx = c > 0 ? static_cast<int>(c) : 0;
@@ -83,8 +87,8 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams &p, int b)
 // Context tokens that query token i of a sequence sees.
 __device__ __forceinline__ int prefill_sees(const PrefillParams &p, const PrefillSeq &s, int i) {
     if (!p.causal) return s.ctx;
-    const int n = s.ctx - s.qlen + i + 1;
-    return n > 0 ? n : 0;
+    const int n = s.past + i + 1;
+    return n < 0 ? 0 : n < s.ctx ? n : s.ctx;
 }
 
 // Warp-wide: the sequence that owns row tile `x` of the batch (its tiles
