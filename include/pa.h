@@ -349,6 +349,8 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
  *   of one dtype, any out dtype, num_heads a multiple of num_kv_heads).
  *   Scores, softmax statistics and output sums are held in fp32; 16-bit caches
  *   on the tensor cores round the softmax's weights once to the caches' type.
+ *   Scores may have any size below 2^126 / log2(e); a row whose visible scores
+ *   are all minus infinity is all zeros, as one that sees nothing.
  *   A value row that some query rows of a tile do not see has to be finite:
  *   its weight there is zero, and zero times infinity is not. Rows past a
  *   context's length may hold anything.

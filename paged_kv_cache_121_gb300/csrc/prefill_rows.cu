@@ -268,7 +268,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_con
                 sees0 = r < rows ? prefill_sees(p, s, r / p.group) : 0;
                 sees1 = r + 8 < rows ? prefill_sees(p, s, (r + 8) / p.group) : 0;
                 st.init();
-                st.m0 = st.m1 = -1e30f;   // finite: a row may see nothing of its first tiles
+                st.m0 = st.m1 = kLowestScore;   // (a row may see nothing of its first tiles)
                 if (seg_end < end) {      // the next segment's sequence and its query rows, now
                     int nb = b + 1;
                     while (P[nb + 1] <= seg_end) ++nb;
@@ -337,14 +337,14 @@ prefill_rows_merge_kernel(const __grid_constant__ PrefillParams p, int ctas) {
     if (pe == pb || kvh >= p.num_kv_heads || r >= s.qlen * p.group) return;
     const int C = min(ctas, W), c0 = rows_owner(pb, W, C), c1 = rows_owner(pe - 1, W, C);
     if (c0 == c1) return;   // held whole: written by its CTA
-    float M = -1e30f, L = 0.f, acc[E];
+    float M = kLowestScore, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int base = c0; base <= c1; base += 4) {
         float m[4], l[4], o[4][E];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            m[j] = -1e30f;
+            m[j] = kLowestScore;
             l[j] = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[j][e] = 0.f;

@@ -93,7 +93,7 @@ prefill_simt_kernel(const __grid_constant__ PrefillParams p) {
     for (int i = 0; i < RT; ++i) {
         const int r = ty * RT + i;
         sees[i] = r < rows ? prefill_sees(p, s, tok0 + r / nh) : 0;
-        m[i] = -1e30f;   // finite: a row that has seen nothing keeps l = 0 with no inf - inf
+        m[i] = kLowestScore;
         l[i] = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -254,7 +254,7 @@ prefill_simt_merge_kernel(const __grid_constant__ PrefillParams p) {
     if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return;
     const int64_t tok = row / p.num_heads;
     if (tok < p.query_start[0] || tok >= p.query_start[p.num_seqs]) return;
-    float M = -1e30f, l = 0.f;
+    float M = kLowestScore, l = 0.f;
     for (int i = 0; i < p.nsplit; ++i) M = fmaxf(M, p.part_max[row * p.nsplit + i]);
     float o[D / 32];
 #pragma unroll

@@ -73,6 +73,11 @@ constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 11;
 constexpr int kSegs = 3;             // published segments in flight
 constexpr int kSegReaders = 11;      // MMA warp, two K warps, eight softmax warps
 constexpr float kSlack = 8.f;        // base-2 headroom before the running maximum moves
+// Weights are 2^(s * scale - m), the product not rounded, where m is the rounded product of a largest score: its
+// rounding moves all of a row's weights by one factor, which cancels: at most 2^4 up to this size of m. Beyond, the
+// factor would leave fp16's range, but there different fp32 scores are 8 or more apart (in base 2), more so the
+// rounding of their sums: such rows take the scale rounded up to a power of two, whose products are exact.
+constexpr float kHugeScore = 134217728.f;   // 2^27
 constexpr int kMaxTail = 160;        // units of a partial wave: fewer than CTAs
 // p.tail_info: units of the cut wave, then eight ints a unit: first query token, query tokens, KV head, first
 // head, heads, first and last CTA that holds a piece of it
@@ -305,6 +310,11 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) a[e] = best3<kMax>(a[e], s[kTile - 4 + e], a[e]);
     return best3<kMax>(best3<kMax>(a[0], a[1], a[2]), a[3], a[3]);
+}
+
+// The power of two above |x| (x normal), with x's sign.
+__device__ __forceinline__ float power_above(float x) {
+    return 2.f * __uint_as_float(__float_as_uint(x) & 0xff800000u);
 }
 
 // Tiles a unit (row tiles from token tok0 of the sequence) has to visit.
@@ -941,7 +951,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh->seg_empty[k % kSegs]));
             const int whole = __reduce_min_sync(0xffffffffu, sees);             // every row of the warp sees these tokens
-            float m = -1e30f, l = 0.f;   // finite: a row that has seen nothing keeps l = 0 with no inf - inf
+            float m = kLowestScore, l = 0.f;
+            float mul = sl2;             // (see kHugeScore)
             for (int j = 0; j < cnt; ++j) {
                 if (!wait_bar(p, sh, &sh->s_full[grp], s_cnt & 1)) { ok = false; break; }
                 ++s_cnt;
@@ -957,7 +968,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 }
                 uint64_t sum[2] = {0, 0};
                 auto weights = [&](int half) {   // 2^(s * scale - m), two at a time
-                    const uint64_t mul2 = pair(sl2, sl2), neg2 = pair(-m, -m);
+                    const uint64_t mul2 = pair(mul, mul), neg2 = pair(-m, -m);
 #pragma unroll
                     for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
                         uint32_t w[16];
@@ -979,10 +990,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[grp][half]));
                 };
-                const float mx = (up ? row_max<true>(s) : row_max<false>(s)) * sl2;
+                const float top = up ? row_max<true>(s) : row_max<false>(s), mx = top * mul;
                 const bool need = mx > m + kSlack;
                 if (__any_sync(0xffffffffu, need)) {
-                    const float m_new = need ? mx : m, alpha = fast_exp2(m - m_new);
+                    if (need) mul = fabsf(top * sl2) > kHugeScore ? power_above(sl2) : sl2;
+                    const float m_new = need ? top * mul : m, alpha = fast_exp2(m - m_new);
                     m = m_new;
                     l *= alpha;
                     // S of this tile was issued behind the group's previous P V: O is at rest until P appears
@@ -1164,14 +1176,14 @@ prefill_tc_merge_kernel(const __grid_constant__ PrefillParams p, int row_tiles, 
     if (t >= row_tokens || tok >= ntok || h >= nh || q0 < 0 || q0 + tok >= p.num_tokens || kvh < 0 ||
         kvh >= p.num_kv_heads || h0 < 0 || h0 + h >= p.group)
         return;
-    float M = -1e30f, l = 0.f, o[kMergeCols];
+    float M = kLowestScore, l = 0.f, o[kMergeCols];
 #pragma unroll
     for (int e = 0; e < kMergeCols; ++e) o[e] = 0.f;
     for (int c = first; c <= last; c += 2) {   // two pieces at a time, folded into a running maximum
         float m[2], s[2], x[2][kMergeCols];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            m[k] = -1e30f;
+            m[k] = kLowestScore;
             s[k] = 0.f;
             if (c + k > last) continue;
             const int64_t piece = static_cast<int64_t>(c + k + r) * row_tiles + rt;

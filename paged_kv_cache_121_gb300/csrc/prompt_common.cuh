@@ -2,6 +2,8 @@
 // (rope.cu) and several query tokens a sequence (prefill_*.cu).
 #pragma once
 
+#include <cfloat>
+
 #include "device_common.cuh"
 
 namespace pa {
@@ -56,6 +58,11 @@ struct PrefillParams {
     int heads_per_cta;            // prefill_rows: KV heads (consumer warps) per CTA
     float scale_log2;
 };
+
+// Where a row's running maximum starts: finite, so that a row that has seen
+// nothing keeps l = 0 with no inf - inf, and below every finite score but the
+// lowest, which it equals.
+constexpr float kLowestScore = -FLT_MAX;
 
 // One sequence's extent, clamped so that no index leaves its array whatever
 // the device-side lengths hold.
