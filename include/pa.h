@@ -347,10 +347,20 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
  *                 large as the largest of their sizes.
  *   Supported: as pa_decode (head_dim 64 or 128, blocks of 1 to 256, q and kv
  *   of one dtype, any out dtype, num_heads a multiple of num_kv_heads).
- *   Scores, softmax statistics and output sums are held in fp32; 16-bit caches
- *   on the tensor cores round the softmax's weights once to the caches' type.
- *   Scores may have any size below 2^126 / log2(e); a row whose visible scores
- *   are all minus infinity is all zeros, as one that sees nothing.
+ *   Scores, softmax statistics and output sums are held in fp32. What the
+ *   softmax's weights are held in goes by the kernel that the sizes choose:
+ *     fp32               fp32 caches; blocks of 1, 2, 4 or no power of two
+ *     two 16-bit parts   (as in decode) else, with a workspace, where
+ *                        max_query_len x the query heads of a KV head is 16 or
+ *                        less, blocks hold 16 tokens or more (or the states are
+ *                        contiguous), the number of KV heads has a divisor from
+ *                        4 to 8 and there are at most 2,048 sequences
+ *     one 16-bit part    else: rounded once to the caches' type
+ *   So max_query_len and a workspace can change the last bits of a token's
+ *   output, by that rounding.
+ *   Scores may have any size, before and after the scale, below 2^125; a row
+ *   whose visible scores are all minus infinity is all zeros, as one that sees
+ *   nothing.
  *   A value row that some query rows of a tile do not see has to be finite:
  *   its weight there is zero, and zero times infinity is not. Rows past a
  *   context's length may hold anything.
