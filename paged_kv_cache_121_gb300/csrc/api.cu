@@ -764,8 +764,10 @@ constexpr int kPrefillSimtMaxSplits = 16;
 constexpr int kPrefillRowsHeads = 8;          // KV heads of a few-rows CTA, at most
 constexpr int kPrefillRowsMinHeads = 4;       //   and at least, for that kernel to be taken
 
-// A wave's units are cut between CTAs only below this many waves: above, an idle
-// tail is under a tenth of the work and the pieces' traffic is not worth it.
+// A wave's units are cut between CTAs only below this many waves: above, equal
+// units idle for at most a seventh of the time (one unit more than six waves), a
+// last wave that is half full for a fourteenth, and the pieces' traffic and the
+// merge take part of that back. Chosen by this arithmetic, not by a sweep.
 constexpr int kPrefillCutWaves = 6;
 // ... and only for contexts of this many tiles, few units (a quarter of the CTAs or fewer) / more: below, the
 // merge's launch (3.3 us) costs more than the shorter wave saves. One row tile: a tile takes about half as long.

@@ -8,8 +8,8 @@
 // warp's registers; padded to the 128 rows of a tcgen05 tile they would make a
 // chain of waits a tile instead. Measured on GB300, prefill_tc against this with
 // its merge: 16 sequences x 4 tokens over 4,164-token contexts, 32 / 8 heads of
-// 128, 57.8 -> 52.7 us (274 MB: 5.2 TB/s, 0.77 of the copy rate); 64 single tokens
-// over 200-1,500 states, 16 heads of 64, 63.6 -> 43.5 (212 MB: 4.9 TB/s).
+// 128, 57.8 -> 52.5 us (274 MB: 5.2 TB/s, 0.77 of the copy rate); 64 single tokens
+// over 200-1,500 states, 16 heads of 64, 63.6 -> 42 (212 MB: 5.0 TB/s, 0.74).
 //
 // A CTA (one per SM) holds up to 8 KV heads, a consumer warp each, and a
 // producer warp that streams 16-token tiles of all of them, one TMA box of K

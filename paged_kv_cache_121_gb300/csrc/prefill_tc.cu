@@ -32,13 +32,17 @@
 //    64-dim half, V too where blocks are long, else both halves in one. A thread
 //    starts a box every ~50 ns, so blocks of 16 need three issuing warps.
 //
-// Bound: the tensor pipe, 76 % busy on long contexts (ncu; the rest is the hand-over
+// Bound: the tensor pipe, 79 % busy on long contexts (ncu; the rest is the hand-over
 // between products and softmax, and the start and end of a unit). Measured on
-// GB300, head_dim 128, causal: 2,048 tokens behind 30,720, 64 / 8 heads, 1,220 to
-// 1,290 us by GPU (1,650 - 1,750 TFLOP/s, where cuBLAS sustains 1,697); four prompts
-// of 4,100, 32 / 8 heads, 370 us (1,490); 64 chunks of 1 to 512 behind up to 3,584,
-// 399 us (1,270). A tile takes about 2,500 cycles (its products 2,048), a change of
-// unit 4,500 to 5,500 (both stamped before the last step, which took 2 % off).
+// GB300, head_dim 128, causal, in a loop of calls on alternating inputs / as the
+// best of a few short CUDA graphs: 2,048 tokens behind 30,720, 64 / 8 heads, 1,354 /
+// 1,230 us (1,573 / 1,730 TFLOP/s, where cuBLAS sustains 1,697); four prompts of
+// 4,100, 32 / 8 heads, 403 / 375 us (1,368 / 1,470); 64 chunks of 1 to 512 behind up
+// to 3,584, 439 / 407 us (1,152 / 1,243). The two differ by the clock under the power
+// limit. A tile takes about 2,500 cycles (its products 2,048), a change of unit 4,500
+// to 5,500 (stamped before the epilogue's last step). At head_dim 64 neither the
+// tensor pipe nor the exponential unit is above 47 %: a tile is paced by a group's
+// chain of product, load, maximum, weights, product.
 //
 // Schedule: whole units, each CTA drawing the next as it goes (with a workspace and
 // more than two waves of units; else CTA c takes c, c + C, ...): the CTAs then work
