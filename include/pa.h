@@ -164,6 +164,8 @@ PA_API pa_status pa_rope(void *out, int64_t out_stride, const void *x, int64_t x
  *   slot_mapping      as pa_reshape_and_cache; a token whose slot is negative
  *                     or past the pool has its query rotated all the same,
  *                     one whose position is negative is skipped whole.
+ *                     The slots written are distinct: of tokens that share
+ *                     one, any mix of their rows may remain.
  *   Requires (num_kv_heads * head_dim * element size) % 16 == 0. */
 PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
                                    int64_t query_stride, const void *key, int64_t key_stride, const void *value,
