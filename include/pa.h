@@ -337,7 +337,10 @@ PA_API pa_status pa_decode_append(void *out, pa_dtype out_dtype, const void *que
  *   max_query_len, max_context_len
  *                 host-side upper bounds; what lies past them is not attended
  *                 (the causal mask still counts from the context's length as
- *                 given) and the rows of a longer query are undefined.
+ *                 given) and the rows of a longer query are undefined. A
+ *                 tile of queries has to pass a context in less than the 2 s
+ *                 that the kernels' waits are bounded by: up to some 60
+ *                 million tokens.
  *   workspace     at least pa_prefill_workspace_size() bytes, 16-byte aligned,
  *                 or NULL / 0 bytes: then no context is split between CTAs
  *                 and the tensor-core kernels balance less, which costs time
