@@ -175,6 +175,56 @@ PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, co
                                    pa_rope_layout layout, float factor, pa_dtype dtype, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Heads normed by their root mean square before they are rotated, as models
+ * that norm queries and keys head by head do: a head x of every token becomes
+ *     R(weight * x / sqrt(mean(x^2) + eps)),
+ * mean over its head_dim dims, R the rotation of pa_rope.
+ *   weight        [head_dim], of x's type: one scale for all heads of the call
+ *   eps           not negative
+ *   everything else as pa_rope (in place, strided rows, padding); squares,
+ *   sums and products in fp32, one rounding. num_tokens == 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+PA_API pa_status pa_norm_rope(void *out, int64_t out_stride, const void *x, int64_t x_stride, const void *weight,
+                              float eps, const int32_t *positions, const double *inv_freq, int num_tokens,
+                              int num_heads, int head_dim, int rotary_dim, pa_rope_layout layout, float factor,
+                              pa_dtype dtype, void *stream);
+
+/* Its gradients: from grad_out, the gradient of out, that of x and that of
+ * weight. The norms are computed again from x.
+ *   grad_x        as x, rows grad_x_stride elements apart; may be x or
+ *                 grad_out itself (same stride), else apart from both. Rows
+ *                 of padding tokens (negative positions) are left as they
+ *                 were, and those tokens add nothing to grad_weight.
+ *   grad_weight   [head_dim] fp32, overwritten: the sum over all tokens and
+ *                 heads, in an order that depends on the sizes and the
+ *                 device alone (the same call gives the same bits).
+ *                 num_tokens == 0 leaves zeros.
+ *   workspace     at least pa_norm_rope_backward_workspace_size() bytes,
+ *                 16-byte aligned; its contents need no initialisation. Calls
+ *                 that share a workspace must not overlap on the GPU. */
+PA_API size_t pa_norm_rope_backward_workspace_size(int num_tokens, int num_heads, int head_dim);
+
+PA_API pa_status pa_norm_rope_backward(void *grad_x, int64_t grad_x_stride, float *grad_weight, const void *grad_out,
+                                       int64_t grad_out_stride, const void *x, int64_t x_stride, const void *weight,
+                                       float eps, const int32_t *positions, const double *inv_freq, int num_tokens,
+                                       int num_heads, int head_dim, int rotary_dim, pa_rope_layout layout,
+                                       float factor, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* pa_rope_and_cache with the norms on the way, in one launch: queries normed
+ * by query_weight and keys by key_weight, then rotated; values are copied as
+ * they are. Same result as pa_norm_rope on query and key followed by
+ * pa_reshape_and_cache. Arguments as pa_rope_and_cache and pa_norm_rope. */
+PA_API pa_status pa_norm_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
+                                        int64_t query_stride, const void *key, int64_t key_stride, const void *value,
+                                        int64_t value_stride, const void *query_weight, const void *key_weight,
+                                        float eps, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                        const int32_t *positions, const double *inv_freq, int num_tokens,
+                                        int num_heads, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                        int rotary_dim, pa_rope_layout layout, float factor, pa_dtype dtype,
+                                        void *stream);
+
+/* ------------------------------------------------------------------------
  * Copy-on-write block copy ("copy_blocks").
  * [P1] "Copy-on-write: when two requests share a prefix" (clone the one block
  * being written); [P3] procedure step 6 and "Across GPUs" (the block copies

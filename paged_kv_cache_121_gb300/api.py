@@ -135,10 +135,8 @@ def pa_rope(out, x, positions, inv_freq, layout=PA_ROPE_HALF, factor=1.0, transp
                                layout, factor, bool(transpose), _dtype(x), _stream(stream)), "pa_rope")
 
 
-def pa_rope_and_cache(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
-                      layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
-    """:func:`pa_rope` on ``query`` [T, Hq, D] into ``query_out`` and on ``key`` [T, Hkv, D] into slot
-    slot_mapping[i] (int64) of the caches, ``value`` copied beside it, in one launch."""
+def _append_args(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq, *weights):
+    """Checks the two appends share; returns (the strided rows' arguments, the sizes)."""
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError("caches are [num_blocks, block_size, num_kv_heads, head_dim], both alike")
     nb, bs, hkv, d = k_cache.shape
@@ -155,11 +153,78 @@ def pa_rope_and_cache(query_out, query, key, value, k_cache, v_cache, slot_mappi
     rot = _rope_vectors(positions, inv_freq, T)
     so, sq = _token_stride(query_out, T, hq, d), _token_stride(query, T, hq, d)
     sk, sv = _token_stride(key, T, hkv, d), _token_stride(value, T, hkv, d)
-    _on_current_device(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq)
+    _on_current_device(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq, *weights)
+    return ((query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv),
+            (T, hq, nb, bs, hkv, d, rot))
+
+
+def pa_rope_and_cache(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                      layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
+    """:func:`pa_rope` on ``query`` [T, Hq, D] into ``query_out`` and on ``key`` [T, Hkv, D] into slot
+    slot_mapping[i] (int64) of the caches, ``value`` copied beside it, in one launch."""
+    rows, sizes = _append_args(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq)
     _check(_lib.load().pa_rope_and_cache(
-        query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(), sv, _ptr(k_cache),
-        _ptr(v_cache), _ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), T, hq, nb, bs, hkv, d, rot, layout, factor,
+        *rows, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), _ptr(positions), _ptr(inv_freq), *sizes, layout, factor,
         _dtype(k_cache), _stream(stream)), "pa_rope_and_cache")
+
+
+def _norm_weight(weight, d: int, dtype) -> None:
+    if weight.dtype != dtype or weight.shape != (d,):
+        raise TypeError("the norm's weight must be [head_dim], of the heads' dtype")
+
+
+def pa_norm_rope(out, x, weight, eps, positions, inv_freq, layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
+    """:func:`pa_rope` on the heads of ``x`` [T, H, D] normed first: each divided by the root of its mean
+    square plus ``eps`` and multiplied by ``weight`` [D] (x's dtype). ``out`` may be ``x``."""
+    T, h, d = x.shape
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    _norm_weight(weight, d, x.dtype)
+    rot = _rope_vectors(positions, inv_freq, T)
+    so, sx = _token_stride(out, T, h, d), _token_stride(x, T, h, d)
+    _on_current_device(out, x, weight, positions, inv_freq)
+    _check(_lib.load().pa_norm_rope(out.data_ptr(), so, x.data_ptr(), sx, _ptr(weight), eps, _ptr(positions),
+                                    _ptr(inv_freq), T, h, d, rot, layout, factor, _dtype(x), _stream(stream)),
+           "pa_norm_rope")
+
+
+def pa_norm_rope_backward_workspace_size(num_tokens, num_heads, head_dim) -> int:
+    return int(_lib.load().pa_norm_rope_backward_workspace_size(num_tokens, num_heads, head_dim))
+
+
+def pa_norm_rope_backward(grad_x, grad_weight, grad_out, x, weight, eps, positions, inv_freq, workspace,
+                          layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
+    """The gradients of :func:`pa_norm_rope`: ``grad_x`` [T, H, D] (may be ``x`` or ``grad_out``) and
+    ``grad_weight`` [D] float32, overwritten, from ``grad_out`` and the forward's arguments. The token rows
+    of grad_x, grad_out and x may be strided. ``workspace``: a uint8 tensor of at least
+    :func:`pa_norm_rope_backward_workspace_size` bytes."""
+    T, h, d = x.shape
+    if not (grad_x.shape == grad_out.shape == x.shape) or not (grad_x.dtype == grad_out.dtype == x.dtype):
+        raise ValueError("grad_x and grad_out must have x's shape and dtype")
+    _norm_weight(weight, d, x.dtype)
+    if grad_weight.dtype != torch.float32 or grad_weight.shape != (d,):
+        raise TypeError("grad_weight must be float32 [head_dim]")
+    rot = _rope_vectors(positions, inv_freq, T)
+    sg, so, sx = (_token_stride(t, T, h, d) for t in (grad_x, grad_out, x))
+    _on_current_device(grad_x, grad_weight, grad_out, x, weight, positions, inv_freq, workspace)
+    _check(_lib.load().pa_norm_rope_backward(
+        grad_x.data_ptr(), sg, _ptr(grad_weight), grad_out.data_ptr(), so, x.data_ptr(), sx, _ptr(weight), eps,
+        _ptr(positions), _ptr(inv_freq), T, h, d, rot, layout, factor, _dtype(x), _ptr(workspace), workspace.nbytes,
+        _stream(stream)), "pa_norm_rope_backward")
+
+
+def pa_norm_rope_and_cache(query_out, query, key, value, query_weight, key_weight, eps, k_cache, v_cache, slot_mapping,
+                           positions, inv_freq, layout=PA_ROPE_HALF, factor=1.0, stream=None) -> None:
+    """:func:`pa_rope_and_cache` with queries and keys normed on the way (:func:`pa_norm_rope`, by
+    ``query_weight`` and ``key_weight`` [D]), in one launch."""
+    rows, sizes = _append_args(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                               query_weight, key_weight)
+    for w in (query_weight, key_weight):
+        _norm_weight(w, sizes[5], k_cache.dtype)
+    _check(_lib.load().pa_norm_rope_and_cache(
+        *rows, _ptr(query_weight), _ptr(key_weight), eps, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+        _ptr(positions), _ptr(inv_freq), *sizes, layout, factor, _dtype(k_cache), _stream(stream)),
+        "pa_norm_rope_and_cache")
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:

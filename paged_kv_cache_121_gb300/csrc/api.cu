@@ -16,6 +16,7 @@
 #include "device_common.cuh"
 #include "internal.h"
 #include "prompt_common.cuh"
+#include "rope_common.cuh"
 
 namespace pa {
 
@@ -747,6 +748,58 @@ bool rope_view_ok(const void *ptr, int64_t stride, int heads, int head_dim, pa_d
 bool rope_in_place_ok(const void *out, int64_t out_stride, const void *x, int64_t x_stride, int num_tokens) {
     return out != x || out_stride == x_stride || num_tokens == 1;
 }
+
+// The checks and arguments of the two appends (rotated; normed and rotated). p comes zeroed.
+pa_status append_params(RopeParams &p, int *sms, void *query_out, int64_t query_out_stride, const void *query,
+                        int64_t query_stride, const void *key, int64_t key_stride, const void *value,
+                        int64_t value_stride, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                        const int32_t *positions, const double *inv_freq, int num_tokens, int num_heads,
+                        int num_blocks, int block_size, int num_kv_heads, int head_dim, int rotary_dim,
+                        pa_rope_layout layout, float factor, pa_dtype dtype) {
+    pa_status st = check_rope(num_tokens, num_heads, head_dim, rotary_dim, layout, factor, dtype);
+    if (st != PA_OK) return st;
+    if (num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
+    if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if ((static_cast<int64_t>(num_kv_heads) * head_dim * element_bytes(dtype)) % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PA_OK;
+    if (!query_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq)
+        return PA_ERR_INVALID_ARG;
+    if (!rope_view_ok(query_out, query_out_stride, num_heads, head_dim, dtype) ||
+        !rope_view_ok(query, query_stride, num_heads, head_dim, dtype) ||
+        !rope_in_place_ok(query_out, query_out_stride, query, query_stride, num_tokens) ||
+        !rope_view_ok(key, key_stride, num_kv_heads, head_dim, dtype) ||
+        !rope_view_ok(value, value_stride, num_kv_heads, head_dim, dtype) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned_to(slot_mapping, 8) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))
+        return PA_ERR_INVALID_ARG;
+    int dev;
+    if ((st = current_device(&dev)) != PA_OK) return st;
+    *sms = sm_count(dev);
+    if (*sms <= 0) return PA_ERR_CUDA;
+    p.x = query;
+    p.out = query_out;
+    p.key = key;
+    p.value = value;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.x_stride = query_stride;
+    p.out_stride = query_out_stride;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = layout == PA_ROPE_INTERLEAVED;
+    p.factor = factor;
+    return PA_OK;
+}
+
+bool valid_eps(float eps) { return std::isfinite(eps) && eps >= 0.f; }
 
 // ---------------------------------------------------------------------------
 // Several query tokens a sequence: prompts, chunks of prompts, verified drafts
@@ -1525,49 +1578,134 @@ PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, co
                                    const int32_t *positions, const double *inv_freq, int num_tokens, int num_heads,
                                    int num_blocks, int block_size, int num_kv_heads, int head_dim, int rotary_dim,
                                    pa_rope_layout layout, float factor, pa_dtype dtype, void *stream) {
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    int sms;
+    const pa_status st = append_params(p, &sms, query_out, query_out_stride, query, query_stride, key, key_stride, value,
+                                       value_stride, k_cache, v_cache, slot_mapping, positions, inv_freq, num_tokens,
+                                       num_heads, num_blocks, block_size, num_kv_heads, head_dim, rotary_dim, layout,
+                                       factor, dtype);
+    if (st != PA_OK || num_tokens == 0) return st;
+    return launch_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_norm_rope(void *out, int64_t out_stride, const void *x, int64_t x_stride, const void *weight,
+                              float eps, const int32_t *positions, const double *inv_freq, int num_tokens,
+                              int num_heads, int head_dim, int rotary_dim, pa_rope_layout layout, float factor,
+                              pa_dtype dtype, void *stream) {
     pa_status st = check_rope(num_tokens, num_heads, head_dim, rotary_dim, layout, factor, dtype);
     if (st != PA_OK) return st;
-    if (num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
-    if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
-    if ((static_cast<int64_t>(num_kv_heads) * head_dim * element_bytes(dtype)) % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (!valid_eps(eps)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
-    if (!query_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq)
-        return PA_ERR_INVALID_ARG;
-    if (!rope_view_ok(query_out, query_out_stride, num_heads, head_dim, dtype) ||
-        !rope_view_ok(query, query_stride, num_heads, head_dim, dtype) ||
-        !rope_in_place_ok(query_out, query_out_stride, query, query_stride, num_tokens) ||
-        !rope_view_ok(key, key_stride, num_kv_heads, head_dim, dtype) ||
-        !rope_view_ok(value, value_stride, num_kv_heads, head_dim, dtype) || !aligned16(k_cache) ||
-        !aligned16(v_cache) || !aligned_to(slot_mapping, 8) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))
+    if (!out || !x || !weight || !positions || !inv_freq) return PA_ERR_INVALID_ARG;
+    if (!rope_view_ok(out, out_stride, num_heads, head_dim, dtype) ||
+        !rope_view_ok(x, x_stride, num_heads, head_dim, dtype) ||
+        !rope_in_place_ok(out, out_stride, x, x_stride, num_tokens) || !rope_view_ok(weight, head_dim, 1, head_dim, dtype) ||
+        !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))
         return PA_ERR_INVALID_ARG;
     int dev;
     if ((st = current_device(&dev)) != PA_OK) return st;
     const int sms = sm_count(dev);
     if (sms <= 0) return PA_ERR_CUDA;
-    RopeParams p;
+    NormRopeParams p;
     std::memset(&p, 0, sizeof p);
-    p.x = query;
-    p.out = query_out;
-    p.key = key;
-    p.value = value;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
-    p.slot_mapping = slot_mapping;
+    p.x = x;
+    p.out = out;
+    p.x_stride = x_stride;
+    p.out_stride = out_stride;
+    p.weight = weight;
+    p.eps = eps;
     p.positions = positions;
     p.inv_freq = inv_freq;
-    p.x_stride = query_stride;
-    p.out_stride = query_out_stride;
-    p.key_stride = key_stride;
-    p.value_stride = value_stride;
-    p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
     p.num_tokens = num_tokens;
     p.num_heads = num_heads;
-    p.num_kv_heads = num_kv_heads;
     p.head_dim = head_dim;
     p.rotary_dim = rotary_dim;
     p.interleaved = layout == PA_ROPE_INTERLEAVED;
     p.factor = factor;
-    return launch_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_norm_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_norm_rope_backward_workspace_size(int num_tokens, int num_heads, int head_dim) {
+    int dev;
+    if (num_tokens <= 0 || num_heads <= 0 || head_dim <= 0 || head_dim > kRopeMaxHeadDim || current_device(&dev) != PA_OK)
+        return 0;
+    const int sms = sm_count(dev);
+    return sms > 0 ? norm_rope_grad_workspace(head_dim, sms) : 0;
+}
+
+PA_API pa_status pa_norm_rope_backward(void *grad_x, int64_t grad_x_stride, float *grad_weight, const void *grad_out,
+                                       int64_t grad_out_stride, const void *x, int64_t x_stride, const void *weight,
+                                       float eps, const int32_t *positions, const double *inv_freq, int num_tokens,
+                                       int num_heads, int head_dim, int rotary_dim, pa_rope_layout layout,
+                                       float factor, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                                       void *stream) {
+    pa_status st = check_rope(num_tokens, num_heads, head_dim, rotary_dim, layout, factor, dtype);
+    if (st != PA_OK) return st;
+    if (!valid_eps(eps) || !grad_weight || !aligned_to(grad_weight, 4)) return PA_ERR_INVALID_ARG;
+    if (num_tokens > 0) {
+        if (!grad_x || !grad_out || !x || !weight || !positions || !inv_freq) return PA_ERR_INVALID_ARG;
+        if (!rope_view_ok(grad_x, grad_x_stride, num_heads, head_dim, dtype) ||
+            !rope_view_ok(grad_out, grad_out_stride, num_heads, head_dim, dtype) ||
+            !rope_view_ok(x, x_stride, num_heads, head_dim, dtype) ||
+            !rope_in_place_ok(grad_x, grad_x_stride, x, x_stride, num_tokens) ||
+            !rope_in_place_ok(grad_x, grad_x_stride, grad_out, grad_out_stride, num_tokens) ||
+            !rope_view_ok(weight, head_dim, 1, head_dim, dtype) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))
+            return PA_ERR_INVALID_ARG;
+    }
+    int dev;
+    if ((st = current_device(&dev)) != PA_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return PA_ERR_CUDA;
+    if (num_tokens > 0 && (!workspace || workspace_bytes < norm_rope_grad_workspace(head_dim, sms) || !aligned16(workspace)))
+        return PA_ERR_WORKSPACE;
+    NormRopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = x;
+    p.out = grad_x;
+    p.grad_out = grad_out;
+    p.x_stride = x_stride;
+    p.out_stride = grad_x_stride;
+    p.grad_out_stride = grad_out_stride;
+    p.grad_weight = grad_weight;
+    p.partials = static_cast<float *>(workspace);
+    p.weight = weight;
+    p.eps = eps;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.head_dim = head_dim;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = layout == PA_ROPE_INTERLEAVED;
+    p.factor = factor;
+    return launch_norm_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_norm_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
+                                        int64_t query_stride, const void *key, int64_t key_stride, const void *value,
+                                        int64_t value_stride, const void *query_weight, const void *key_weight,
+                                        float eps, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                        const int32_t *positions, const double *inv_freq, int num_tokens,
+                                        int num_heads, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                        int rotary_dim, pa_rope_layout layout, float factor, pa_dtype dtype,
+                                        void *stream) {
+    NormRopeParams p;
+    std::memset(&p, 0, sizeof p);
+    if (!valid_eps(eps)) return PA_ERR_INVALID_ARG;
+    if (num_tokens > 0 && (!query_weight || !key_weight || !rope_view_ok(query_weight, head_dim, 1, head_dim, dtype) ||
+                           !rope_view_ok(key_weight, head_dim, 1, head_dim, dtype)))
+        return PA_ERR_INVALID_ARG;
+    int sms;
+    const pa_status st = append_params(p, &sms, query_out, query_out_stride, query, query_stride, key, key_stride, value,
+                                       value_stride, k_cache, v_cache, slot_mapping, positions, inv_freq, num_tokens,
+                                       num_heads, num_blocks, block_size, num_kv_heads, head_dim, rotary_dim, layout,
+                                       factor, dtype);
+    if (st != PA_OK || num_tokens == 0) return st;
+    p.weight = query_weight;
+    p.key_weight = key_weight;
+    p.eps = eps;
+    return launch_norm_rope(p, static_cast<int>(dtype), sms, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API size_t pa_prefill_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,

@@ -10,6 +10,7 @@ namespace pa {
 struct DecodeParams;
 struct PrefixParams;
 struct RopeParams;
+struct NormRopeParams;
 struct PrefillParams;
 
 bool decode_mma_supported(int head_dim, int block_size);   // D 64/128, blocks of 1..256 (powers of two)
@@ -76,6 +77,9 @@ cudaError_t launch_reshape_and_cache(const void *key, const void *value, void *k
                                      int64_t num_slots, int row_bytes, cudaStream_t stream);
 // Rotary positions (rope.cu); `type` as kv_type. Sets p's launch fields.
 cudaError_t launch_rope(RopeParams &p, int type, int sms, cudaStream_t stream);
+// Heads normed and rotated, or (grad_out given) the gradients (norm_rope.cu)
+size_t norm_rope_grad_workspace(int head_dim, int sms);
+cudaError_t launch_norm_rope(NormRopeParams &p, int type, int sms, cudaStream_t stream);
 // Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid
 // (row tiles of the batch, Hkv * ntile, nsplit); `tall`: 64-row tiles, else 16.
 // With nsplit > 1 the merge is launched too.
