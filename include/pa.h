@@ -433,6 +433,97 @@ PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa
                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * A cache of bounded length: attention weights, and eviction by them.
+ *
+ * weights [num_seqs, num_kv_heads, weights_stride] fp32 holds what the cached
+ * tokens weighed so far: entry t of a row belongs to position t of that
+ * sequence's context, summed over the query heads that read the KV head. Row
+ * b goes with row b of block_tables. Both calls below do, for t < context,
+ *     weights[t] = decay * weights[t] + (what this call's rows gave token t),
+ * a row's softmax weights adding up to 1; the entries of the tokens that this
+ * call's queries belong to (the context's last ones) start from zero, so no
+ * entry needs initialisation, and with decay 0 the old ones are not read.
+ * Entries at or past the context are left as they were. decay is finite and
+ * not negative. Statistics and sums are fp32 and no atomics add them: the
+ * same call gives the same bits.
+ * ---------------------------------------------------------------------- */
+
+/* pa_decode, and the weights of its rows: one query token a sequence, the
+ * context's last. A sequence of length 0 gets a row of zeros in out and keeps
+ * its weights.
+ *   weights_stride  elements, at least max_context_len
+ *   workspace       at least pa_decode_weights_workspace_size() bytes, 16-byte
+ *                   aligned (the rows' scores); its contents need no
+ *                   initialisation. Calls that share a workspace must not
+ *                   overlap on the GPU.
+ *   everything else as pa_decode; any block size from 1 to 256. */
+PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                               int block_size, int max_context_len);
+
+PA_API pa_status pa_decode_weights(void *out, pa_dtype out_dtype, float *weights, int64_t weights_stride,
+                                   const void *query, pa_dtype q_dtype, const void *k_cache, const void *v_cache,
+                                   pa_dtype kv_dtype, const int32_t *block_tables, const int32_t *context_lens,
+                                   int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int num_blocks, int max_context_len, float scale,
+                                   float decay, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The weights that several query tokens a sequence give the cached tokens
+ * (pa_prefill computes their outputs): the context's last ones, causal, token i
+ * of n sees the first context - n + i + 1 tokens.
+ *   query, query_start, context_lens, max_query_len, max_context_len
+ *               as pa_prefill. A sequence without query tokens keeps its
+ *               weights, decay or not.
+ *   window      0: every query token counts; else only the last `window` of each
+ *               sequence's do (the entries of all its query tokens start from
+ *               zero all the same)
+ *   workspace   at least pa_prefill_weights_workspace_size() bytes, 16-byte
+ *               aligned (the rows' statistics), as above
+ *   Supported: as pa_decode_weights. */
+PA_API size_t pa_prefill_weights_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                                int head_dim, int block_size, int max_query_len,
+                                                int max_context_len, int window);
+
+PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, const void *query, pa_dtype q_dtype,
+                                    const void *k_cache, pa_dtype kv_dtype, const int32_t *block_tables,
+                                    const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                    int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, int num_blocks, int max_query_len, int max_context_len,
+                                    float scale, float decay, int window, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Eviction: of sequence b's context, each KV head keeps min(keep_lens[b],
+ * context) tokens -- the last num_recent, the first num_sinks (fewer where the
+ * two do not fit together: the last ones go first), and of the others those
+ * with the largest weights (equal ones: the lowest positions; NaN counts as
+ * minus infinity). In the order of their positions they become tokens 0, 1, ..
+ * of the blocks that new_tables lists, keys and values as they were (rotated
+ * keys keep their rotation), and the heads of one place may come from different
+ * tokens. The context is then min(keep_lens[b], context) tokens long, and
+ * decode goes on with new_tables.
+ *   weights       as above, at least max_context_len a row
+ *   new_weights   [num_seqs, num_kv_heads, new_weights_stride] fp32: the kept
+ *                 tokens' weights, in their new order; must not overlap weights
+ *   kept          [num_seqs, num_kv_heads, kept_stride] int32: the positions
+ *                 that the kept tokens had. Entries past a sequence's new length
+ *                 are left as they were, here and in new_weights.
+ *   new_tables    [num_seqs, max_new_blocks] int32: blocks of the same pool. None
+ *                 may be a block that this call reads or lists twice; the old
+ *                 blocks are not written, so ones that other sequences share
+ *                 stay right (pa_bm_compact hands out such blocks).
+ *   keep_lens     [num_seqs] int32; at most kept_stride, new_weights_stride and
+ *                 max_new_blocks * block_size (longer ones are cut). Negative:
+ *                 the sequence is left alone.
+ *   Any head_dim whose rows are whole 16-byte vectors, any block size, all three
+ *   dtypes. Rows whose old or new block lies outside the pool are not moved.
+ *   Two launches, no workspace (kept passes between them). */
+PA_API pa_status pa_evict(int32_t *kept, int64_t kept_stride, float *new_weights, int64_t new_weights_stride,
+                          const float *weights, int64_t weights_stride, void *k_cache, void *v_cache,
+                          pa_dtype kv_dtype, const int32_t *block_tables, const int32_t *context_lens,
+                          const int32_t *new_tables, const int32_t *keep_lens, int num_seqs, int num_kv_heads,
+                          int head_dim, int block_size, int max_blocks_per_seq, int max_new_blocks, int num_blocks,
+                          int max_context_len, int num_sinks, int num_recent, void *stream);
+
+/* ------------------------------------------------------------------------
  * Cross attention: every query token of a sequence over all of an encoder's
  * states, whose count is unrelated to the query's. The states are contiguous,
  * as the encoder's projection leaves them; for states kept in pages call
@@ -689,6 +780,18 @@ PA_API pa_status pa_bm_append_slot(pa_bm *bm, int64_t seq, int64_t *slot, int64_
 /* `child` starts as a copy of `parent`: same table and token count, one more
  * reference on each block. */
 PA_API pa_status pa_bm_fork(pa_bm *bm, int64_t parent, int64_t child);
+
+/* Room for a compacted copy of `seq` (pa_evict): takes cdiv(num_tokens,
+ * block_size) fresh blocks, which become the sequence's table (written to
+ * new_table[0..cap), its length to *n) and num_tokens its token count, and drops
+ * one reference on each of its old blocks, those reaching zero returning to the
+ * front of the free queue in block-table order. Fresh ones are taken before old
+ * ones are released, so the two never meet in one call; the caller moves the data
+ * before the released blocks are written again, and reads the old table
+ * (pa_bm_block_table) ahead of this call. num_tokens is at most the sequence's
+ * (PA_ERR_INVALID_ARG); PA_ERR_OUT_OF_BLOCKS, a short cap (*n is still set) and a
+ * swapped-out sequence (PA_ERR_INVALID_ARG) leave the manager unchanged. */
+PA_API pa_status pa_bm_compact(pa_bm *bm, int64_t seq, int num_tokens, int32_t *new_table, int cap, int *n);
 
 /* Drops one reference on each of the sequence's blocks; blocks reaching zero
  * return to the front of the free queue, in block-table order. */

@@ -345,6 +345,108 @@ def pa_prefill(out, query, k_cache, v_cache, block_tables, context_lens, query_s
            "pa_prefill")
 
 
+def _weights_table(t, num_seqs: int, num_kv_heads: int, at_least: int, name: str) -> int:
+    """Row stride of a [num_seqs, num_kv_heads, S] fp32 table of weights, S at least `at_least`."""
+    if t.dtype != torch.float32 or t.dim() != 3:
+        raise TypeError(f"{name} must be float32 [num_seqs, num_kv_heads, tokens]")
+    if t.shape[0] != num_seqs or t.shape[1] != num_kv_heads or t.shape[2] < at_least:
+        raise ValueError(f"{name} must be [num_seqs, num_kv_heads, tokens], with room for max_context_len")
+    return t.shape[2]
+
+
+def _paged_args(tables, lens, k_cache) -> None:
+    if tables.dtype != torch.int32 or tables.dim() != 2 or lens.dtype != torch.int32 or lens.shape != (tables.shape[0],):
+        raise TypeError("block_tables must be int32 [num_seqs, max_blocks], lengths int32 [num_seqs]")
+    if k_cache.dim() != 4:
+        raise ValueError("caches are [num_blocks, block_size, num_kv_heads, head_dim]")
+
+
+def pa_decode_weights_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len) -> int:
+    return int(_lib.load().pa_decode_weights_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                            max_context_len))
+
+
+def pa_decode_weights(out, weights, query, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
+                      workspace, decay=1.0, stream=None) -> None:
+    """:func:`pa_decode` into ``out`` [B, Hq, D], and the weight its rows gave each cached token: ``weights``
+    [B, Hkv, S] float32 (S at least max_context_len; entry t belongs to position t) becomes ``decay`` times
+    itself plus the softmax weights summed over the query heads of each KV head; the newest token's entry
+    starts from zero. ``workspace``: a uint8 tensor of at least :func:`pa_decode_weights_workspace_size` bytes."""
+    _paged_args(block_tables, context_lens, k_cache)
+    nb, bs, hkv, d = k_cache.shape
+    B, hq, _ = query.shape
+    if out.shape != query.shape or query.shape[2] != d or v_cache.shape != k_cache.shape:
+        raise ValueError("query and out are [num_seqs, num_heads, head_dim], both caches alike")
+    if not (query.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("query and caches must have one dtype")
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables must have a row for each query")
+    stride = _weights_table(weights, B, hkv, max_context_len, "weights")
+    _on_current_device(out, weights, query, k_cache, v_cache, block_tables, context_lens, workspace)
+    _check(_lib.load().pa_decode_weights(
+        _ptr(out), _dtype(out), _ptr(weights), stride, _ptr(query), _dtype(query), _ptr(k_cache), _ptr(v_cache),
+        _dtype(k_cache), _ptr(block_tables), _ptr(context_lens), B, hq, hkv, d, bs, block_tables.shape[1], nb,
+        max_context_len, scale, decay, _ptr(workspace), workspace.nbytes, _stream(stream)), "pa_decode_weights")
+
+
+def pa_prefill_weights_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                                      max_context_len, window=0) -> int:
+    return int(_lib.load().pa_prefill_weights_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                                             block_size, max_query_len, max_context_len, window))
+
+
+def pa_prefill_weights(weights, query, k_cache, block_tables, context_lens, query_start, max_query_len, max_context_len,
+                       scale, workspace, decay=0.0, window=0, stream=None) -> None:
+    """The weights that several query tokens a sequence give the cached tokens, into ``weights`` [B, Hkv, S] as
+    :func:`pa_decode_weights` does: tokens ``query_start[b]`` to ``query_start[b + 1]`` of ``query`` [T, Hq, D]
+    are the last of sequence b's ``context_lens[b]`` tokens, each seeing the context up to itself. ``window``: only
+    the last so many of each sequence count (0: all). ``workspace``: a uint8 tensor of at least
+    :func:`pa_prefill_weights_workspace_size` bytes."""
+    _paged_args(block_tables, context_lens, k_cache)
+    nb, bs, hkv, d = k_cache.shape
+    T, hq, dq = query.shape
+    B = context_lens.shape[0]
+    if dq != d:
+        raise ValueError("query must be [num_tokens, num_heads, head_dim]")
+    if query.dtype != k_cache.dtype:
+        raise TypeError("query and cache must have one dtype")
+    if query_start.dtype != torch.int32 or query_start.shape != (B + 1,):
+        raise TypeError("query_start must be int32 [num_seqs + 1]")
+    stride = _weights_table(weights, B, hkv, max_context_len, "weights")
+    _on_current_device(weights, query, k_cache, block_tables, context_lens, query_start, workspace)
+    _check(_lib.load().pa_prefill_weights(
+        _ptr(weights), stride, _ptr(query), _dtype(query), _ptr(k_cache), _dtype(k_cache), _ptr(block_tables),
+        _ptr(context_lens), _ptr(query_start), B, T, hq, hkv, d, bs, block_tables.shape[1], nb, max_query_len,
+        max_context_len, scale, decay, window, _ptr(workspace), workspace.nbytes, _stream(stream)),
+        "pa_prefill_weights")
+
+
+def pa_evict(kept, new_weights, weights, k_cache, v_cache, block_tables, context_lens, new_tables, keep_lens,
+             max_context_len, sinks=0, recent=0, stream=None) -> None:
+    """Keep ``keep_lens[b]`` (int32 [B], negative: leave the sequence alone) tokens of each sequence and KV head:
+    the last ``recent``, the first ``sinks`` and those with the largest ``weights`` [B, Hkv, S]; in the order of
+    their positions they move to the blocks that ``new_tables`` [B, max_new_blocks] (int32) lists, blocks that
+    nothing else in the call reads or writes. ``kept`` [B, Hkv, K] int32 gets the positions they had,
+    ``new_weights`` [B, Hkv, S'] float32 their weights."""
+    _paged_args(block_tables, context_lens, k_cache)
+    _paged_args(new_tables, keep_lens, k_cache)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("both caches must be alike")
+    nb, bs, hkv, d = k_cache.shape
+    B = context_lens.shape[0]
+    if new_tables.shape[0] != B:
+        raise ValueError("new_tables must have a row for each sequence")
+    if kept.dtype != torch.int32 or kept.dim() != 3 or kept.shape[:2] != (B, hkv):
+        raise TypeError("kept must be int32 [num_seqs, num_kv_heads, tokens]")
+    stride = _weights_table(weights, B, hkv, max_context_len, "weights")
+    new_stride = _weights_table(new_weights, B, hkv, 0, "new_weights")
+    _on_current_device(kept, new_weights, weights, k_cache, v_cache, block_tables, context_lens, new_tables, keep_lens)
+    _check(_lib.load().pa_evict(
+        _ptr(kept), kept.shape[2], _ptr(new_weights), new_stride, _ptr(weights), stride, _ptr(k_cache), _ptr(v_cache),
+        _dtype(k_cache), _ptr(block_tables), _ptr(context_lens), _ptr(new_tables), _ptr(keep_lens), B, hkv, d, bs,
+        block_tables.shape[1], new_tables.shape[1], nb, max_context_len, sinks, recent, _stream(stream)), "pa_evict")
+
+
 def pa_cross_attention(out, query, k, v, state_lens, query_start, max_query_len, max_state_len, scale, workspace=None,
                        stream=None) -> None:
     """Every query token of sequence b (tokens ``query_start[b]`` to
@@ -511,6 +613,13 @@ class BlockManager:
 
     def fork(self, parent: int, child: int) -> None:
         _check(self._lib.pa_bm_fork(self._h, parent, child), "pa_bm_fork")
+
+    def compact(self, seq: int, num_tokens: int):
+        """The blocks of a compacted copy of ``seq`` (:func:`pa_evict`), now its table; its old ones are released."""
+        cap = -(-max(num_tokens, 0) // self.block_size)
+        buf, n = (ctypes.c_int32 * max(1, cap))(), ctypes.c_int(0)
+        _check(self._lib.pa_bm_compact(self._h, seq, num_tokens, buf, cap, ctypes.byref(n)), "pa_bm_compact")
+        return [int(buf[i]) for i in range(n.value)]
 
     def free(self, seq: int) -> None:
         _check(self._lib.pa_bm_free(self._h, seq), "pa_bm_free")

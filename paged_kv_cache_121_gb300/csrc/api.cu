@@ -17,6 +17,7 @@
 #include "internal.h"
 #include "prompt_common.cuh"
 #include "rope_common.cuh"
+#include "weights_common.cuh"
 
 namespace pa {
 
@@ -1037,6 +1038,42 @@ pa_status run_prefill(const PrefillShape &s, void *out, pa_dtype out_dtype, cons
                : PA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------------------
+// Attention weights of cached tokens, and eviction by them
+// ---------------------------------------------------------------------------
+constexpr int kWeightStatsCtasPerSm = 4;    // CTAs that the CUDA-core statistics aim at
+constexpr int kWeightStatsMinSplit = 512;   // context tokens a piece, at least
+
+bool valid_decay(float decay) { return std::isfinite(decay) && decay >= 0.f; }
+
+struct WeightsPlan {
+    int max_count;       // query tokens of a sequence that count, at most
+    bool compact;        // statistics laid out sequence by sequence (else by query token)
+    int64_t stat_rows;
+    int nsplit;
+    size_t total;        // workspace bytes
+};
+
+WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms) {
+    WeightsPlan pl;
+    pl.max_count = window > 0 ? std::min(window, max_query) : max_query;
+    const int64_t compact_rows = static_cast<int64_t>(s.num_seqs) * pl.max_count;
+    pl.compact = compact_rows < num_tokens;
+    pl.stat_rows = std::min<int64_t>(compact_rows, num_tokens);
+    const int64_t tiles = s.num_seqs * static_cast<int64_t>(s.num_kv_heads) *
+                          cdiv64(static_cast<int64_t>(pl.max_count) * (s.num_heads / s.num_kv_heads), prefill_weights_simt_rows());
+    pl.nsplit = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>({static_cast<int64_t>(sms) * kWeightStatsCtasPerSm / std::max<int64_t>(tiles, 1),
+                              s.max_ctx / kWeightStatsMinSplit, kMaxSplits})));
+    pl.total = align256(static_cast<size_t>(pl.nsplit) * pl.stat_rows * s.num_heads * sizeof(float2));
+    return pl;
+}
+
+pa_status check_prefill_weights(const DecodeShape &s, int num_tokens, int max_query, int window) {
+    if (num_tokens < 0 || max_query < 0 || window < 0) return PA_ERR_INVALID_ARG;
+    return check_shape(s);
+}
+
 }  // namespace
 
 int *device_status_word() {
@@ -1732,6 +1769,185 @@ PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa
     if (st != PA_OK) return st;
     return run_prefill(s, out, out_dtype, query, k_cache, v_cache, kv_dtype, block_tables, context_lens, query_start,
                        scale, causal != 0, workspace, workspace_bytes, stream);
+}
+
+PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                               int block_size, int max_context_len) {
+    const int64_t blocks = block_size > 0 ? std::max<int64_t>(cdiv64(max_context_len, block_size), 1) : 1;
+    const DecodeShape s{num_seqs, num_heads, num_kv_heads, head_dim, block_size, static_cast<int>(blocks), 1, max_context_len};
+    if (check_shape(s) != PA_OK) return 0;
+    return static_cast<size_t>(num_seqs) * num_heads * decode_weights_score_stride(max_context_len) * sizeof(float);
+}
+
+PA_API pa_status pa_decode_weights(void *out, pa_dtype out_dtype, float *weights, int64_t weights_stride,
+                                   const void *query, pa_dtype q_dtype, const void *k_cache, const void *v_cache,
+                                   pa_dtype kv_dtype, const int32_t *block_tables, const int32_t *context_lens,
+                                   int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int num_blocks, int max_context_len, float scale,
+                                   float decay, void *workspace, size_t workspace_bytes, void *stream) {
+    const DecodeShape s{num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                        max_blocks_per_seq, num_blocks, max_context_len};
+    pa_status st = check_shape(s);
+    if (st != PA_OK) return st;
+    if (!valid_dtype(out_dtype) || !std::isfinite(scale) || !valid_decay(decay) || weights_stride < max_context_len)
+        return PA_ERR_INVALID_ARG;
+    if ((st = check_dtypes(q_dtype, kv_dtype)) != PA_OK) return st;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !weights || !query || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned_to(weights, 4) ||
+        !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t stride = decode_weights_score_stride(max_context_len);
+    const size_t need = static_cast<size_t>(num_seqs) * num_heads * stride * sizeof(float);
+    if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PA_ERR_WORKSPACE;
+    int dev;
+    if ((st = current_device(&dev)) != PA_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return PA_ERR_CUDA;
+    DecodeWeightsParams p;
+    std::memset(&p, 0, sizeof p);
+    p.query = query;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.out = out;
+    p.weights = weights;
+    p.scores = static_cast<float *>(workspace);
+    p.weights_stride = weights_stride;
+    p.score_stride = stride;
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.max_ctx = max_context_len;
+    p.out_type = static_cast<int>(out_dtype);
+    p.scale_log2 = scale * kLog2e;
+    p.decay = decay;
+    return launch_decode_weights(p, static_cast<int>(kv_dtype), head_dim, sms, as_stream(stream)) == cudaSuccess ? PA_OK
+                                                                                                              : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_prefill_weights_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
+                                                int head_dim, int block_size, int max_query_len,
+                                                int max_context_len, int window) {
+    const int64_t blocks = block_size > 0 ? std::max<int64_t>(cdiv64(max_context_len, block_size), 1) : 1;
+    const DecodeShape s{num_seqs, num_heads, num_kv_heads, head_dim, block_size, static_cast<int>(blocks), 1, max_context_len};
+    if (check_prefill_weights(s, num_tokens, max_query_len, window) != PA_OK) return 0;
+    int dev;
+    if (current_device(&dev) != PA_OK) return 0;
+    const int sms = sm_count(dev);
+    return sms > 0 ? plan_weights(s, num_tokens, max_query_len, window, sms).total : 0;
+}
+
+PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, const void *query, pa_dtype q_dtype,
+                                    const void *k_cache, pa_dtype kv_dtype, const int32_t *block_tables,
+                                    const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                    int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, int num_blocks, int max_query_len, int max_context_len,
+                                    float scale, float decay, int window, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    const DecodeShape s{num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                        max_blocks_per_seq, num_blocks, max_context_len};
+    pa_status st = check_prefill_weights(s, num_tokens, max_query_len, window);
+    if (st != PA_OK) return st;
+    if (!std::isfinite(scale) || !valid_decay(decay) || weights_stride < max_context_len) return PA_ERR_INVALID_ARG;
+    if ((st = check_dtypes(q_dtype, kv_dtype)) != PA_OK) return st;
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0 || max_context_len == 0) return PA_OK;
+    if (!weights || !query || !k_cache || !block_tables || !context_lens || !query_start) return PA_ERR_INVALID_ARG;
+    if (!aligned16(query) || !aligned16(k_cache) || !aligned_to(weights, 4) || !aligned_to(block_tables, 4) ||
+        !aligned_to(context_lens, 4) || !aligned_to(query_start, 4))
+        return PA_ERR_INVALID_ARG;
+    int dev;
+    if ((st = current_device(&dev)) != PA_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return PA_ERR_CUDA;
+    const WeightsPlan pl = plan_weights(s, num_tokens, max_query_len, window, sms);
+    if (!workspace || workspace_bytes < pl.total || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    PrefillWeightsParams p;
+    std::memset(&p, 0, sizeof p);
+    p.query = query;
+    p.k_cache = k_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.weights = weights;
+    p.stats = static_cast<float2 *>(workspace);
+    p.weights_stride = weights_stride;
+    p.stat_rows = pl.stat_rows;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.max_count = pl.max_count;
+    p.max_ctx = max_context_len;
+    p.window = window;
+    p.compact = pl.compact;
+    p.nsplit = pl.nsplit;
+    p.scale_log2 = scale * kLog2e;
+    p.decay = decay;
+    return launch_prefill_weights_simt(p, static_cast<int>(kv_dtype), head_dim, as_stream(stream)) == cudaSuccess ? PA_OK
+                                                                                                               : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_evict(int32_t *kept, int64_t kept_stride, float *new_weights, int64_t new_weights_stride,
+                          const float *weights, int64_t weights_stride, void *k_cache, void *v_cache,
+                          pa_dtype kv_dtype, const int32_t *block_tables, const int32_t *context_lens,
+                          const int32_t *new_tables, const int32_t *keep_lens, int num_seqs, int num_kv_heads,
+                          int head_dim, int block_size, int max_blocks_per_seq, int max_new_blocks, int num_blocks,
+                          int max_context_len, int num_sinks, int num_recent, void *stream) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 ||
+        max_new_blocks <= 0 || num_blocks <= 0 || max_context_len < 0 || num_sinks < 0 || num_recent < 0 ||
+        kept_stride < 0 || new_weights_stride < 0 || weights_stride < max_context_len || !valid_dtype(kv_dtype))
+        return PA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size) return PA_ERR_INVALID_ARG;
+    const int64_t row_bytes = static_cast<int64_t>(head_dim) * element_bytes(kv_dtype);
+    if (row_bytes % 16 != 0 || row_bytes > (1 << 20) || num_seqs > 65535 ||
+        static_cast<int64_t>(num_seqs) * num_kv_heads > INT32_MAX || num_kv_heads > (1 << 20))
+        return PA_ERR_UNSUPPORTED;
+    const int64_t most = std::min<int64_t>({kept_stride, new_weights_stride, static_cast<int64_t>(max_new_blocks) * block_size,
+                                            max_context_len});
+    if (num_seqs == 0 || most == 0) return PA_OK;
+    if (!kept || !new_weights || !weights || !k_cache || !v_cache || !block_tables || !context_lens || !new_tables ||
+        !keep_lens || new_weights == weights)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned_to(kept, 4) || !aligned_to(new_weights, 4) ||
+        !aligned_to(weights, 4) || !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) ||
+        !aligned_to(new_tables, 4) || !aligned_to(keep_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    EvictParams p;
+    std::memset(&p, 0, sizeof p);
+    p.weights = weights;
+    p.new_weights = new_weights;
+    p.kept = kept;
+    p.weights_stride = weights_stride;
+    p.new_weights_stride = new_weights_stride;
+    p.kept_stride = kept_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.new_tables = new_tables;
+    p.context_lens = context_lens;
+    p.keep_lens = keep_lens;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.row_bytes = static_cast<int>(row_bytes);
+    p.block_size = block_size;
+    p.max_blocks = max_blocks_per_seq;
+    p.max_new_blocks = max_new_blocks;
+    p.num_blocks = num_blocks;
+    p.max_ctx = max_context_len;
+    p.max_keep = static_cast<int>(most);
+    p.sinks = num_sinks;
+    p.recent = num_recent;
+    return launch_evict(p, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k,

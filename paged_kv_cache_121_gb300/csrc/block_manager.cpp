@@ -129,6 +129,14 @@ static pa_status collect_group(pa_bm *bm, const int64_t *ids, int n, bool swappe
     return PA_OK;
 }
 
+// One reference less on each of a table's blocks; released ones go to the queue front, keeping
+// their table order.
+static void release_blocks(pa_bm *bm, const std::vector<int32_t> &table) {
+    for (int32_t b : table) --bm->refcount[b];
+    for (auto r = table.rbegin(); r != table.rend(); ++r)
+        if (bm->refcount[*r] == 0 && !bm->q.on_queue[*r]) bm->push_front(*r);
+}
+
 extern "C" {
 
 PA_API pa_status pa_bm_create(int num_blocks, int block_size, int reserve_null_block, pa_bm **out) {
@@ -226,6 +234,30 @@ PA_API pa_status pa_bm_fork(pa_bm *bm, int64_t parent, int64_t child) {
     return PA_OK;
 }
 
+PA_API pa_status pa_bm_compact(pa_bm *bm, int64_t seq, int num_tokens, int32_t *new_table, int cap, int *n) {
+    if (!bm || !n || num_tokens < 0) return PA_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq);
+    if (it == bm->seqs.end()) return PA_ERR_NOT_FOUND;
+    Sequence &s = it->second;
+    if (s.swapped || num_tokens > s.tokens) return PA_ERR_INVALID_ARG;
+    const int64_t need = (static_cast<int64_t>(num_tokens) + bm->block_size - 1) / bm->block_size;
+    *n = static_cast<int>(need);
+    if (cap < need || (need > 0 && !new_table)) return PA_ERR_INVALID_ARG;
+    if (need > bm->q.count) return PA_ERR_OUT_OF_BLOCKS;
+    std::vector<int32_t> fresh;
+    try {
+        fresh.reserve(static_cast<size_t>(need));
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_OUT_OF_BLOCKS;   // (nothing has changed)
+    }
+    for (int64_t i = 0; i < need; ++i) fresh.push_back(bm->pop_front());
+    std::copy(fresh.begin(), fresh.end(), new_table);
+    s.table.swap(fresh);
+    s.tokens = num_tokens;
+    release_blocks(bm, fresh);
+    return PA_OK;
+}
+
 PA_API pa_status pa_bm_free(pa_bm *bm, int64_t seq) {
     if (!bm) return PA_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq);
@@ -239,10 +271,7 @@ PA_API pa_status pa_bm_free(pa_bm *bm, int64_t seq) {
         bm->seqs.erase(it);
         return PA_OK;
     }
-    for (int32_t b : table) --bm->refcount[b];
-    // released blocks go to the queue front, keeping their table order
-    for (auto r = table.rbegin(); r != table.rend(); ++r)
-        if (bm->refcount[*r] == 0 && !bm->q.on_queue[*r]) bm->push_front(*r);
+    release_blocks(bm, table);
     bm->seqs.erase(it);
     return PA_OK;
 }

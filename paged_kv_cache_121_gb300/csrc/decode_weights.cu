@@ -1,0 +1,459 @@
+// One decode step that also adds the weight it gave every cached token to a table:
+// out = softmax(scale q K^T) V, weights = decay * weights + sum over the query heads
+// of each KV head of their softmax weights.
+//
+// Mathematics. A token's weight needs its row's maximum and sum, which stand only
+// after the last token. So the scores are kept (4 bytes a token and query head: 3 %
+// of the K and V bytes of a group of 4 heads of 128) and turned into weights by the
+// CTA that made them, once the row's statistics are merged; no second pass over K.
+//
+// Bound: HBM, K and V read once. How:
+//  * One cluster of up to 8 CTAs = one sequence x a group of KV heads; each CTA takes
+//    a range of the context. A warp owns one KV head and every sets-th tile of the
+//    range and fetches its own tiles by 16-byte asynchronous copies into a ring of
+//    its own (24 KB), through the block table, token by token: any block size will do
+//    and no warp waits for another before the end. Rows are swizzled (16-byte chunk ^
+//    token & 7), so that the matrix loads have no bank conflicts.
+//  * 16-bit caches: products on mma.m16n8k16 (M = the query heads, 16 at most a pass;
+//    bound by memory, so the wider tcgen05 tiles would stand empty), softmax online in
+//    base 2, weights of V in two 16-bit parts, as in decode_mma.cu. fp32: CUDA cores.
+//  * The warps' states meet in shared memory, the cluster's CTAs through distributed
+//    shared memory; each CTA merges a slice of the outputs and, for itself, every
+//    row's maximum and sum, and then goes through its own scores (in L2 still).
+//    One launch, no atomics: the same call gives the same bits.
+//  * More than 16 query heads a KV head: the passes follow one another in the CTA.
+#include <algorithm>
+
+#include "internal.h"
+#include "mma_tile.cuh"
+#include "weights_common.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRingBytes = 24 * 1024;   // a warp's tiles in flight
+
+template <typename T, int D>
+struct StepCfg {
+    static constexpr bool kFloat = sizeof(T) == 4;
+    static constexpr int kTile = kFloat ? 8 : 16;                  // tokens
+    static constexpr int kRow = D * static_cast<int>(sizeof(T));   // bytes of one head's row
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kStage = 2 * kTile * kRow;                // K, then V
+    static constexpr int kStages = kRingBytes / kStage;
+    static constexpr int kStateStride = D + 8;                     // floats a row: 8-byte stores of 4 rows in 32 banks
+    static constexpr int kState = 32 + kRowsPerTile * kStateStride;
+    static_assert(kState * 4 <= kRingBytes, "a warp's state takes its ring's place");
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+    const int bytes = live ? 16 : 0;   // (the rest is filled with zeros)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// One warp's query rows and running state, 16-bit caches.
+template <typename T, int D>
+struct StepTile {
+    using C = StepCfg<T, D>;
+    static constexpr bool kF16 = std::is_same<T, __half>::value;
+    WarpState<D> st;
+    uint32_t qa[D / 16][4];
+
+    __device__ __forceinline__ void start(const T *query, float *, int rows, int lane) {   // query: the warp's first row
+        st.init();
+        const uint32_t *q0 = reinterpret_cast<const uint32_t *>(query) + (lane >> 2) * (D / 2);
+        load_query_fragments<D>(qa, q0, q0 + 8 * (D / 2), (lane >> 2) < rows, (lane >> 2) + 8 < rows, lane);
+    }
+
+    // One tile of `valid` tokens; scores: the first row's, at the tile's first token.
+    __device__ __forceinline__ void add(const unsigned char *stage, const float *, float *scores, int64_t score_stride,
+                                        int rows, int valid, float scale, int lane) {
+        const int r = lane >> 2, q4 = lane & 3;
+        const uint32_t kbase = smem_addr(stage), vbase = kbase + C::kTile * C::kRow;
+        float s[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float odd[4] = {0.f, 0.f, 0.f, 0.f};
+            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            const int tok = 8 * j + (lane & 7);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk += 2) {
+                const int c = 2 * kk + (lane >> 3);
+                uint32_t b0, b1, b2, b3;
+                ldmatrix_x4(kbase + tok * C::kRow + ((c ^ (tok & 7)) << 4), b0, b1, b2, b3);
+                mma_16816<kF16>(s[j], qa[kk], b0, b1);
+                mma_16816<kF16>(odd, qa[kk + 1], b2, b3);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = (s[j][e] + odd[e]) * scale;
+        }
+        if (valid < C::kTile) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (8 * j + 2 * q4 + e >= valid) s[j][e] = s[j][2 + e] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // (the rows of scores are padded to whole tiles)
+            float *to = scores + r * score_stride + 8 * j + 2 * q4;
+            if (r < rows) *reinterpret_cast<float2 *>(to) = make_float2(s[j][0], s[j][1]);
+            if (r + 8 < rows) *reinterpret_cast<float2 *>(to + 8 * score_stride) = make_float2(s[j][2], s[j][3]);
+        }
+        float m0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float m1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+        }
+        // the reference maximum moves only where a score passes it by 2^kRescaleSlack
+        const bool up0 = m0 > st.m0 + kRescaleSlack, up1 = m1 > st.m1 + kRescaleSlack;
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float n0 = up0 ? m0 : st.m0, n1 = up1 ? m1 : st.m1;
+            const float a0 = up0 ? fast_exp2(st.m0 - n0) : 1.f, a1 = up1 ? fast_exp2(st.m1 - n1) : 1.f;
+            st.m0 = n0;
+            st.m1 = n1;
+            st.l0 *= a0;
+            st.l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                st.o[i][0] *= a0;
+                st.o[i][1] *= a0;
+                st.o[i][2] *= a1;
+                st.o[i][3] *= a1;
+            }
+        }
+        // (a row that has seen nothing but -inf has m = -inf: its weights are zeros)
+        const float b0 = st.m0 == -INFINITY ? 0.f : st.m0, b1 = st.m1 == -INFINITY ? 0.f : st.m1;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float p0 = fast_exp2(s[j][0] - b0), p1 = fast_exp2(s[j][1] - b0);
+            const float p2 = fast_exp2(s[j][2] - b1), p3 = fast_exp2(s[j][3] - b1);
+            st.l0 += p0 + p1;
+            st.l1 += p2 + p3;
+            split_x2<kF16>(p0, p1, hi[2 * j], lo[2 * j]);
+            split_x2<kF16>(p2, p3, hi[2 * j + 1], lo[2 * j + 1]);
+        }
+#pragma unroll
+        for (int dn = 0; dn < D / 8; dn += 2) {
+            const int mi = lane >> 3;
+            const int tok = (mi & 1) * 8 + (lane & 7), c = dn + (mi >> 1);
+            uint32_t v0, v1, v2, v3;
+            ldmatrix_x4_trans(vbase + tok * C::kRow + ((c ^ (tok & 7)) << 4), v0, v1, v2, v3);
+            mma_16816<kF16>(st.o[dn], hi, v0, v1);
+            mma_16816<kF16>(st.o[dn + 1], hi, v2, v3);
+            mma_16816<kF16>(st.o[dn], lo, v0, v1);
+            mma_16816<kF16>(st.o[dn + 1], lo, v2, v3);
+        }
+    }
+
+    // State rows: (max, sum) of each of 16 rows, then the rows' sums of V.
+    __device__ __forceinline__ void leave(float *state, int, int lane) {
+        const int r = lane >> 2, q4 = lane & 3;
+        st.reduce_sums();
+#pragma unroll
+        for (int dn = 0; dn < D / 8; ++dn) {
+            float *o = state + 32 + r * C::kStateStride + 8 * dn + 2 * q4;
+            *reinterpret_cast<float2 *>(o) = make_float2(st.o[dn][0], st.o[dn][1]);
+            *reinterpret_cast<float2 *>(o + 8 * C::kStateStride) = make_float2(st.o[dn][2], st.o[dn][3]);
+        }
+        if (q4 == 0) {
+            *reinterpret_cast<float2 *>(state + 2 * r) = make_float2(st.m0, st.l0);
+            *reinterpret_cast<float2 *>(state + 2 * (r + 8)) = make_float2(st.m1, st.l1);
+        }
+    }
+};
+
+// fp32 caches: lane = (token of 8, quarter of the dims) for the scores, D / 32 dims a lane for the sums of V.
+template <int D>
+struct StepTile<float, D> {
+    using C = StepCfg<float, D>;
+    static constexpr int kDims = D / 32;
+    float m[kRowsPerTile], l[kRowsPerTile], o[kRowsPerTile][kDims];
+
+    __device__ __forceinline__ void start(const float *query, float *q, int rows, int lane) {
+#pragma unroll
+        for (int r = 0; r < kRowsPerTile; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) o[r][d] = 0.f;
+        }
+        for (int i = lane; i < rows * D; i += 32) q[i] = query[i];
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void add(const unsigned char *stage, const float *q, float *scores, int64_t score_stride,
+                                        int rows, int valid, float scale, int lane) {
+        const int tok = lane >> 2, quarter = lane & 3;
+        const unsigned char *k = stage + tok * C::kRow;
+        const unsigned char *v = stage + C::kTile * C::kRow;
+#pragma unroll
+        for (int r = 0; r < kRowsPerTile; ++r) {
+            if (r >= rows) break;
+            float s = 0.f;
+#pragma unroll 4
+            for (int c = quarter; c < C::kChunks; c += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(k + ((c ^ (tok & 7)) << 4));
+                const float4 b = *reinterpret_cast<const float4 *>(q + r * D + 4 * c);
+                s += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s = tok < valid ? s * scale : -INFINITY;
+            if (quarter == 0) scores[r * score_stride + tok] = s;
+            float top = s;
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (top > m[r]) {
+                const float a = fast_exp2(m[r] - top);
+                m[r] = top;
+                l[r] *= a;
+#pragma unroll
+                for (int d = 0; d < kDims; ++d) o[r][d] *= a;
+            }
+            const float p = fast_exp2(s - (m[r] == -INFINITY ? 0.f : m[r]));
+            if (quarter == 0) l[r] += p;
+#pragma unroll
+            for (int t = 0; t < C::kTile; ++t) {
+                const float pt = __shfl_sync(0xffffffffu, p, 4 * t);
+#pragma unroll
+                for (int d = 0; d < kDims; ++d) {   // dim lane + 32 d of token t
+                    const int dim = lane + 32 * d;
+                    const float x = *reinterpret_cast<const float *>(v + t * C::kRow + (((dim >> 2) ^ (t & 7)) << 4) + (dim & 3) * 4);
+                    o[r][d] += pt * x;
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void leave(float *state, int rows, int lane) {
+#pragma unroll
+        for (int r = 0; r < kRowsPerTile; ++r) {
+            if (r >= rows) break;
+            float sum = l[r];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) state[32 + r * C::kStateStride + lane + 32 * d] = o[r][d];
+            if (lane == 0) *reinterpret_cast<float2 *>(state + 2 * r) = make_float2(m[r], sum);
+        }
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 1)
+decode_weights_kernel(const __grid_constant__ DecodeWeightsParams p) {
+    using C = StepCfg<T, D>;
+    extern __shared__ __align__(128) unsigned char smem[];   // the warps' rings, later their states; fp32: query rows
+    __shared__ float2 s_row[8][kRowsPerTile];                // a KV head's rows: maximum, 1 / sum
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nwarps = blockDim.x >> 5;
+    grid_dependency_wait();
+
+    const int b = blockIdx.z, head0 = blockIdx.y * p.heads_per_cta;
+    const int head = head0 + warp / p.sets, set = warp % p.sets;   // this warp's KV head, its share of the tiles
+    const int given = p.context_lens[b];
+    int len = max(0, min(given, p.max_ctx));
+    len = static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(p.max_blocks) * p.block_size));
+    const int tok_begin = min(len, static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * p.part_tokens, static_cast<int64_t>(len))));
+    const int tok_end = static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(tok_begin) + p.part_tokens));
+    const int all_tiles = (tok_end - tok_begin + C::kTile - 1) / C::kTile;
+    const int tiles = all_tiles > set ? (all_tiles - set + p.sets - 1) / p.sets : 0;   // this warp's
+    const int32_t *table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+    unsigned char *ring = smem + warp * kRingBytes;
+    const uint32_t ring_addr = smem_addr(ring);
+    float *q_rows = reinterpret_cast<float *>(smem + nwarps * kRingBytes) + warp * (C::kFloat ? kRowsPerTile * D : 0);
+    const int64_t token_bytes = static_cast<int64_t>(p.num_kv_heads) * C::kRow;
+    const unsigned char *k_head = static_cast<const unsigned char *>(p.k_cache) + head * C::kRow;
+    const unsigned char *v_head = static_cast<const unsigned char *>(p.v_cache) + head * C::kRow;
+
+    auto first_token = [&](int i) { return tok_begin + (set + i * p.sets) * C::kTile; };
+    // the slot of the lane's token of tile i (-1: nothing to read)
+    auto slot_of = [&](int i) -> int64_t {
+        const int t = first_token(i) + lane;
+        if (i >= tiles || lane >= C::kTile || t >= tok_end) return -1;
+        const int blk = table[t / p.block_size];
+        if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) return -1;
+        return static_cast<int64_t>(blk) * p.block_size + t % p.block_size;
+    };
+    auto fetch = [&](int i, int64_t slot) {
+        if (i < tiles) {
+            const uint32_t k_dst = ring_addr + (i % C::kStages) * C::kStage, v_dst = k_dst + C::kTile * C::kRow;
+#pragma unroll
+            for (int n = 0; n < C::kTile * C::kChunks / 32; ++n) {
+                const int at = n * 32 + lane, t = at / C::kChunks, c = at % C::kChunks;
+                const int64_t from = __shfl_sync(0xffffffffu, slot, t);
+                const int64_t off = from < 0 ? 0 : from * token_bytes + c * 16;
+                const uint32_t to = t * C::kRow + ((c ^ (t & 7)) << 4);
+                copy16(k_dst + to, k_head + off, from >= 0);
+                copy16(v_dst + to, v_head + off, from >= 0);
+            }
+        }
+        copy_commit();
+    };
+
+    for (int first = 0; first < p.group; first += kRowsPerTile) {   // 16 query heads of each KV head a pass
+        const int rows = min(kRowsPerTile, p.group - first);
+        const int64_t row0 = static_cast<int64_t>(b) * p.num_heads + head * p.group + first;   // the warp's first row
+        StepTile<T, D> tile;
+        tile.start(static_cast<const T *>(p.query) + row0 * D, q_rows, rows, lane);
+        int64_t slot = slot_of(0);
+        for (int i = 0; i < C::kStages - 1; ++i) {
+            const int64_t now = slot;
+            slot = slot_of(i + 1);
+            fetch(i, now);
+        }
+        float *scores = p.scores + row0 * p.score_stride;
+        for (int i = 0; i < tiles; ++i) {
+            const int64_t now = slot;
+            slot = slot_of(i + C::kStages);
+            fetch(i + C::kStages - 1, now);
+            copy_wait<C::kStages - 1>();
+            __syncwarp();
+            const int t0 = first_token(i);
+            tile.add(ring + (i % C::kStages) * C::kStage, q_rows, scores + t0, p.score_stride, rows, min(C::kTile, tok_end - t0),
+                     p.scale_log2, lane);
+            __syncwarp();   // the stage is free
+        }
+        copy_wait<0>();
+        if (first + kRowsPerTile >= p.group) grid_dependents_launch();
+        __syncwarp();
+        float *state = reinterpret_cast<float *>(ring);
+        tile.leave(state, rows, lane);
+        cluster_sync_all();   // every state of the cluster can be read
+
+        const int nsplit = p.nsplit, states = nsplit * p.sets;
+        const uint32_t base = smem_addr(smem);
+        auto state_addr = [&](int j, int n) {   // state n of the cluster's CTAs and warps for KV head j of the group
+            return cluster_map(base + static_cast<uint32_t>((j * p.sets + n % p.sets) * kRingBytes), n / p.sets);
+        };
+        for (int i = threadIdx.x; i < p.heads_per_cta * rows; i += blockDim.x) {
+            const int j = i / rows, r = i - j * rows;
+            float top = -INFINITY, sum = 0.f;
+            for (int n = 0; n < states; ++n) {
+                const float2 ml = ld_cluster_f32x2(state_addr(j, n) + 8 * r);
+                if (ml.y > 0.f) {
+                    const float up = fmaxf(top, ml.x);
+                    sum = sum * (sum > 0.f ? fast_exp2(top - up) : 0.f) + ml.y * fast_exp2(ml.x - up);
+                    top = up;
+                } else if (!(ml.y == 0.f)) {   // NaN
+                    sum = ml.y;
+                    top = 0.f;
+                    break;
+                }
+            }
+            s_row[j][r] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(top, 1.f / sum);
+        }
+        __syncthreads();
+        // a slice of the outputs: 4 dims of one row a thread
+        const int total = p.heads_per_cta * rows * (D / 4);
+        const int slice = (total + nsplit - 1) / nsplit;
+        const int rank = static_cast<int>(cluster_rank());
+        for (int i = rank * slice + threadIdx.x; i < min(total, (rank + 1) * slice); i += blockDim.x) {
+            const int j = i / (rows * (D / 4)), rem = i - j * rows * (D / 4);
+            const int r = rem / (D / 4), d = 4 * (rem - r * (D / 4));
+            const float2 ml = s_row[j][r];
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int n = 0; n < states; ++n) {
+                const uint32_t at = state_addr(j, n);
+                const float2 own = ld_cluster_f32x2(at + 8 * r);
+                const float4 o = ld_cluster_f32x4(at + 4 * (32 + r * C::kStateStride + d));
+                const float f = own.y == 0.f ? 0.f : fast_exp2(own.x - ml.x) * ml.y;
+                if (own.y == 0.f) continue;
+                acc.x += f * o.x;
+                acc.y += f * o.y;
+                acc.z += f * o.z;
+                acc.w += f * o.w;
+            }
+            const int64_t at = (static_cast<int64_t>(b) * p.num_heads + (head0 + j) * p.group + first + r) * D + d;
+            store_pair_as(p.out, p.out_type, at, acc.x, acc.y);
+            store_pair_as(p.out, p.out_type, at + 2, acc.z, acc.w);
+        }
+        // this CTA's scores become weights
+        const int n_tok = tok_end - tok_begin;
+        for (int j = 0; j < p.heads_per_cta; ++j) {
+            const float *from = p.scores + (static_cast<int64_t>(b) * p.num_heads + (head0 + j) * p.group + first) * p.score_stride;
+            float *to = p.weights + (static_cast<int64_t>(b) * p.num_kv_heads + head0 + j) * p.weights_stride;
+            for (int i = threadIdx.x; i < n_tok; i += blockDim.x) {
+                const int t = tok_begin + i;
+                float w = 0.f;
+#pragma unroll 4
+                for (int r = 0; r < rows; ++r) {
+                    const float2 ml = s_row[j][r];
+                    w += fast_exp2(from[r * p.score_stride + t] - ml.x) * ml.y;
+                }
+                // the newest token's weight starts here
+                if (first > 0) w += to[t];
+                else if (t != given - 1 && p.decay != 0.f) w += p.decay * to[t];
+                to[t] = w;
+            }
+        }
+        cluster_sync_all();   // the peers have read this CTA's states
+    }
+}
+
+// KV heads a CTA serves, its warps, the CTAs of a context. Two CTAs of 4 warps an SM, or, where even
+// single heads and clusters of 8 leave SMs without one, one of 8 warps.
+struct StepPlan {
+    int heads, warps, nsplit, part_tokens;
+};
+
+StepPlan plan_step(int num_seqs, int num_kv_heads, int max_ctx, int sms) {
+    StepPlan pl;
+    const int64_t slots = 2 * static_cast<int64_t>(sms);
+    pl.heads = 4;
+    while (pl.heads > 1 && (num_kv_heads % pl.heads != 0 ||
+                            static_cast<int64_t>(num_seqs) * (num_kv_heads / pl.heads) * kMaxClusterSplits * 4 < slots * 3))
+        pl.heads /= 2;
+    const int64_t units = static_cast<int64_t>(num_seqs) * (num_kv_heads / pl.heads);
+    pl.warps = units * kMaxClusterSplits <= sms ? 8 : 4;
+    // a CTA's warps have two tiles each at least
+    const int64_t most = std::max(1, max_ctx / (pl.warps / pl.heads * 32));
+    pl.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kMaxClusterSplits, slots / units, most})));
+    const int64_t part = (static_cast<int64_t>(max_ctx) + pl.nsplit - 1) / pl.nsplit;
+    pl.part_tokens = static_cast<int>(std::min<int64_t>((part + 15) / 16 * 16, INT32_MAX / 16 * 16));
+    return pl;
+}
+
+template <typename T, int D>
+cudaError_t launch_step(DecodeWeightsParams &p, const StepPlan &pl, cudaStream_t stream) {
+    const size_t smem = static_cast<size_t>(pl.warps) * (kRingBytes + (sizeof(T) == 4 ? kRowsPerTile * D * 4 : 0));
+    const dim3 grid(static_cast<unsigned>(pl.nsplit), static_cast<unsigned>(p.num_kv_heads / pl.heads),
+                    static_cast<unsigned>(p.num_seqs));
+    auto kern = decode_weights_kernel<T, D>;
+    static unsigned long long done = 0;
+    const cudaError_t e = ensure_smem_limit(kern, 8 * kRingBytes + (sizeof(T) == 4 ? 8 * 1024 : 0), done);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, grid, dim3(32 * pl.warps), smem, stream, static_cast<unsigned>(pl.nsplit), p);
+}
+
+}  // namespace
+
+int64_t decode_weights_score_stride(int max_ctx) { return (static_cast<int64_t>(max_ctx) + 15) / 16 * 16; }
+
+cudaError_t launch_decode_weights(DecodeWeightsParams &p, int type, int head_dim, int sms, cudaStream_t stream) {
+    StepPlan pl = plan_step(p.num_seqs, p.num_kv_heads, p.max_ctx, sms);
+    if (type == 0) pl.warps = 4;   // (fp32 query rows take the room of the other four)
+    p.heads_per_cta = pl.heads;
+    p.sets = pl.warps / pl.heads;
+    p.nsplit = pl.nsplit;
+    p.part_tokens = pl.part_tokens;
+    if (head_dim == 128)
+        return type == 0   ? launch_step<float, 128>(p, pl, stream)
+               : type == 1 ? launch_step<__nv_bfloat16, 128>(p, pl, stream)
+                           : launch_step<__half, 128>(p, pl, stream);
+    return type == 0   ? launch_step<float, 64>(p, pl, stream)
+           : type == 1 ? launch_step<__nv_bfloat16, 64>(p, pl, stream)
+                       : launch_step<__half, 64>(p, pl, stream);
+}
+
+}  // namespace pa

@@ -11,6 +11,9 @@ struct DecodeParams;
 struct PrefixParams;
 struct RopeParams;
 struct NormRopeParams;
+struct DecodeWeightsParams;
+struct PrefillWeightsParams;
+struct EvictParams;
 struct PrefillParams;
 
 bool decode_mma_supported(int head_dim, int block_size);   // D 64/128, blocks of 1..256 (powers of two)
@@ -80,6 +83,13 @@ cudaError_t launch_rope(RopeParams &p, int type, int sms, cudaStream_t stream);
 // Heads normed and rotated, or (grad_out given) the gradients (norm_rope.cu)
 size_t norm_rope_grad_workspace(int head_dim, int sms);
 cudaError_t launch_norm_rope(NormRopeParams &p, int type, int sms, cudaStream_t stream);
+// A decode step and the weights it gave (decode_weights.cu); a prompt's weights
+// (prefill_weights_*.cu); the eviction that goes by them (evict.cu)
+int64_t decode_weights_score_stride(int max_ctx);   // floats a row of scores
+cudaError_t launch_decode_weights(DecodeWeightsParams &p, int type, int head_dim, int sms, cudaStream_t stream);
+int prefill_weights_simt_rows();                    // rows of a tile
+cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int type, int head_dim, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 // Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid
 // (row tiles of the batch, Hkv * ntile, nsplit); `tall`: 64-row tiles, else 16.
 // With nsplit > 1 the merge is launched too.

@@ -1,0 +1,115 @@
+// Arguments of the kernels around attention weights: the weights that decode
+// steps and prompts gave the cached tokens (decode_weights.cu,
+// prefill_weights.cu), and the eviction that goes by them (evict.cu).
+#pragma once
+
+#include "device_common.cuh"
+
+namespace pa {
+
+// One decode step that leaves the weight it gave each cached token.
+struct DecodeWeightsParams {
+    const void *query;            // [num_seqs, num_heads, head_dim]
+    const void *k_cache, *v_cache;
+    const int32_t *block_tables, *context_lens;
+    void *out;                    // [num_seqs, num_heads, head_dim]
+    float *weights;               // [num_seqs, num_kv_heads, weights_stride]
+    float *scores;                // [num_seqs, num_heads, score_stride]: scale * q.k * log2(e)
+    int64_t weights_stride;
+    int64_t score_stride;         // a multiple of 16
+    int num_seqs, num_heads, num_kv_heads, group;
+    int block_size, max_blocks, num_blocks;
+    int max_ctx;
+    int heads_per_cta, sets;      // KV heads of a CTA, warps that share each
+    int nsplit, part_tokens;      // CTAs (one cluster) and tokens each of a context
+    int out_type;
+    float scale_log2, decay;
+};
+
+// The weights that several query tokens a sequence gave each cached token, without their outputs.
+// A sequence's rows are the (query token, query head) pairs of one KV head that count, token by token.
+struct PrefillWeightsParams {
+    const void *query;            // [num_tokens, num_heads, head_dim]
+    const void *k_cache;
+    const int32_t *block_tables, *context_lens, *query_start;
+    float *weights;               // [num_seqs, num_kv_heads, weights_stride]
+    float2 *stats;                // [nsplit][stat_rows][num_heads]: maximum and sum of a row's scores (base 2)
+    int64_t weights_stride, stat_rows;
+    int *status;
+    int num_seqs, num_tokens, num_heads, num_kv_heads, group;
+    int block_size, max_blocks, num_blocks;
+    int max_count, max_ctx;       // host bounds: query tokens that count, context tokens
+    int window;                   // the last so many query tokens count (0: all)
+    int compact;                  // stat rows are sequence * max_count + i, else the query token's index
+    int nsplit;                   // pieces of a context that a row's statistics are made in
+    float scale_log2, decay;
+};
+
+// One sequence's extent, clamped so that no index leaves its array whatever the device-side lengths hold.
+struct WeightSeq {
+    int q0, count;      // first query token that counts, how many
+    int ctx;            // context tokens
+    int past;           // context tokens ahead of the first one that counts (negative: leading rows see nothing)
+    int fresh;          // tokens from here on are the call's own: their weights start here
+    int64_t stat0;      // the first one's row of statistics
+    __device__ int sees(int i) const {   // context tokens that counted query token i sees
+        const int64_t n = static_cast<int64_t>(past) + i + 1;
+        return n < 0 ? 0 : n < ctx ? static_cast<int>(n) : ctx;
+    }
+};
+
+__device__ __forceinline__ WeightSeq weight_seq(const PrefillWeightsParams &p, int b) {
+    WeightSeq s;
+    const int start = p.query_start[b];
+    const int64_t given = static_cast<int64_t>(p.query_start[b + 1]) - start;
+    int64_t n = given;
+    if (start < 0 || start > p.num_tokens) n = 0;
+    n = n < p.num_tokens - start ? n : p.num_tokens - start;
+    n = n > 0 ? n : 0;
+    int64_t count = p.window > 0 && p.window < n ? p.window : n;
+    const int64_t skip = n - count;
+    count = count < p.max_count ? count : p.max_count;
+    s.q0 = start + static_cast<int>(skip);
+    s.count = static_cast<int>(count);
+    const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.block_size;
+    int64_t c = p.context_lens[b];
+    c = c > 0 ? c : 0;
+    s.past = s.count > 0 ? static_cast<int>(c - given + skip) : 0;
+    s.fresh = s.count > 0 ? static_cast<int>(c - given) : 0;
+    c = c < cap ? c : cap;
+    c = c < p.max_ctx ? c : p.max_ctx;
+    s.ctx = s.count > 0 ? static_cast<int>(c) : 0;   // (no query tokens: nothing of the sequence is touched)
+    s.stat0 = p.compact ? static_cast<int64_t>(b) * p.max_count : s.q0;
+    return s;
+}
+
+// A row's maximum and sum over the pieces of its context, as what to take from a score before 2^x:
+// maximum + log2(sum). A row without any weight takes plus infinity: all its weights are zeros.
+__device__ __forceinline__ float row_offset(const PrefillWeightsParams &p, int64_t stat, int head) {
+    float top = -INFINITY, sum = 0.f;
+    for (int s = 0; s < p.nsplit; ++s) {
+        const float2 ml = p.stats[(s * p.stat_rows + stat) * p.num_heads + head];
+        if (ml.y == 0.f) continue;
+        if (!(ml.y > 0.f)) return ml.y;   // NaN
+        const float up = fmaxf(top, ml.x);
+        sum = (sum > 0.f ? sum * fast_exp2(top - up) : 0.f) + ml.y * fast_exp2(ml.x - up);
+        top = up;
+    }
+    return sum > 0.f ? top + log2f(sum) : INFINITY;
+}
+
+struct EvictParams {
+    const float *weights;         // [num_seqs, num_kv_heads, weights_stride]
+    float *new_weights;           // [num_seqs, num_kv_heads, new_weights_stride]
+    int32_t *kept;                // [num_seqs, num_kv_heads, kept_stride]
+    int64_t weights_stride, new_weights_stride, kept_stride;
+    void *k_cache, *v_cache;      // [num_blocks, block_size, num_kv_heads, row_bytes]
+    const int32_t *block_tables;  // [num_seqs, max_blocks]
+    const int32_t *new_tables;    // [num_seqs, max_new_blocks]
+    const int32_t *context_lens, *keep_lens;
+    int num_seqs, num_kv_heads, row_bytes, block_size, max_blocks, max_new_blocks, num_blocks;
+    int max_ctx, max_keep;        // host bounds: what lies past them is cut
+    int sinks, recent;
+};
+
+}  // namespace pa
