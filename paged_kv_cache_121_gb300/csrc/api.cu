@@ -1050,28 +1050,37 @@ struct WeightsPlan {
     int max_count;       // query tokens of a sequence that count, at most
     bool compact;        // statistics laid out sequence by sequence (else by query token)
     int64_t stat_rows;
-    int nsplit;
+    int pair, pieces;    // 16-bit caches: prefill_weights_tc's cut
+    int nsplit;          // pieces that a row's statistics are made in
     size_t total;        // workspace bytes
 };
 
-WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms) {
-    WeightsPlan pl;
+WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms, bool tc) {
+    WeightsPlan pl{};
     pl.max_count = window > 0 ? std::min(window, max_query) : max_query;
     const int64_t compact_rows = static_cast<int64_t>(s.num_seqs) * pl.max_count;
     pl.compact = compact_rows < num_tokens;
     pl.stat_rows = std::min<int64_t>(compact_rows, num_tokens);
-    const int64_t tiles = s.num_seqs * static_cast<int64_t>(s.num_kv_heads) *
-                          cdiv64(static_cast<int64_t>(pl.max_count) * (s.num_heads / s.num_kv_heads), prefill_weights_simt_rows());
-    pl.nsplit = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>({static_cast<int64_t>(sms) * kWeightStatsCtasPerSm / std::max<int64_t>(tiles, 1),
-                              s.max_ctx / kWeightStatsMinSplit, kMaxSplits})));
+    const int64_t rows = static_cast<int64_t>(pl.max_count) * (s.num_heads / s.num_kv_heads);
+    if (tc) {
+        plan_prefill_weights_tc(s.num_seqs, s.num_kv_heads, rows, s.max_ctx, sms, &pl.pair, &pl.pieces);
+        pl.nsplit = pl.pair ? pl.pieces : 2 * pl.pieces;
+    } else {
+        const int64_t tiles = s.num_seqs * static_cast<int64_t>(s.num_kv_heads) * cdiv64(rows, prefill_weights_simt_rows());
+        pl.nsplit = static_cast<int>(std::max<int64_t>(
+            1, std::min<int64_t>({static_cast<int64_t>(sms) * kWeightStatsCtasPerSm / std::max<int64_t>(tiles, 1),
+                                  s.max_ctx / kWeightStatsMinSplit, kMaxSplits})));
+    }
     pl.total = align256(static_cast<size_t>(pl.nsplit) * pl.stat_rows * s.num_heads * sizeof(float2));
     return pl;
 }
 
 pa_status check_prefill_weights(const DecodeShape &s, int num_tokens, int max_query, int window) {
     if (num_tokens < 0 || max_query < 0 || window < 0) return PA_ERR_INVALID_ARG;
-    return check_shape(s);
+    const pa_status st = check_shape(s);
+    if (st != PA_OK) return st;
+    const int64_t rows = static_cast<int64_t>(window > 0 ? std::min(window, max_query) : max_query) * (s.num_heads / s.num_kv_heads);
+    return prefill_weights_tc_fits(s.num_seqs, s.num_kv_heads, rows, s.max_ctx) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -1840,7 +1849,9 @@ PA_API size_t pa_prefill_weights_workspace_size(int num_seqs, int num_tokens, in
     int dev;
     if (current_device(&dev) != PA_OK) return 0;
     const int sms = sm_count(dev);
-    return sms > 0 ? plan_weights(s, num_tokens, max_query_len, window, sms).total : 0;
+    if (sms <= 0) return 0;
+    return std::max(plan_weights(s, num_tokens, max_query_len, window, sms, false).total,
+                    plan_weights(s, num_tokens, max_query_len, window, sms, true).total);
 }
 
 PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, const void *query, pa_dtype q_dtype,
@@ -1865,7 +1876,8 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     if ((st = current_device(&dev)) != PA_OK) return st;
     const int sms = sm_count(dev);
     if (sms <= 0) return PA_ERR_CUDA;
-    const WeightsPlan pl = plan_weights(s, num_tokens, max_query_len, window, sms);
+    const bool tc = is16(kv_dtype);
+    const WeightsPlan pl = plan_weights(s, num_tokens, max_query_len, window, sms, tc);
     if (!workspace || workspace_bytes < pl.total || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     PrefillWeightsParams p;
     std::memset(&p, 0, sizeof p);
@@ -1891,10 +1903,15 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.window = window;
     p.compact = pl.compact;
     p.nsplit = pl.nsplit;
+    p.pair = pl.pair;
+    p.pieces = pl.pieces;
     p.scale_log2 = scale * kLog2e;
     p.decay = decay;
-    return launch_prefill_weights_simt(p, static_cast<int>(kv_dtype), head_dim, as_stream(stream)) == cudaSuccess ? PA_OK
-                                                                                                               : PA_ERR_CUDA;
+    p.status = status_word(dev);
+    if (!p.status) return PA_ERR_CUDA;
+    const cudaError_t e = tc ? launch_prefill_weights_tc(p, kv_dtype == PA_F16, head_dim, sms, as_stream(stream))
+                             : launch_prefill_weights_simt(p, head_dim, as_stream(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_evict(int32_t *kept, int64_t kept_stride, float *new_weights, int64_t new_weights_stride,

@@ -88,7 +88,10 @@ cudaError_t launch_norm_rope(NormRopeParams &p, int type, int sms, cudaStream_t 
 int64_t decode_weights_score_stride(int max_ctx);   // floats a row of scores
 cudaError_t launch_decode_weights(DecodeWeightsParams &p, int type, int head_dim, int sms, cudaStream_t stream);
 int prefill_weights_simt_rows();                    // rows of a tile
-cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int type, int head_dim, cudaStream_t stream);
+cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int head_dim, cudaStream_t stream);   // fp32
+bool prefill_weights_tc_fits(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx);
+void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces);
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 // Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid
 // (row tiles of the batch, Hkv * ntile, nsplit); `tall`: 64-row tiles, else 16.

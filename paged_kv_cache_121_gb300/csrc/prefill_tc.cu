@@ -63,6 +63,7 @@
 
 #include "internal.h"
 #include "prompt_common.cuh"
+#include "packed_math.cuh"
 #include "tcgen05.cuh"
 
 namespace pa {
@@ -166,16 +167,6 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
     return p;
 }
 
-// One lane of a converged warp, always the same: the one that issues MMAs, TMA
-// copies and commits. What the instructions take is computed from values known
-// to be uniform: an MMA then issues every 64 cycles (M = N = 128, K = 16), the
-// tensor pipe's own rate, where descriptors in per-thread registers took up to 146.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t on;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
-    return on != 0;
-}
-
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit A packed two to a column.
 __device__ __forceinline__ void tc_mma_16bit_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                 uint32_t accumulate) {
@@ -186,9 +177,6 @@ __device__ __forceinline__ void tc_mma_16bit_ts(uint32_t d_tmem, uint32_t a_tmem
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// A value all lanes hold alike, made known as such to the compiler.
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
 // Warp-wide: 128 consecutive fp32 columns of this warp's 32 lanes, one wait (in
 // the same block, so that no use is scheduled before it).
 __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
@@ -265,32 +253,10 @@ __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t (&w)[8]
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
-
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
     if constexpr (kF16) return pack_f16x2(a, b);
     else return pack_bf16x2(a, b);
-}
-
-// Two fp32 values in one register pair, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // The largest (kMax) or smallest of a row's scores, three operands at a time.

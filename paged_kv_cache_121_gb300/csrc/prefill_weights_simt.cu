@@ -27,24 +27,13 @@ constexpr int kThreads = 256;        // 16 x 16, 4 x 4 products each
 constexpr int kPitch = kSide + 4;    // floats of one dim's row
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(bf16_bits_to_float(v.x & 0xffffu), bf16_bits_to_float(v.x >> 16), bf16_bits_to_float(v.y & 0xffffu),
-                       bf16_bits_to_float(v.y >> 16));
-}
-__device__ __forceinline__ float4 load4(const __half *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
 // Rows i0 .. i0 + 63 of an operand, transposed to [dim][row]; row(i) is null for one that does not exist (zeros).
 template <int D, typename Row>
 __device__ __forceinline__ void load_tile(float *tile, Row row) {
     constexpr int kVecs = D / 4;
     for (int i = threadIdx.x; i < kSide * kVecs; i += kThreads) {
         const int r = i % kSide, c = i / kSide;
-        const auto *src = row(r);
+        const float *src = row(r);
         const float4 x = src ? load4(src + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
         float *to = tile + 4 * c * kPitch + r;
         to[0] = x.x;
@@ -73,28 +62,28 @@ __device__ __forceinline__ void tile_product(const float *held, const float *str
     }
 }
 
-template <typename T, int D>
+template <int D>
 struct Operands {
     const PrefillWeightsParams &p;
     const WeightSeq &s;
     int b, head;
     // row r of the KV head's queries
-    __device__ const T *query(int64_t r) const {
+    __device__ const float *query(int64_t r) const {
         if (r >= static_cast<int64_t>(s.count) * p.group) return nullptr;
         const int64_t token = s.q0 + r / p.group;
-        return static_cast<const T *>(p.query) + (token * p.num_heads + head * p.group + r % p.group) * D;
+        return static_cast<const float *>(p.query) + (token * p.num_heads + head * p.group + r % p.group) * D;
     }
-    __device__ const T *key(int t) const {   // (a block outside the pool reads as zeros)
+    __device__ const float *key(int t) const {   // (a block outside the pool reads as zeros)
         if (t >= s.ctx) return nullptr;
         const int blk = p.block_tables[static_cast<int64_t>(b) * p.max_blocks + t / p.block_size];
         if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) return nullptr;
         const int64_t slot = static_cast<int64_t>(blk) * p.block_size + t % p.block_size;
-        return static_cast<const T *>(p.k_cache) + (slot * p.num_kv_heads + head) * D;
+        return static_cast<const float *>(p.k_cache) + (slot * p.num_kv_heads + head) * D;
     }
 };
 
 // The rows' statistics: grid (row tiles x pieces of the context, KV heads, sequences).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     extern __shared__ __align__(16) float tiles[];
@@ -106,7 +95,7 @@ weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     const WeightSeq s = weight_seq(p, b);
     const int64_t rows = static_cast<int64_t>(s.count) * p.group, r0 = static_cast<int64_t>(tile) * kSide;
     if (r0 >= rows) return;
-    const Operands<T, D> at{p, s, b, head};
+    const Operands<D> at{p, s, b, head};
     const int last = static_cast<int>(min(rows, r0 + kSide) - 1);
     const int reach = s.sees(last / p.group);   // keys that any row of the tile sees
     const int key_tiles = (reach + kSide - 1) / kSide;
@@ -160,7 +149,7 @@ weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
 }
 
 // The sums over rows: grid (key tiles, KV heads, sequences).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     extern __shared__ __align__(16) float tiles[];
@@ -172,7 +161,7 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     const int b = blockIdx.z, head = blockIdx.y, t0 = blockIdx.x * kSide;
     const WeightSeq s = weight_seq(p, b);
     if (t0 >= s.ctx) return;
-    const Operands<T, D> at{p, s, b, head};
+    const Operands<D> at{p, s, b, head};
     const int64_t rows = static_cast<int64_t>(s.count) * p.group;
     // the first token whose queries see the tile's first key
     const int first = max(0, t0 - s.past);
@@ -212,31 +201,29 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt(const PrefillWeightsParams &p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>(2) * D * kPitch * sizeof(float);
     static unsigned long long stats_done = 0, sums_done = 0;
-    cudaError_t e = ensure_smem_limit(weight_stats_simt_kernel<T, D>, smem, stats_done);
-    if (e == cudaSuccess) e = ensure_smem_limit(weight_sums_simt_kernel<T, D>, smem, sums_done);
+    cudaError_t e = ensure_smem_limit(weight_stats_simt_kernel<D>, smem, stats_done);
+    if (e == cudaSuccess) e = ensure_smem_limit(weight_sums_simt_kernel<D>, smem, sums_done);
     if (e != cudaSuccess) return e;
     const int64_t row_tiles = (static_cast<int64_t>(p.max_count) * p.group + kSide - 1) / kSide;
     const dim3 rows(static_cast<unsigned>(row_tiles * p.nsplit), static_cast<unsigned>(p.num_kv_heads),
                     static_cast<unsigned>(p.num_seqs));
-    e = launch_kernel(weight_stats_simt_kernel<T, D>, rows, dim3(kThreads), smem, stream, 1u, p);
+    e = launch_kernel(weight_stats_simt_kernel<D>, rows, dim3(kThreads), smem, stream, 1u, p);
     if (e != cudaSuccess) return e;
     const dim3 keys(static_cast<unsigned>((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide),
                     static_cast<unsigned>(p.num_kv_heads), static_cast<unsigned>(p.num_seqs));
-    return launch_kernel(weight_sums_simt_kernel<T, D>, keys, dim3(kThreads), smem, stream, 1u, p);
+    return launch_kernel(weight_sums_simt_kernel<D>, keys, dim3(kThreads), smem, stream, 1u, p);
 }
 
 }  // namespace
 
 int prefill_weights_simt_rows() { return kSide; }
 
-cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int type, int head_dim, cudaStream_t stream) {
-    if (type == 1) return head_dim == 128 ? launch_simt<__nv_bfloat16, 128>(p, stream) : launch_simt<__nv_bfloat16, 64>(p, stream);
-    if (type == 2) return head_dim == 128 ? launch_simt<__half, 128>(p, stream) : launch_simt<__half, 64>(p, stream);
-    return head_dim == 128 ? launch_simt<float, 128>(p, stream) : launch_simt<float, 64>(p, stream);
+cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int head_dim, cudaStream_t stream) {
+    return head_dim == 128 ? launch_simt<128>(p, stream) : launch_simt<64>(p, stream);
 }
 
 }  // namespace pa

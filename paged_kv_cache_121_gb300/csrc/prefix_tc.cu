@@ -115,14 +115,6 @@ int TcCfg<D, kGroups>::max_ring_bytes() {
     return room / kStageBytes * kStageBytes;
 }
 
-// A matrix descriptor's start-address field is the byte address / 16 in its
-// low 14 bits; shared-memory addresses stay below 2^18, so the descriptor of
-// base + bytes is the base's plus bytes / 16 (no carry leaves the field).
-// Stepping by constant adds keeps the MMA thread's work per instruction to
-// one add: computed in full each time, the descriptors cost more issue time
-// than the instructions themselves at N = 64.
-__host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
-
 // A single thread's wait, and a whole warp's.
 __device__ __forceinline__ bool tc_wait(const PrefixParams &p, TcBars *bars, uint64_t *bar, uint32_t parity) {
     if (*reinterpret_cast<volatile int *>(&bars->abort_flag)) return false;

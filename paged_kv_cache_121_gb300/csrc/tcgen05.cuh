@@ -53,6 +53,27 @@ __device__ __forceinline__ void tc_mma_16bit(uint32_t d_tmem, uint64_t a_desc, u
         : "memory");
 }
 
+// A matrix descriptor's start-address field is the byte address / 16 in its
+// low 14 bits; shared-memory addresses stay below 2^18, so the descriptor of
+// base + bytes is the base's plus bytes / 16 (no carry leaves the field).
+// Stepping by constant adds keeps the MMA thread's work per instruction to
+// one add: computed in full each time, the descriptors cost more issue time
+// than the instructions themselves at N = 64.
+__host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
+
+// One lane of a converged warp, always the same: the one that issues MMAs, TMA
+// copies and commits. What the instructions take is computed from values known
+// to be uniform: an MMA then issues every 64 cycles (M = N = 128, K = 16), the
+// tensor pipe's own rate, where descriptors in per-thread registers took up to 146.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
+// A value all lanes hold alike, made known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Arrive once on the mbarrier when every tcgen05.mma this thread issued so
 // far has completed.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {

@@ -42,6 +42,8 @@ struct PrefillWeightsParams {
     int window;                   // the last so many query tokens count (0: all)
     int compact;                  // stat rows are sequence * max_count + i, else the query token's index
     int nsplit;                   // pieces of a context that a row's statistics are made in
+    int pieces, pair;             // prefill_weights_tc: ranges of keys a unit of rows is cut into; 1: a unit is two
+                                  //   row tiles, else one whose two halves of each range make a piece each
     float scale_log2, decay;
 };
 

@@ -122,6 +122,18 @@ def test_long_context_splits_and_many_rows():
         assert torch.equal(w.nan_to_num(7.0), call(paged, q, old, start, d ** -0.5, 1.0, window).nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_many_units_of_every_shape(dt):
+    """More (sequence, head, tile) units than SMs, contexts of an odd number of tiles among them, so that what a
+    CTA looks ahead to differs from unit to unit."""
+    lens = [130, 300, 77, 257, 513, 1, 700] * 9
+    qlens = [5, 300, 77, 2, 60, 1, 130] * 9
+    paged, q, old, start = problem(qlens, lens, 8, 4, 64, 16, dt, 13)
+    for window in (0, 3):
+        w = call(paged, q, old, start, 0.125, 1.0, window)
+        check_weights(w, *weights_after(paged, old, split(q, start), 0.125, 1.0, 8, window))
+
+
 def test_captured_and_replayed():
     paged, q, old, start = problem((130, 64), (1300, 64), 16, 4, 128, 16, "bf16", 11)
     old = torch.rand_like(old)
