@@ -1050,9 +1050,10 @@ struct WeightsPlan {
     int max_count;       // query tokens of a sequence that count, at most
     bool compact;        // statistics laid out sequence by sequence (else by query token)
     int64_t stat_rows;
-    int pair, pieces;    // 16-bit caches: prefill_weights_tc's cut
+    int pair, pieces, row_pieces;   // 16-bit caches: prefill_weights_tc's cut
+    int64_t ordered;     //   and the units it puts in order
     int nsplit;          // pieces that a row's statistics are made in
-    size_t total;        // workspace bytes
+    size_t offsets_at, stats_at, order_at, parts_at, total;   // workspace bytes: the counter, the rows' offsets, ...
 };
 
 WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms, bool tc) {
@@ -1063,15 +1064,22 @@ WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, in
     pl.stat_rows = std::min<int64_t>(compact_rows, num_tokens);
     const int64_t rows = static_cast<int64_t>(pl.max_count) * (s.num_heads / s.num_kv_heads);
     if (tc) {
-        plan_prefill_weights_tc(s.num_seqs, s.num_kv_heads, rows, s.max_ctx, sms, &pl.pair, &pl.pieces);
-        pl.nsplit = pl.pair ? pl.pieces : 2 * pl.pieces;
+        plan_prefill_weights_tc(s.num_seqs, s.num_kv_heads, rows, s.max_ctx, sms, &pl.pair, &pl.pieces, &pl.row_pieces,
+                                &pl.ordered);
+        pl.nsplit = pl.pair ? 2 * pl.pieces : 4 * pl.pieces;   // (the columns' halves are two pieces)
     } else {
         const int64_t tiles = s.num_seqs * static_cast<int64_t>(s.num_kv_heads) * cdiv64(rows, prefill_weights_simt_rows());
         pl.nsplit = static_cast<int>(std::max<int64_t>(
             1, std::min<int64_t>({static_cast<int64_t>(sms) * kWeightStatsCtasPerSm / std::max<int64_t>(tiles, 1),
                                   s.max_ctx / kWeightStatsMinSplit, kMaxSplits})));
     }
-    pl.total = align256(static_cast<size_t>(pl.nsplit) * pl.stat_rows * s.num_heads * sizeof(float2));
+    const size_t all = static_cast<size_t>(pl.stat_rows) * s.num_heads;
+    pl.offsets_at = 256;
+    pl.stats_at = pl.offsets_at + align256(all * sizeof(float));
+    pl.order_at = pl.stats_at + (pl.nsplit > 1 ? align256(pl.nsplit * all * sizeof(float2)) : 0);
+    pl.parts_at = pl.order_at + align256(static_cast<size_t>(pl.ordered) * sizeof(int));
+    pl.total = pl.parts_at + (pl.row_pieces > 1 ? align256(static_cast<size_t>(pl.row_pieces) * s.num_seqs * s.num_kv_heads * s.max_ctx *
+                                                           sizeof(float)) : 0);
     return pl;
 }
 
@@ -1080,6 +1088,7 @@ pa_status check_prefill_weights(const DecodeShape &s, int num_tokens, int max_qu
     const pa_status st = check_shape(s);
     if (st != PA_OK) return st;
     const int64_t rows = static_cast<int64_t>(window > 0 ? std::min(window, max_query) : max_query) * (s.num_heads / s.num_kv_heads);
+    if (s.num_heads / s.num_kv_heads > 65536) return PA_ERR_UNSUPPORTED;
     return prefill_weights_tc_fits(s.num_seqs, s.num_kv_heads, rows, s.max_ctx) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
@@ -1887,7 +1896,13 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.context_lens = context_lens;
     p.query_start = query_start;
     p.weights = weights;
-    p.stats = static_cast<float2 *>(workspace);
+    char *ws = static_cast<char *>(workspace);
+    p.counter = reinterpret_cast<int *>(ws);
+    p.offsets = reinterpret_cast<float *>(ws + pl.offsets_at);
+    p.stats = reinterpret_cast<float2 *>(ws + pl.stats_at);
+    p.order = pl.ordered ? reinterpret_cast<int *>(ws + pl.order_at) : nullptr;
+    p.parts = reinterpret_cast<float *>(ws + pl.parts_at);
+    p.row_pieces = pl.row_pieces;
     p.weights_stride = weights_stride;
     p.stat_rows = pl.stat_rows;
     p.num_seqs = num_seqs;
@@ -1895,6 +1910,7 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     p.group = num_heads / num_kv_heads;
+    p.group_div.set(p.group);
     p.block_size = block_size;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
@@ -1906,6 +1922,9 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.pair = pl.pair;
     p.pieces = pl.pieces;
     p.scale_log2 = scale * kLog2e;
+    // masked scores are infinities before the scale on the tensor cores: a zero scale would make them
+    // NaN; the smallest normal number gives the same weights, all alike
+    if (tc && std::fabs(p.scale_log2) < FLT_MIN) p.scale_log2 = FLT_MIN;
     p.decay = decay;
     p.status = status_word(dev);
     if (!p.status) return PA_ERR_CUDA;

@@ -90,7 +90,8 @@ cudaError_t launch_decode_weights(DecodeWeightsParams &p, int type, int head_dim
 int prefill_weights_simt_rows();                    // rows of a tile
 cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int head_dim, cudaStream_t stream);   // fp32
 bool prefill_weights_tc_fits(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx);
-void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces);
+void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces,
+                             int *row_pieces, int64_t *ordered);
 cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 // Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid

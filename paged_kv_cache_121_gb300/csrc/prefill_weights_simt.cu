@@ -143,8 +143,7 @@ weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
         for (int d = 1; d < 16; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         const int64_t r = r0 + 4 * y + i;
         if (x == 0 && r < rows)
-            p.stats[(piece * p.stat_rows + s.stat0 + r / p.group) * p.num_heads + head * p.group + r % p.group] =
-                make_float2(top, sum);
+            leave_stats(p, piece, s.stat0 + r / p.group, static_cast<int>(head * p.group + r % p.group), top, sum);
     }
 }
 
@@ -174,7 +173,7 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
         if (threadIdx.x < kSide) {
             const int64_t r = r0 + threadIdx.x;
             const bool live = r < rows;
-            offset[threadIdx.x] = live ? row_offset(p, s.stat0 + r / p.group, static_cast<int>(head * p.group + r % p.group)) : INFINITY;
+            offset[threadIdx.x] = live ? p.offsets[(s.stat0 + r / p.group) * p.num_heads + head * p.group + r % p.group] : INFINITY;
             sees[threadIdx.x] = live ? s.sees(static_cast<int>(r / p.group)) : 0;
         }
         __syncthreads();
@@ -201,6 +200,12 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     }
 }
 
+__global__ void __launch_bounds__(kThreads) weight_offsets_kernel(const __grid_constant__ PrefillWeightsParams p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    merge_stats(p, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x);
+}
+
 template <int D>
 cudaError_t launch_simt(const PrefillWeightsParams &p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>(2) * D * kPitch * sizeof(float);
@@ -212,6 +217,9 @@ cudaError_t launch_simt(const PrefillWeightsParams &p, cudaStream_t stream) {
     const dim3 rows(static_cast<unsigned>(row_tiles * p.nsplit), static_cast<unsigned>(p.num_kv_heads),
                     static_cast<unsigned>(p.num_seqs));
     e = launch_kernel(weight_stats_simt_kernel<D>, rows, dim3(kThreads), smem, stream, 1u, p);
+    if (e == cudaSuccess && p.nsplit > 1)
+        e = launch_kernel(weight_offsets_kernel, dim3(static_cast<unsigned>((p.stat_rows * p.num_heads + kThreads - 1) / kThreads)),
+                          dim3(kThreads), 0, stream, 1u, p);
     if (e != cudaSuccess) return e;
     const dim3 keys(static_cast<unsigned>((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide),
                     static_cast<unsigned>(p.num_kv_heads), static_cast<unsigned>(p.num_seqs));

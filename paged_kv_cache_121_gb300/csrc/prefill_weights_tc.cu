@@ -1,7 +1,7 @@
 // The weights that several query tokens a sequence gave each cached token, on the
 // fifth-generation tensor cores (tcgen05 + tensor memory): 16-bit caches, any block size.
 //
-// Mathematics: prefill_weights_simt.cu. Two kernels, one skeleton: scores of 128 x 128
+// Mathematics: prefill_weights_simt.cu. Two passes, one skeleton: scores of 128 x 128
 // (M = rows that are held, N = rows that are streamed, K = head_dim) land in tensor
 // memory with a held row a lane, so that what is reduced over lies along a thread's own
 // columns:
@@ -9,26 +9,27 @@
 //    maximum and sum of 2^(s - maximum);
 //  * sums: keys held, query rows streamed; a thread adds up 2^(s - o_row) for its key.
 //
-// Bound: the exponentials, two a (row, key) pair at 16 a cycle and SM, four times the
-// time of the products; for windows of few queries, reading K twice. So the tensor
-// cores run ahead and the exponentials never wait: persistent CTAs, one an SM, of
-//  * warps 0-3 and 4-7: two groups, each with a tile of scores in work and one behind
-//    it (4 x 128 columns of tensor memory);
-//  * warp 8: issues the products;
-//  * warp 9: fetches the held tiles, warps 10 and 11 the streamed ones in turn, by 16-byte
-//    asynchronous copies laid out as the 128-byte swizzled K-major operand (row r's chunk
-//    c at c ^ (r & 7)): rows are gathered one by one, so blocks of any size and rows of
-//    several query heads cost the same. A warp has up to two tiles on their way, and
-//    makes a tile's copies visible to the tensor cores (fence.proxy.async) before it
-//    reports it. Each slot is filled by one warp alone, so that the warp that waits for it
-//    has seen every earlier phase of its barriers.
+// Bound: the products and the exponentials, 512 cycles a tile each (two passes: twice
+// the products and exponentials of one attention's scores); for windows of few queries,
+// reading K twice. So neither waits for the other. Persistent CTAs, one an SM, of
+//  * warps 0-7 and 8-15: two groups, each with a tile of scores in work and one behind
+//    it (4 x 128 columns of tensor memory), two warps a lane quarter, so that a scheduler
+//    has four warps to hide an exponential's latency with;
+//  * warp 16: issues the products;
+//  * warps 17-20: fetch the tiles, 32 rows of each a warp, by 16-byte asynchronous copies
+//    laid out as the 128-byte swizzled K-major operand (row r's chunk c at c ^ (r & 7)).
+//    Rows are gathered one by one, so blocks of any size and rows of several query heads
+//    cost the same; up to two tiles of a warp are on their way, and it makes a tile's
+//    copies visible to the tensor cores (fence.proxy.async) before it reports them. (TMA
+//    gathers of four rows: 80 cycles each, a third of this rate.) The first of them
+//    draws the units and lays them out in a ring of shared memory for all others.
 // A unit holds two tiles, one a group, so that a streamed tile feeds 256 held rows;
 // where a KV head has 128 query rows or less, a unit of the statistics holds one, and
-// the groups take every other key tile. Held tiles are double-buffered: the next unit's
-// are fetched while this one's are in use. Units go round the CTAs back and forth,
-// longest first.
+// the groups take every other key tile. Long units first; those of the sums, whose
+// lengths differ most, are drawn from a counter, those of the statistics (cut into
+// pieces of the context) go round the CTAs back and forth.
 // Every wait is bounded; on expiry the kernel records a timeout, waits (bounded) for its
-// products, frees its tensor memory and returns.
+// products and copies, frees its tensor memory and returns.
 #include <algorithm>
 
 #include "internal.h"
@@ -41,13 +42,15 @@ namespace pa {
 namespace {
 
 constexpr int kSide = 128;               // rows of a tile, either side
-constexpr int kGroupWarps = 4;
+constexpr int kGroupWarps = 8;           // two for each 32 lanes of tensor memory: columns 0 .. 63 and 64 .. 127
 constexpr int kMmaWarp = 2 * kGroupWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
-constexpr int kStreamWarps = 2;          // behind the one that fetches held tiles (12 warps: 168 registers a thread)
-constexpr int kThreads = 32 * (kLoadWarp + 1 + kStreamWarps);
+constexpr int kLoadWarps = 4;            // 32 rows of every tile each (21 warps: 96 registers a thread)
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr int kTileSpace = 192 * 1024;   // shared memory for tiles
 constexpr int kMaxSlots = 12;
+constexpr int kUnits = 4;                // units laid out ahead
+constexpr int kLongUnit = 4;             // streamed tiles of a unit that is not fetched ahead
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -57,25 +60,40 @@ struct TcTile {
     static constexpr int kSlots = kTileSpace / kBytes;
     static constexpr int kChunks = D / 8;              // 16-byte chunks of a row
     static_assert(kSlots <= kMaxSlots, "barriers for every slot");
-    static_assert((kSlots - 2) % kStreamWarps == 0 && (kSlots - 4) % kStreamWarps == 0, "a streamed slot has one warp that fills it");
+};
+
+// A unit of work.
+struct Unit {
+    int b, head, tile;   // the first of the held tiles (b negative: no more units)
+    int held;            // tiles held: 1 or 2
+    int piece;
+    int lo, hi;          // streamed tiles
+    int from[2], to[2];  // those that each group scores: from .. to - 1
+    int rows;            // query rows of the KV head
+    WeightSeq s;
 };
 
 struct Shared {
+    uint64_t unit_full[kUnits], unit_empty[kUnits];
     uint64_t held_full[2][2], held_empty[2][2];   // [tile][buffer]
     uint64_t str_full[kMaxSlots], str_empty[kMaxSlots];
-    uint64_t s_full[2][2], s_free[2][2];       // [group][buffer of scores]
-    uint64_t off_full[2][2];                   // [group][buffer of offsets]
+    uint64_t s_full[2][2], s_free[2][2];          // [group][buffer of scores]
+    uint64_t part_full[2], part_free[2];          // [group]
     uint64_t done;
     uint32_t tmem;
     int abort_flag;
-    __align__(16) float off[2][2][kSide];      // [group][buffer]: what to take from the scores of each streamed row
+    Unit unit[kUnits];
+    __align__(16) float off[2 * kGroupWarps][kSide / 2];   // [warp]: minus what to take from its streamed rows' scores
+    float part[2][kSide];                         // [group]: the sums over the second half of the columns
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
-    const int bytes = live ? 16 : 0;   // (the rest is filled with zeros)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void *src, bool live) {
+    const int bytes = live ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void copy_wait() {
@@ -95,121 +113,193 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-
-// A unit of work, the same in every thread.
-struct Unit {
-    int k;             // its place in the CTA's list (negative: none)
-    int b, head, tile; // the first of the held tiles
-    int held;          // tiles held: 1 or 2
-    int piece;
-    int lo, hi;        // streamed tiles
-    int from0, from1, to0, to1;   // those that each group scores: from .. to - 1
-    WeightSeq s;
-    __device__ __forceinline__ int from(int g) const { return g ? from1 : from0; }
-    __device__ __forceinline__ int to(int g) const { return g ? to1 : to0; }
-};
 
 template <bool kSums>
 __host__ __device__ __forceinline__ int64_t unit_count(const PrefillWeightsParams &p) {
     const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-    if (kSums) return (static_cast<int64_t>(p.max_ctx) + 2 * kSide - 1) / (2 * kSide) * heads;
+    if (kSums) return (static_cast<int64_t>(p.max_ctx) + 2 * kSide - 1) / (2 * kSide) * p.row_pieces * heads;
     const int64_t side = p.pair ? 2 * kSide : kSide;
     return (static_cast<int64_t>(p.max_count) * p.group + side - 1) / side * p.pieces * heads;
 }
 
-// The CTA's next unit with anything in it, from place k on. (Units, rows and keys fit 30 bits.)
-template <bool kSums>
-__device__ __forceinline__ Unit next_unit(const PrefillWeightsParams &p, int k) {
-    const unsigned heads = p.num_seqs * p.num_kv_heads, units = static_cast<unsigned>(unit_count<kSums>(p));
-    Unit u;
-    for (;; ++k) {
-        u.k = -1;
-        if (k * gridDim.x >= units) return u;
-        const unsigned at = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (at >= units) continue;
-        const unsigned order = at / heads, bh = at - order * heads;
-        u.b = static_cast<int>(bh / static_cast<unsigned>(p.num_kv_heads));
-        u.head = static_cast<int>(bh) - u.b * p.num_kv_heads;
-        u.s = weight_seq(p, u.b);
-        const int rows = u.s.count * p.group;
-        const int row_tiles = (rows + kSide - 1) / kSide, key_tiles = (u.s.ctx + kSide - 1) / kSide;
-        if (kSums) {   // the first keys are seen by most rows
-            u.tile = static_cast<int>(order) * 2;
-            if (u.tile >= key_tiles) continue;
-            u.held = min(2, key_tiles - u.tile);
-            u.piece = 0;
-            auto first = [&](int tile) {   // the first row tile that sees the key tile
-                const int64_t token = static_cast<int64_t>(tile) * kSide - u.s.past;
-                return token <= 0 ? 0 : token >= u.s.count ? row_tiles : static_cast<int>(token) * p.group / kSide;
-            };
-            u.from0 = first(u.tile);
-            u.from1 = u.held > 1 ? first(u.tile + 1) : row_tiles;
-            u.hi = u.to0 = u.to1 = row_tiles;
-            u.lo = min(u.from0, u.from1);
-        } else {       // the last rows see most keys
-            const int per_unit = p.pair ? 2 : 1;
-            const int all = (p.max_count * p.group + per_unit * kSide - 1) / (per_unit * kSide);
-            const int row_unit = static_cast<int>(order) / p.pieces;
-            u.piece = static_cast<int>(order) - row_unit * p.pieces;
-            u.tile = (all - 1 - row_unit) * per_unit;
-            if (u.tile >= row_tiles) continue;
-            u.held = min(per_unit, row_tiles - u.tile);
-            auto end = [&](int tile) {     // one past the last key tile that the row tile sees
-                const int row = min(rows, (tile + 1) * kSide) - 1;
-                return (u.s.sees(row / p.group) + kSide - 1) / kSide;
-            };
-            const int end0 = end(u.tile), end1 = u.held > 1 ? end(u.tile + 1) : 0;
-            const int most = max(end0, end1), per = (most + p.pieces - 1) / p.pieces;
-            u.lo = min(most, u.piece * per);
-            u.hi = min(most, u.lo + per);
-            u.from0 = u.from1 = u.lo;
-            u.to0 = p.pair ? min(u.hi, end0) : u.hi;
-            u.to1 = p.pair ? min(u.hi, end1) : u.hi;
-        }
-        u.k = k;
-        return u;
-    }
+// The row tiles of a unit of keys, numbered (pair of key tiles x piece of the rows) x sequence: those that each
+// group scores. False where there is nothing in it.
+__device__ __forceinline__ bool lay_out_sums(const PrefillWeightsParams &p, int n, Unit &u) {
+    const int order = n / p.num_seqs, pair = order / p.row_pieces;
+    u.b = n - order * p.num_seqs;
+    u.piece = order - pair * p.row_pieces;
+    u.s = weight_seq(p, u.b);
+    u.rows = u.s.count * p.group;
+    const int row_tiles = (u.rows + kSide - 1) / kSide, key_tiles = (u.s.ctx + kSide - 1) / kSide;
+    u.tile = pair * 2;
+    u.lo = u.hi = 0;
+    if (u.tile >= key_tiles) return false;
+    u.held = min(2, key_tiles - u.tile);
+    auto first = [&](int tile) {   // the first row tile that sees the key tile
+        const int64_t token = static_cast<int64_t>(tile) * kSide - u.s.past;
+        return token <= 0 ? 0 : token >= u.s.count ? row_tiles : static_cast<int>(token) * p.group / kSide;
+    };
+    const int from0 = first(u.tile), from1 = u.held > 1 ? first(u.tile + 1) : row_tiles;
+    const int lo = min(from0, from1), per = (row_tiles - lo + p.row_pieces - 1) / p.row_pieces;
+    u.lo = min(row_tiles, lo + u.piece * per);
+    u.hi = min(row_tiles, u.lo + per);
+    u.from[0] = max(from0, u.lo);
+    u.from[1] = max(from1, u.lo);
+    u.to[0] = u.to[1] = u.hi;
+    return true;
 }
 
+// Unit number `at`, longest first; false where there is nothing in it. (Units, rows and keys fit 30 bits.)
+template <bool kSums>
+__device__ __forceinline__ bool lay_out(const PrefillWeightsParams &p, unsigned at, Unit &u) {
+    if (kSums) {
+        const int n = static_cast<int>(at / static_cast<unsigned>(p.num_kv_heads));
+        u.head = static_cast<int>(at) - n * p.num_kv_heads;
+        return lay_out_sums(p, p.order ? p.order[n] : n, u);
+    }
+    const unsigned heads = p.num_seqs * p.num_kv_heads, order = at / heads, bh = at - order * heads;
+    u.b = static_cast<int>(bh / static_cast<unsigned>(p.num_kv_heads));
+    u.head = static_cast<int>(bh) - u.b * p.num_kv_heads;
+    u.s = weight_seq(p, u.b);
+    u.rows = u.s.count * p.group;
+    const int row_tiles = (u.rows + kSide - 1) / kSide;
+    // the last rows see most keys
+    const int per_unit = p.pair ? 2 : 1;
+    const int all = (p.max_count * p.group + per_unit * kSide - 1) / (per_unit * kSide);
+    const int row_unit = static_cast<int>(order) / p.pieces;
+    u.piece = static_cast<int>(order) - row_unit * p.pieces;
+    u.tile = (all - 1 - row_unit) * per_unit;
+    if (u.tile >= row_tiles) return false;
+    u.held = min(per_unit, row_tiles - u.tile);
+    auto end = [&](int tile) {     // one past the last key tile that the row tile sees
+        const int row = min(u.rows, (tile + 1) * kSide) - 1;
+        return (u.s.sees(row / p.group) + kSide - 1) / kSide;
+    };
+    const int end0 = end(u.tile), end1 = u.held > 1 ? end(u.tile + 1) : 0;
+    const int most = max(end0, end1), per = (most + p.pieces - 1) / p.pieces;
+    u.lo = min(most, u.piece * per);
+    u.hi = min(most, u.lo + per);
+    u.from[0] = u.from[1] = u.lo;
+    u.to[0] = p.pair ? min(u.hi, end0) : u.hi;
+    u.to[1] = p.pair ? min(u.hi, end1) : u.hi;
+    return true;
+}
+
+// mbar_try_wait, suspended until the phase completes or some 20 us are over: 20 warps that poll would take the issue
+// slots of those that compute.
+__device__ __forceinline__ bool mbar_doze(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait_one(const PrefillWeightsParams &p, Shared *sh, uint64_t *bar, int parity) {
-    if (*reinterpret_cast<volatile int *>(&sh->abort_flag)) return false;
-    if (mbar_wait(smem_addr(bar), parity)) return true;
-    record_status(p.status, kStatusTimeout);
-    *reinterpret_cast<volatile int *>(&sh->abort_flag) = 1;
+    if (mbar_doze(smem_addr(bar), parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!*reinterpret_cast<volatile int *>(&sh->abort_flag)) {
+        if (mbar_doze(smem_addr(bar), parity)) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            record_status(p.status, kStatusTimeout);
+            *reinterpret_cast<volatile int *>(&sh->abort_flag) = 1;
+        }
+    }
     return false;
 }
+// A whole warp's wait: the answer is the same in all its lanes.
 __device__ __forceinline__ bool wait_warp(const PrefillWeightsParams &p, Shared *sh, uint64_t *bar, int parity) {
-    return mbar_wait_warp(smem_addr(bar), parity, p.status, &sh->abort_flag);
+    if (__all_sync(0xffffffffu, mbar_doze(smem_addr(bar), parity))) return true;
+    return __all_sync(0xffffffffu, wait_one(p, sh, bar, parity));
+}
+
+// Sum of 2^(s * scale - offset) over 32 streamed rows; kMasked: only over columns see .. end - 1.
+template <bool kMasked>
+__device__ __forceinline__ float sum_weights(const float (&s)[32], const float *minus_off, uint64_t scale2, int see, int end) {
+    uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        const float4 o = *reinterpret_cast<const float4 *>(minus_off + c);
+        float e[4];
+        unpair(fma2(pair(s[c], s[c + 1]), scale2, pair(o.x, o.y)), e[0], e[1]);
+        unpair(fma2(pair(s[c + 2], s[c + 3]), scale2, pair(o.z, o.w)), e[2], e[3]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            e[n] = fast_exp2(e[n]);
+            if (kMasked && (c + n < see || c + n >= end)) e[n] = 0.f;
+        }
+        acc[0] = add2(acc[0], pair(e[0], e[1]));
+        acc[1] = add2(acc[1], pair(e[2], e[3]));
+    }
+    float a, b;
+    unpair(add2(acc[0], acc[1]), a, b);
+    return a + b;
+}
+
+// A row's maximum (raw scores, times the scale's sign) and sum of 2^(s * scale - maximum) go on with 32 keys.
+template <bool kNegative>
+__device__ __forceinline__ void add_stats(const float (&s)[32], uint64_t scale2, float scale, float &top, float &sum) {
+    float best[4] = {top, top, top, top};
+#pragma unroll
+    for (int c = 0; c < 32; c += 8)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            best[n] = kNegative ? max3(best[n], -s[c + 2 * n], -s[c + 2 * n + 1]) : max3(best[n], s[c + 2 * n], s[c + 2 * n + 1]);
+    const float up = max3(fmaxf(best[0], best[1]), best[2], best[3]);
+    const float size = fabsf(scale), ref = up == -INFINITY ? 0.f : up * size;   // (nothing seen yet: 2^-inf = 0)
+    sum *= fast_exp2(top * size - ref);
+    top = up;
+    const uint64_t minus = pair(-ref, -ref);
+    uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        float a, b;
+        unpair(fma2(pair(s[2 * c], s[2 * c + 1]), scale2, minus), a, b);
+        acc[c & 1] = add2(acc[c & 1], pair(fast_exp2(a), fast_exp2(b)));
+    }
+    float a, b;
+    unpair(add2(acc[0], acc[1]), a, b);
+    sum += a + b;
 }
 
 template <int D, bool kF16, bool kSums>
 __global__ void __launch_bounds__(kThreads, 1)
-prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
+prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p, const int held_buffers) {
     using T = TcTile<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Shared *sh = reinterpret_cast<Shared *>(tiles + kTileSpace);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per_unit = kSums || p.pair ? 2 : 1;
-    const int str_slots = T::kSlots - 2 * per_unit;      // streamed tiles, behind two buffers of held ones
+    const bool split = !kSums && !p.pair;                // the groups take every other streamed tile of one held tile
+    const int held_slots = (split ? 1 : 2) * held_buffers;
+    const int str_slots = T::kSlots - held_slots;        // streamed tiles, behind the held ones
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i)
             for (int j = 0; j < 2; ++j) {
-                mbar_init(smem_addr(&sh->held_full[i][j]), 1);
+                mbar_init(smem_addr(&sh->held_full[i][j]), kLoadWarps);
                 mbar_init(smem_addr(&sh->held_empty[i][j]), 1);
                 mbar_init(smem_addr(&sh->s_full[i][j]), 1);
                 mbar_init(smem_addr(&sh->s_free[i][j]), kGroupWarps);
-                mbar_init(smem_addr(&sh->off_full[i][j]), kGroupWarps);
             }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh->part_full[i]), kGroupWarps / 2);
+            mbar_init(smem_addr(&sh->part_free[i]), kGroupWarps / 2);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(smem_addr(&sh->unit_full[i]), 1);
+            mbar_init(smem_addr(&sh->unit_empty[i]), 2 * kGroupWarps + 1 + kLoadWarps - 1);   // (all but the one that lays them out)
         }
         for (int i = 0; i < kMaxSlots; ++i) {
-            mbar_init(smem_addr(&sh->str_full[i]), 1);
+            mbar_init(smem_addr(&sh->str_full[i]), kLoadWarps);
             mbar_init(smem_addr(&sh->str_empty[i]), 1);
         }
         mbar_init(smem_addr(&sh->done), 1);
@@ -222,66 +312,70 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    // scores of group g, buffer n
-    auto s_col = [&](int g, int n) { return tmem + static_cast<uint32_t>((2 * g + n) * kSide); };
+
+    // unit k of this CTA, for a warp that has read what it needs of it
+    auto unit_ready = [&](int k) { return wait_warp(p, sh, &sh->unit_full[k % kUnits], (k / kUnits) & 1); };
+    auto unit_read = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->unit_empty[k % kUnits]));
+    };
 
     if (warp >= kLoadWarp) {
-        // -------------------------------- loaders --------------------------------
-        const bool holds = warp == kLoadWarp;
-        const int mine = warp - kLoadWarp - 1;
-        bool ok = true;
+        // ---------------------------- units and tiles ----------------------------
+        const int mine = warp - kLoadWarp;
+        const uint32_t base = smem_addr(tiles) + mine * 32 * 128;   // this warp's rows of the first slot
         uint64_t *pending = nullptr;   // the barrier of the tile that is on its way
-        auto report = [&]() {          // the pending tile has arrived
+        auto report = [&]() {          // its rows have arrived
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(pending));
             pending = nullptr;
         };
-        // Fetch a tile into dst once `empty` has completed the phase of this parity (negative: it is free).
-        auto fetch = [&](const Unit &u, bool keys, int tile, uint32_t dst, uint64_t *full, uint64_t *empty, int parity) {
-            if (parity >= 0) {
-                if (pending && !__all_sync(0xffffffffu, mbar_test(smem_addr(empty), parity))) {
-                    copy_wait<0>();   // what the others wait for is reported before this warp waits for them
-                    report();
-                }
-                if (!wait_warp(p, sh, empty, parity)) return false;
+        // What others wait for is reported before this warp waits for them.
+        auto wait_for = [&](uint64_t *bar, int parity) {
+            if (pending && !__all_sync(0xffffffffu, mbar_test(smem_addr(bar), parity))) {
+                copy_wait<0>();
+                report();
             }
-            const int rows = u.s.count * p.group;
-            const uint16_t *row[4];
-            if (keys) {
-                const int32_t *table = p.block_tables + static_cast<int64_t>(u.b) * p.max_blocks;
-                int blk[4], at[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int t = tile * kSide + n * 32 + lane;
-                    at[n] = t < u.s.ctx ? t % p.block_size : 0;
-                    blk[n] = t < u.s.ctx ? table[t / p.block_size] : -1;
-                }
-#pragma unroll
-                for (int n = 0; n < 4; ++n)   // (a block outside the pool reads as zeros)
-                    row[n] = static_cast<unsigned>(blk[n]) < static_cast<unsigned>(p.num_blocks)
-                                 ? static_cast<const uint16_t *>(p.k_cache) +
-                                       ((static_cast<int64_t>(blk[n]) * p.block_size + at[n]) * p.num_kv_heads + u.head) * D
-                                 : nullptr;
-            } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int r = tile * kSide + n * 32 + lane, token = r / p.group;
-                    row[n] = r < rows ? static_cast<const uint16_t *>(p.query) +
-                                            ((static_cast<int64_t>(u.s.q0) + token) * p.num_heads + u.head * p.group + r - token * p.group) * D
-                                      : nullptr;
-                }
+            return wait_warp(p, sh, bar, parity);
+        };
+        // The lane's row of a tile (none: zeros, as for a block outside the pool).
+        auto locate = [&](const Unit &u, bool keys, int tile) {
+            const int r = tile * kSide + mine * 32 + lane;
+            const uint16_t *row = nullptr;
+            if (keys && r < u.s.ctx) {
+                const int j = r / p.block_size, blk = p.block_tables[static_cast<int64_t>(u.b) * p.max_blocks + j];
+                if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks))
+                    row = static_cast<const uint16_t *>(p.k_cache) +
+                          ((static_cast<int64_t>(blk) * p.block_size + (r - j * p.block_size)) * p.num_kv_heads + u.head) * D;
+            } else if (!keys && r < u.rows) {
+                const int token = r / p.group;
+                row = static_cast<const uint16_t *>(p.query) +
+                      ((static_cast<int64_t>(u.s.q0) + token) * p.num_heads + u.head * p.group + r - token * p.group) * D;
             }
+            return row;
+        };
+        // Fetch a tile's rows once `empty` has completed the phase of this parity (negative: the slot is free).
+        auto fetch = [&](const uint16_t *row, int slot, uint64_t *full, uint64_t *empty, int parity) {
+            if (parity >= 0 && !wait_for(empty, parity)) return false;
+            // A lane copies chunk c of every kStep-th row. Several rows' places are read at a time: a copy is ordered
+            // behind the reads before it.
+            constexpr int kStep = 32 / T::kChunks;
+            const int r0 = lane / T::kChunks, c = lane % T::kChunks;
+            const uint32_t to = base + slot * T::kBytes + (c >> 3) * T::kHalf + r0 * 128;
+            const bool all = __all_sync(0xffffffffu, row != nullptr);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int i0 = 0; i0 < T::kChunks; i0 += 8) {
+                const uint16_t *src[8];
 #pragma unroll
-                for (int i = 0; i < T::kChunks; ++i) {
-                    const int at = i * 32 + lane, r = at / T::kChunks, c = at % T::kChunks;
-                    const uint16_t *src = reinterpret_cast<const uint16_t *>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row[n]), r));
-                    const int R = n * 32 + r;
-                    copy16(dst + (c >> 3) * T::kHalf + R * 128 + (((c & 7) ^ (R & 7)) << 4),
-                           src ? src + c * 8 : static_cast<const uint16_t *>(p.query), src != nullptr);
+                for (int i = 0; i < 8; ++i)
+                    src[i] = reinterpret_cast<const uint16_t *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r0 + (i0 + i) * kStep));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t dst = to + (i0 + i) * kStep * 128 + (((c & 7) ^ ((r0 + (i0 + i) * kStep) & 7)) << 4);
+                    if (all) copy16(dst, src[i] + c * 8);
+                    else copy16_or_zeros(dst, src[i] ? src[i] + c * 8 : static_cast<const uint16_t *>(p.query), src[i] != nullptr);
                 }
             }
             copy_commit();
@@ -292,26 +386,57 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
             pending = full;
             return true;
         };
-        const uint32_t base = smem_addr(tiles);
-        int held[2] = {0, 0}, streamed = 0;
-        for (Unit u = next_unit<kSums>(p, 0); u.k >= 0 && ok; u = next_unit<kSums>(p, u.k + 1)) {
-            if (u.lo >= u.hi) continue;
-            if (holds) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i >= u.held || !ok) break;
-                    const int n = held[i]++, buf = n & 1;
-                    ok = fetch(u, kSums, u.tile + i, base + (2 * i + buf) * T::kBytes, &sh->held_full[i][buf],
-                               &sh->held_empty[i][buf], n >= 2 ? ((n >> 1) - 1) & 1 : -1);
+        const unsigned units = static_cast<unsigned>(unit_count<kSums>(p));
+        unsigned turn = 0, at = blockIdx.x;
+        int count[2] = {0, 0}, streamed = 0;   // held tiles so far, first and second of a unit; streamed ones
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            Unit u;
+            if (mine == 0) {
+                // Long units of the sums are drawn, once the tiles of the one before are on their way: drawn earlier they
+                // would wait here while other CTAs have none. Others go round the CTAs back and forth (a draw would
+                // take as long as a short unit).
+                const bool draws = kSums && held_buffers == 1;
+                bool found = false;
+                while (!found && (at < units || (!draws && turn * gridDim.x < units))) {
+                    if (at < units) found = lay_out<kSums>(p, at, u);
+                    if (draws) {
+                        if (lane == 0) at = gridDim.x + atomicAdd(p.counter, 1);
+                        at = __shfl_sync(0xffffffffu, at, 0);
+                    } else {
+                        ++turn;
+                        at = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    }
                 }
-                continue;
+                if (!found) u.b = -1;
+                if (k >= kUnits && !wait_for(&sh->unit_empty[k % kUnits], (k / kUnits - 1) & 1)) break;
+                if (lane == 0) {
+                    sh->unit[k % kUnits] = u;
+                    mbar_arrive(smem_addr(&sh->unit_full[k % kUnits]));
+                }
+            } else {
+                if (!wait_for(&sh->unit_full[k % kUnits], (k / kUnits) & 1)) break;
+                u = sh->unit[k % kUnits];
+                unit_read(k);
             }
-            for (int i = u.lo + ((mine ^ streamed) & 1); i < u.hi && ok; i += kStreamWarps) {
-                const int n = streamed + i - u.lo, slot = n % str_slots, round = n / str_slots;
-                ok = fetch(u, !kSums, i, base + (2 * per_unit + slot) * T::kBytes, &sh->str_full[slot], &sh->str_empty[slot],
+            if (u.b < 0) break;
+            if (u.lo >= u.hi) continue;
+            // (a tile's rows are looked up while the one before is sent for)
+            const uint16_t *held[2] = {locate(u, kSums, u.tile), u.held > 1 ? locate(u, kSums, u.tile + 1) : nullptr};
+            const uint16_t *next = locate(u, !kSums, u.lo);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i >= u.held || !ok) break;
+                const int n = count[i]++, round = n / held_buffers, buf = n - round * held_buffers;
+                ok = fetch(held[i], i * held_buffers + buf, &sh->held_full[i][buf], &sh->held_empty[i][buf],
                            round > 0 ? (round - 1) & 1 : -1);
             }
-            streamed += u.hi - u.lo;
+            for (int i = u.lo; i < u.hi && ok; ++i, ++streamed) {
+                const uint16_t *row = next;
+                if (i + 1 < u.hi) next = locate(u, !kSums, i + 1);
+                const int round = streamed / str_slots, slot = streamed - round * str_slots;
+                ok = fetch(row, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], round > 0 ? (round - 1) & 1 : -1);
+            }
         }
         copy_wait<0>();
         if (pending) report();
@@ -319,41 +444,52 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
         // ------------------------------ products ------------------------------
         constexpr uint32_t id = idesc_16bit_f32(kSide, kSide, false, false, kF16);
         const uint64_t first_tile = smem_desc_sw128(smem_addr(tiles), 16, 1024);
+        auto tile_at = [&](int slot) { return first_tile + static_cast<uint32_t>(slot) * static_cast<uint32_t>(T::kBytes >> 4); };
         int holds[2] = {0, 0}, streamed = 0, count[2] = {0, 0};
         bool ok = true;
-        for (Unit u = next_unit<kSums>(p, 0); u.k >= 0 && ok; u = next_unit<kSums>(p, u.k + 1)) {
-            const int lo = uniform(u.lo), hi = uniform(u.hi), held = uniform(u.held);
+        for (int k = 0; ok && unit_ready(k); ++k) {
+            const Unit *u = &sh->unit[k % kUnits];
+            const int b = uniform(u->b), lo = uniform(u->lo), hi = uniform(u->hi), held = uniform(u->held);
+            const int from[2] = {uniform(u->from[0]), uniform(u->from[1])}, to[2] = {uniform(u->to[0]), uniform(u->to[1])};
+            unit_read(k);
+            if (b < 0) break;
             if (lo >= hi) continue;
-            const int buf[2] = {holds[0] & 1, holds[1] & 1};
-            const int from[2] = {uniform(u.from0), uniform(u.from1)}, to[2] = {uniform(u.to0), uniform(u.to1)};
-            int counted[2] = {count[0], count[1]};
+            int round[2], buf[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                round[i] = holds[i] / held_buffers;
+                buf[i] = holds[i] - round[i] * held_buffers;
+            }
             bool fine = true;
             if (elect_one()) {
                 auto run = [&]() {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (i < held && !wait_one(p, sh, &sh->held_full[i][buf[i]], (holds[i] >> 1) & 1)) return false;
-                    int n = streamed;
-                    for (int i = lo; i < hi; ++i, ++n) {
-                        const int slot = n % str_slots;
-                        if (!wait_one(p, sh, &sh->str_full[slot], (n / str_slots) & 1)) return false;
-                        const uint64_t sd = first_tile + static_cast<uint32_t>(2 * per_unit + slot) * static_cast<uint32_t>(T::kBytes >> 4);
+                        if (i < held && !wait_one(p, sh, &sh->held_full[i][buf[i]], round[i] & 1)) return false;
+                    int counted[2] = {count[0], count[1]}, slot = streamed % str_slots, phase = (streamed / str_slots) & 1;
+                    for (int i = lo; i < hi; ++i) {
+                        if (!wait_one(p, sh, &sh->str_full[slot], phase)) return false;
+                        const uint64_t sd = tile_at(held_slots + slot);
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            if (i < from[g] || i >= to[g] || !(kSums || p.pair || ((i - lo) & 1) == g)) continue;
+                            if (i < from[g] || i >= to[g] || (split && ((i - lo) & 1) != g)) continue;
                             const int c = counted[g]++;
                             if (c >= 2 && !wait_one(p, sh, &sh->s_free[g][c & 1], ((c >> 1) - 1) & 1)) return false;
                             tc_fence_after();
-                            const int tile = per_unit == 2 ? 2 * g + buf[g] : buf[0];
-                            const uint64_t hd = first_tile + static_cast<uint32_t>(tile) * static_cast<uint32_t>(T::kBytes >> 4);
+                            const uint64_t hd = tile_at(split ? buf[0] : g * held_buffers + buf[g]);
+                            const uint32_t to_col = tmem + static_cast<uint32_t>((2 * g + (c & 1)) * kSide);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint64_t step = desc_step((kk / 4) * T::kHalf + (kk % 4) * 32);
-                                tc_mma_16bit(s_col(g, c & 1), hd + step, sd + step, id, kk > 0 ? 1u : 0u);
+                                tc_mma_16bit(to_col, hd + step, sd + step, id, kk > 0 ? 1u : 0u);
                             }
                             tc_commit(smem_addr(&sh->s_full[g][c & 1]));
                         }
                         tc_commit(smem_addr(&sh->str_empty[slot]));
+                        if (++slot == str_slots) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -368,10 +504,8 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
             ++holds[0];
             holds[1] += held > 1;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {   // what the issuing lane counted
-                const int n = max(0, min(to[g], hi) - max(from[g], lo));
-                count[g] += kSums || p.pair ? n : (hi - lo + 1 - g) / 2;
-            }
+            for (int g = 0; g < 2; ++g)   // what the issuing lane counted
+                count[g] += split ? (hi - lo + 1 - g) / 2 : max(0, min(to[g], hi) - max(from[g], lo));
         }
         if (elect_one()) {   // every product issued has run once `done` completes
             tc_commit(smem_addr(&sh->done));
@@ -380,132 +514,112 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
         __syncwarp();
     } else {
         // ------------------------------ exponentials ------------------------------
-        const int g = warp / kGroupWarps, R = (warp & 3) * 32 + lane;
+        const int g = warp / kGroupWarps, h = (warp / 4) & 1, R = (warp & 3) * 32 + lane;   // group, half of the columns, lane
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
-        int count = 0;   // tiles scored
-        bool ok = true;
-        float next_off = INFINITY;
-        // this thread's column of streamed tile i (sums: a query row)
-        auto column = [&](const Unit &u, int i) {
-            const int r = i * kSide + R, token = r / p.group;
-            const bool live = token < u.s.count;
-            next_off = live ? row_offset(p, u.s.stat0 + token, u.head * p.group + r - token * p.group) : INFINITY;
+        int count = 0;            // tiles scored
+        bool ok = true, ahead = false;
+        float next_off[2] = {0.f, 0.f};   // sums: the offsets of two of this warp's columns in the next tile, once `ahead`
+        float *const off = sh->off[warp];
+        auto columns = [&](const Unit *u, int i) {   // (loaded here, used a tile later)
+            const float *from = p.offsets + u->s.stat0 * p.num_heads + u->head * p.group;
+            const int r = i * kSide + h * 64 + lane * 2, rows = u->rows, skip = p.num_heads - p.group;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)   // (a row's place among those of all KV heads)
+                next_off[n] = r + n < rows ? from[r + n + static_cast<int64_t>(p.group_div.of(r + n)) * skip] : INFINITY;
+            ahead = true;
         };
-        Unit u = next_unit<kSums>(p, 0);
-        if (kSums && u.k >= 0 && u.from(g) < u.to(g)) column(u, u.from(g));
-        while (u.k >= 0 && ok) {
-            const Unit next = next_unit<kSums>(p, u.k + 1);
-            const int tile = kSums || p.pair ? u.tile + g : u.tile;
-            const int held_row = tile * kSide + R;
+        for (int k = 0; ok; ++k) {
+            if (!unit_ready(k)) break;
+            const Unit *u = &sh->unit[k % kUnits];   // (given back at the unit's end)
+            if (u->b < 0) break;
+            const int tile = split ? u->tile : u->tile + g;
+            const int held_row = tile * kSide + R, rows = u->rows;
             float top = -INFINITY, sum = 0.f;   // statistics: maximum and sum; sums: the sum
             int row_sees = 0, first_row = 0;    // statistics: keys that the row sees; sums: the first row that sees the key
-            if (!kSums && held_row < u.s.count * p.group) row_sees = u.s.sees(held_row / p.group);
+            int whole_from = 0, whole_to = 0;   // sums: row tiles whose rows all exist and see all of the key tile. (Rows past the
+                                                //   last one are zeros, whose products with infinite keys are no numbers)
+            if (!kSums && held_row < rows) row_sees = u->s.sees(held_row / p.group);
             if (kSums) {
-                const int64_t token = static_cast<int64_t>(held_row) - u.s.past;
-                first_row = token <= 0 ? 0 : token >= u.s.count ? u.s.count * p.group : static_cast<int>(token) * p.group;
+                const int64_t token = static_cast<int64_t>(held_row) - u->s.past;
+                first_row = token <= 0 ? 0 : token >= u->s.count ? rows : static_cast<int>(token) * p.group;
+                const int64_t all = static_cast<int64_t>(tile + 1) * kSide - 1 - u->s.past;   // the first token that sees it all
+                whole_to = (tile + 1) * kSide <= u->s.ctx && all < u->s.count ? rows / kSide : 0;
+                whole_from = all <= 0 || whole_to == 0 ? 0 : (static_cast<int>(all) * p.group + kSide - 1) / kSide;
             }
-            const int step = kSums || p.pair ? 1 : 2, last = u.to(g);
-            for (int i = u.from(g) + (step == 2 ? g : 0); i < last; i += step, ++count) {
+            const int step = split ? 2 : 1, last = u->to[g];
+            for (int i = u->from[g] + (split ? g : 0); i < last; i += step, ++count) {
                 const int buf = count & 1;
                 if (kSums) {
-                    sh->off[g][buf][R] = next_off;
+                    if (!ahead) columns(u, i);
+                    *reinterpret_cast<float2 *>(off + lane * 2) = make_float2(-next_off[0], -next_off[1]);
+                    ahead = false;
+                    if (i + 1 < last) {
+                        columns(u, i + 1);
+                    } else {   // the next unit's first tile
+                        if (!unit_ready(k + 1)) { ok = false; break; }
+                        const Unit *next = &sh->unit[(k + 1) % kUnits];
+                        if (next->b >= 0 && next->from[g] < next->to[g]) columns(next, next->from[g]);
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh->off_full[g][buf]));
-                    if (i + 1 < last) column(u, i + 1);
-                    else if (next.k >= 0 && next.from(g) < next.to(g)) column(next, next.from(g));
-                    if (!wait_warp(p, sh, &sh->off_full[g][buf], (count >> 1) & 1)) { ok = false; break; }
                 }
                 if (!wait_warp(p, sh, &sh->s_full[g][buf], (count >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float s[64];
-                    tmem_ld64(tmem + lane_off + static_cast<uint32_t>((2 * g + buf) * kSide + half * 64), s);
-                    if (half == 1) {
+                const bool whole = i >= whole_from && i < whole_to;
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    const int col = h * 64 + part * 32;
+                    float s[32];
+                    tmem_ld32(tmem + lane_off + static_cast<uint32_t>((2 * g + buf) * kSide + col), s);
+                    if (part == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&sh->s_free[g][buf]));
                     }
+                    const int c0 = i * kSide + col;   // the first column's row (statistics: key)
                     if (kSums) {
-                        const float *off = &sh->off[g][buf][half * 64];
-                        // the tile's first row sees least; rows past the last one are zeros, whose products
-                        // with an infinite key are no numbers: they see nothing
-                        const bool whole = (i + 1) * kSide <= u.s.count * p.group && (tile + 1) * kSide <= u.s.sees(i * kSide / p.group);
-                        const int c0 = i * kSide + half * 64, see = first_row - c0, end = u.s.count * p.group - c0;
-                        uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            const float4 o = *reinterpret_cast<const float4 *>(off + c);
-                            float e[4];
-                            unpair(fma2(pair(s[c], s[c + 1]), scale2, pair(-o.x, -o.y)), e[0], e[1]);
-                            unpair(fma2(pair(s[c + 2], s[c + 3]), scale2, pair(-o.z, -o.w)), e[2], e[3]);
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) e[n] = fast_exp2(e[n]);
-                            if (!whole) {
-#pragma unroll
-                                for (int n = 0; n < 4; ++n)
-                                    if (c + n < see || c + n >= end) e[n] = 0.f;
-                            }
-                            acc[0] = add2(acc[0], pair(e[0], e[1]));
-                            acc[1] = add2(acc[1], pair(e[2], e[3]));
-                        }
-                        float a, b;
-                        unpair(add2(acc[0], acc[1]), a, b);
-                        sum += a + b;
+                        sum += whole ? sum_weights<false>(s, off + part * 32, scale2, 0, 32)
+                                     : sum_weights<true>(s, off + part * 32, scale2, first_row - c0, rows - c0);
                     } else {
-                        const int t0 = i * kSide + half * 64;
-                        uint64_t x[32];
+                        const bool negative = p.scale_log2 < 0.f;
+                        if (__any_sync(0xffffffffu, c0 + 32 > row_sees)) {
+                            const float masked = negative ? INFINITY : -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] = mul2(pair(s[2 * c], s[2 * c + 1]), scale2);
-                        if (__any_sync(0xffffffffu, t0 + 64 > row_sees)) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                float a, b;
-                                unpair(x[c], a, b);
-                                x[c] = pair(t0 + 2 * c < row_sees ? a : -INFINITY, t0 + 2 * c + 1 < row_sees ? b : -INFINITY);
-                            }
+                            for (int c = 0; c < 32; ++c)
+                                if (c0 + c >= row_sees) s[c] = masked;
                         }
-                        float best[4] = {top, top, top, top};
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            float a, b;
-                            unpair(x[c], a, b);
-                            best[c & 3] = fmaxf(best[c & 3], fmaxf(a, b));
-                        }
-                        const float up = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-                        const float ref = up == -INFINITY ? 0.f : up;   // (nothing seen yet: 2^-inf = 0)
-                        sum *= fast_exp2(top - ref);
-                        top = up;
-                        const uint64_t minus = pair(-ref, -ref);
-                        uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            float a, b;
-                            unpair(add2(x[c], minus), a, b);
-                            acc[c & 1] = add2(acc[c & 1], pair(fast_exp2(a), fast_exp2(b)));
-                        }
-                        float a, b;
-                        unpair(add2(acc[0], acc[1]), a, b);
-                        sum += a + b;
+                        if (negative) add_stats<true>(s, scale2, p.scale_log2, top, sum);
+                        else add_stats<false>(s, scale2, p.scale_log2, top, sum);
                     }
                 }
+                if (kSums) __syncwarp();   // the offsets have been read
             }
             if (!ok) break;
-            // (a unit that this group has nothing of did not look ahead)
-            if (kSums && u.from(g) >= last && next.k >= 0 && next.from(g) < next.to(g)) column(next, next.from(g));
-            if (kSums) {
-                if (g < u.held && held_row < u.s.ctx) {
-                    float *w = p.weights + (static_cast<int64_t>(u.b) * p.num_kv_heads + u.head) * p.weights_stride + held_row;
-                    *w = sum + (held_row < u.s.fresh && p.decay != 0.f ? p.decay * *w : 0.f);
+            if (kSums) {   // the two halves of the columns
+                if (h == 1) {
+                    if (k > 0 && !wait_warp(p, sh, &sh->part_free[g], (k - 1) & 1)) break;
+                    sh->part[g][R] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh->part_full[g]));
+                } else {
+                    if (!wait_warp(p, sh, &sh->part_full[g], k & 1)) break;
+                    sum += sh->part[g][R];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh->part_free[g]));
                 }
-            } else if ((!p.pair || g < u.held) && held_row < u.s.count * p.group) {
+                if (h == 0 && g < u->held && held_row < u->s.ctx) {
+                    float *w = p.weights + (static_cast<int64_t>(u->b) * p.num_kv_heads + u->head) * p.weights_stride + held_row;
+                    if (p.row_pieces > 1)
+                        p.parts[((static_cast<int64_t>(u->piece) * p.num_seqs + u->b) * p.num_kv_heads + u->head) * p.max_ctx + held_row] = sum;
+                    else
+                        *w = sum + (held_row < u->s.fresh && p.decay != 0.f ? p.decay * *w : 0.f);
+                }
+            } else if ((split || g < u->held) && held_row < rows) {
                 const int token = held_row / p.group;
-                const int slot = p.pair ? u.piece : 2 * u.piece + g;
-                p.stats[(slot * p.stat_rows + u.s.stat0 + token) * p.num_heads + u.head * p.group + held_row - token * p.group] =
-                    make_float2(top, sum);
+                leave_stats(p, 2 * (split ? 2 * u->piece + g : u->piece) + h, u->s.stat0 + token, u->head * p.group + held_row - token * p.group,
+                            top * fabsf(p.scale_log2), sum);
             }
-            u = next;
+            unit_read(k);
         }
     }
     tc_fence_before();
@@ -517,22 +631,90 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p) {
     }
 }
 
+// Between the passes: the rows' statistics put together; and, in the last CTA, the second pass's units in order of
+// their length (to one of 256 lengths; which of equal ones is first does not show in the result), and its counter.
+// Ragged chunks: the units as they are numbered leave the SMs idle for a third of the pass.
+constexpr int kOrderThreads = 256;
+__global__ void __launch_bounds__(kOrderThreads) weight_between_kernel(const __grid_constant__ PrefillWeightsParams p, int units) {
+    __shared__ int start[256], scan[kOrderThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int t = threadIdx.x, lane = t & 31;
+    if (blockIdx.x != gridDim.x - 1) {
+        merge_stats(p, static_cast<int64_t>(blockIdx.x) * kOrderThreads + t);
+        return;
+    }
+    if (t == 0) *p.counter = 0;
+    if (!p.order) return;
+    const int longest = max(1, static_cast<int>((static_cast<int64_t>(p.max_count) * p.group + kSide - 1) / kSide));
+    auto bucket = [&](int n) {   // the longest in bucket 0, those with nothing in the last
+        Unit u;
+        const int len = lay_out_sums(p, n, u) ? u.hi - u.lo : -1;
+        return len < 0 ? 255 : 254 - static_cast<int>(min(static_cast<int64_t>(254), static_cast<int64_t>(len) * 254 / longest));
+    };
+    start[t] = 0;
+    __syncthreads();
+    for (int n = t; n < units; n += kOrderThreads) atomicAdd(&start[bucket(n)], 1);
+    __syncthreads();
+    int sum = start[t];
+    const int mine = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+    }
+    if (lane == 31) scan[t >> 5] = sum;
+    __syncthreads();
+    int before = sum - mine;
+    for (int w = 0; w < (t >> 5); ++w) before += scan[w];
+    start[t] = before;
+    __syncthreads();
+    for (int n = t; n < units; n += kOrderThreads) p.order[atomicAdd(&start[bucket(n)], 1)] = n;
+}
+
+// The pieces of the rows put together: weights = decay * weights + their sums.
+__global__ void __launch_bounds__(kOrderThreads) weight_parts_kernel(const __grid_constant__ PrefillWeightsParams p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int b = blockIdx.y / p.num_kv_heads, t = blockIdx.x * kOrderThreads + threadIdx.x;
+    const WeightSeq s = weight_seq(p, b);
+    if (t >= s.ctx) return;
+    const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
+    float sum = 0.f;
+    for (int i = 0; i < p.row_pieces; ++i) sum += p.parts[(i * rows + blockIdx.y) * p.max_ctx + t];
+    float *w = p.weights + blockIdx.y * p.weights_stride + t;
+    *w = sum + (t < s.fresh && p.decay != 0.f ? p.decay * *w : 0.f);
+}
+
 constexpr size_t kSmemBytes = 1024 + kTileSpace + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
 template <int D, bool kF16, bool kSums>
-cudaError_t launch_one(const PrefillWeightsParams &p, int sms, cudaStream_t stream) {
+cudaError_t launch_pass(const PrefillWeightsParams &p, int sms, cudaStream_t stream) {
     auto kern = prefill_weights_tc_kernel<D, kF16, kSums>;
     static unsigned long long done = 0;
     const cudaError_t e = ensure_smem_limit(kern, kSmemBytes, done);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(std::min<int64_t>(unit_count<kSums>(p), sms))), dim3(kThreads), kSmemBytes, stream, 1u, p);
+    // A unit that streams many tiles: more of them on their way. Short units: the next one's held tiles too.
+    const int64_t streamed = kSums ? (static_cast<int64_t>(p.max_count) * p.group + kSide - 1) / kSide
+                                   : ((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide + p.pieces - 1) / p.pieces;
+    const int held_buffers = (kSums || p.pair) && streamed >= kLongUnit ? 1 : 2;
+    return launch_kernel(kern, dim3(static_cast<unsigned>(std::min<int64_t>(unit_count<kSums>(p), sms))), dim3(kThreads),
+                         kSmemBytes, stream, 1u, p, held_buffers);
 }
 
 template <int D, bool kF16>
 cudaError_t launch_both(const PrefillWeightsParams &p, int sms, cudaStream_t stream) {
-    const cudaError_t e = launch_one<D, kF16, false>(p, sms, stream);
-    return e != cudaSuccess ? e : launch_one<D, kF16, true>(p, sms, stream);
+    cudaError_t e = launch_pass<D, kF16, false>(p, sms, stream);
+    if (e == cudaSuccess)
+        e = launch_kernel(weight_between_kernel,
+                          dim3(static_cast<unsigned>((p.stat_rows * p.num_heads + kOrderThreads - 1) / kOrderThreads + 1)),
+                          dim3(kOrderThreads), 0, stream, 1u, p, static_cast<int>(unit_count<true>(p) / p.num_kv_heads));
+    if (e == cudaSuccess) e = launch_pass<D, kF16, true>(p, sms, stream);
+    if (e != cudaSuccess || p.row_pieces == 1) return e;
+    const dim3 grid(static_cast<unsigned>((p.max_ctx + kOrderThreads - 1) / kOrderThreads),
+                    static_cast<unsigned>(p.num_seqs * p.num_kv_heads));
+    return launch_kernel(weight_parts_kernel, grid, dim3(kOrderThreads), 0, stream, 1u, p);
 }
 
 }  // namespace
@@ -544,23 +726,35 @@ bool prefill_weights_tc_fits(int num_seqs, int num_kv_heads, int64_t rows, int m
            ((rows + kSide - 1) / kSide + 1) * heads <= most / kMaxSplits && (max_ctx / (2 * kSide) + 1) * heads <= most;
 }
 
-// How the statistics are cut: rows of a unit, pieces of a context. A unit's time is its key tiles, and
-// half a tile to begin and end; the pieces are those whose rounds over the SMs take least.
-void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces) {
+// How the passes are cut. Statistics: rows of a unit, pieces of a context; a unit's time is its key tiles and some
+// to begin and end with, and the pieces are those whose rounds over the SMs take least. Sums: pieces of the rows
+// where the SMs would get fewer than kFewUnits units each.
+constexpr int kFewUnits = 3;
+constexpr int kMaxRowPieces = 8;
+constexpr int64_t kMaxOrdered = 4096;   // units that one CTA puts in order
+void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces,
+                             int *row_pieces, int64_t *ordered) {
     *pair = rows > kSide;
-    const int64_t side = *pair ? 2 * kSide : kSide;
-    const int64_t units = static_cast<int64_t>(num_seqs) * num_kv_heads * ((rows + side - 1) / side);
+    const int64_t side = *pair ? 2 * kSide : kSide, heads = static_cast<int64_t>(num_seqs) * num_kv_heads;
+    const int64_t units = heads * ((rows + side - 1) / side);
     const int64_t tiles = (static_cast<int64_t>(max_ctx) + kSide - 1) / kSide;
     double best = 0;
     *pieces = 1;
-    for (int n = 1; n <= kMaxSplits / 2 && n <= tiles; ++n) {
+    for (int n = 1; n <= kMaxSplits / 4 && n <= tiles; ++n) {
         const double rounds = static_cast<double>((units * n + sms - 1) / sms);
-        const double time = rounds * (static_cast<double>((tiles + n - 1) / n) * (*pair ? 2 : 1) + 0.5);
+        const double time = rounds * (static_cast<double>((tiles + n - 1) / n) * (*pair ? 2 : 1) + (*pair ? 3 : 1));
         if (n == 1 || time < best * 0.97) {
             best = time;
             *pieces = n;
         }
     }
+    const int64_t key_units = (static_cast<int64_t>(max_ctx) + 2 * kSide - 1) / (2 * kSide) * heads;
+    const int64_t row_tiles = (rows + kSide - 1) / kSide;
+    *row_pieces = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>({(kFewUnits * sms + key_units - 1) / std::max<int64_t>(key_units, 1), row_tiles / 4, kMaxRowPieces})));
+    if (heads > 65535) *row_pieces = 1;
+    const int64_t n = key_units / num_kv_heads * *row_pieces;
+    *ordered = row_tiles >= kLongUnit && n <= kMaxOrdered ? n : 0;   // (0: taken as they are numbered)
 }
 
 cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, int sms, cudaStream_t stream) {

@@ -26,6 +26,21 @@ struct DecodeWeightsParams {
     float scale_log2, decay;
 };
 
+// Division of 0 <= n < 2^31 by a number known ahead, d <= 2^16: n * m >> (31 + s) with s = ceil(log2 d) and
+// m = floor(2^(31 + s) / d) + 1 (Granlund and Montgomery, "Division by invariant integers using multiplication").
+struct FixedDivisor {
+    uint32_t m;
+    int s;
+    void set(int d) {
+        s = 0;
+        while ((1 << s) < d) ++s;
+        m = static_cast<uint32_t>((uint64_t(1) << (31 + s)) / d + 1);
+    }
+    __device__ __forceinline__ int of(int n) const {
+        return s == 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m) >> (s - 1));
+    }
+};
+
 // The weights that several query tokens a sequence gave each cached token, without their outputs.
 // A sequence's rows are the (query token, query head) pairs of one KV head that count, token by token.
 struct PrefillWeightsParams {
@@ -33,10 +48,15 @@ struct PrefillWeightsParams {
     const void *k_cache;
     const int32_t *block_tables, *context_lens, *query_start;
     float *weights;               // [num_seqs, num_kv_heads, weights_stride]
-    float2 *stats;                // [nsplit][stat_rows][num_heads]: maximum and sum of a row's scores (base 2)
+    float *offsets;               // [stat_rows][num_heads]: what to take from a row's scores (base 2) before 2^x
+    float2 *stats;                // nsplit > 1: [nsplit][stat_rows][num_heads] maximum and sum of each piece
+    int *counter;                 // prefill_weights_tc: units of the second pass drawn beyond one a CTA
+    int *order;                   //   its units (one KV head's), longest first, or null (as they are numbered)
+    float *parts;                 //   row_pieces > 1: [row_pieces][num_seqs][num_kv_heads][max_ctx] sums over pieces of the rows
     int64_t weights_stride, stat_rows;
     int *status;
     int num_seqs, num_tokens, num_heads, num_kv_heads, group;
+    FixedDivisor group_div;       // by group
     int block_size, max_blocks, num_blocks;
     int max_count, max_ctx;       // host bounds: query tokens that count, context tokens
     int window;                   // the last so many query tokens count (0: all)
@@ -44,6 +64,7 @@ struct PrefillWeightsParams {
     int nsplit;                   // pieces of a context that a row's statistics are made in
     int pieces, pair;             // prefill_weights_tc: ranges of keys a unit of rows is cut into; 1: a unit is two
                                   //   row tiles, else one whose two halves of each range make a piece each
+    int row_pieces;               // ranges of rows that a unit of keys is cut into
     float scale_log2, decay;
 };
 
@@ -85,19 +106,36 @@ __device__ __forceinline__ WeightSeq weight_seq(const PrefillWeightsParams &p, i
     return s;
 }
 
-// A row's maximum and sum over the pieces of its context, as what to take from a score before 2^x:
-// maximum + log2(sum). A row without any weight takes plus infinity: all its weights are zeros.
-__device__ __forceinline__ float row_offset(const PrefillWeightsParams &p, int64_t stat, int head) {
+// What to take from a row's scores: maximum + log2(sum), so that 2^x are its weights. A row that weighs
+// nothing takes plus infinity.
+__device__ __forceinline__ float row_offset(float top, float sum) {
+    return sum > 0.f ? top + log2f(sum) : sum == 0.f ? INFINITY : sum;   // (the last: NaN)
+}
+
+// A row's statistics over one piece of its context; the only piece leaves the offset itself.
+__device__ __forceinline__ void leave_stats(const PrefillWeightsParams &p, int piece, int64_t stat, int head, float top,
+                                            float sum) {
+    if (p.nsplit == 1) p.offsets[stat * p.num_heads + head] = row_offset(top, sum);
+    else p.stats[(piece * p.stat_rows + stat) * p.num_heads + head] = make_float2(top, sum);
+}
+
+// The pieces' statistics of row i (of stat_rows x num_heads), put together.
+__device__ __forceinline__ void merge_stats(const PrefillWeightsParams &p, int64_t i) {
+    const int64_t all = p.stat_rows * p.num_heads;
+    if (i >= all) return;
     float top = -INFINITY, sum = 0.f;
-    for (int s = 0; s < p.nsplit; ++s) {
-        const float2 ml = p.stats[(s * p.stat_rows + stat) * p.num_heads + head];
-        if (ml.y == 0.f) continue;
-        if (!(ml.y > 0.f)) return ml.y;   // NaN
-        const float up = fmaxf(top, ml.x);
-        sum = (sum > 0.f ? sum * fast_exp2(top - up) : 0.f) + ml.y * fast_exp2(ml.x - up);
-        top = up;
+    for (int s0 = 0; s0 < p.nsplit; s0 += 8) {
+        float2 ml[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) ml[s] = s0 + s < p.nsplit ? p.stats[(s0 + s) * all + i] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float up = fmaxf(top, ml[s].x), ref = up == -INFINITY ? 0.f : up;
+            sum = sum * fast_exp2(top - ref) + ml[s].y * fast_exp2(ml[s].x - ref);
+            top = up;
+        }
     }
-    return sum > 0.f ? top + log2f(sum) : INFINITY;
+    p.offsets[i] = row_offset(top, sum);
 }
 
 struct EvictParams {

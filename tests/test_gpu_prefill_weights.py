@@ -122,6 +122,17 @@ def test_long_context_splits_and_many_rows():
         assert torch.equal(w.nan_to_num(7.0), call(paged, q, old, start, d ** -0.5, 1.0, window).nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("dt", list(DT))
+def test_a_block_outside_the_pool_reads_as_zeros(dt):
+    paged, q, old, start = problem((30, 9), (200, 9), 8, 2, 128, 16, dt, 12)
+    old = torch.zeros_like(old)
+    for entry, bad in ((2, paged.blocks + 7), (5, -1), (12, 1 << 29)):   # (200 tokens: the last block is cut)
+        paged.tables[0, entry] = bad
+        paged.seq_k[0][16 * entry:16 * entry + 16] = 0
+    w = call(paged, q, old, start, 0.1, 1.0)
+    check_weights(w, *weights_after(paged, old, split(q, start), 0.1, 1.0, 8))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_many_units_of_every_shape(dt):
     """More (sequence, head, tile) units than SMs, contexts of an odd number of tiles among them, so that what a
