@@ -1928,9 +1928,20 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.decay = decay;
     p.status = status_word(dev);
     if (!p.status) return PA_ERR_CUDA;
-    const cudaError_t e = tc ? launch_prefill_weights_tc(p, kv_dtype == PA_F16, head_dim, sms, as_stream(stream))
-                             : launch_prefill_weights_simt(p, head_dim, as_stream(stream));
-    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    if (!tc) return launch_prefill_weights_simt(p, head_dim, as_stream(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    const bool f16 = kv_dtype == PA_F16;
+    const int key_box = prefill_weights_tc_key_box(block_size), query_box = prefill_weights_tc_query_box(p.group);
+    CUtensorMap map_q, map_k;
+    std::memset(&map_q, 0, sizeof map_q);
+    std::memset(&map_k, 0, sizeof map_k);
+    if (key_box && query_box) {
+        if ((st = make_cache_map(&map_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, key_box, 1, 1, f16)) != PA_OK ||
+            (st = make_query_group_map(&map_q, query, num_tokens, num_kv_heads, p.group, head_dim, query_box, f16)) != PA_OK)
+            return st;
+    }
+    return launch_prefill_weights_tc(p, f16, head_dim, key_box && query_box, map_q, map_k, sms, as_stream(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_evict(int32_t *kept, int64_t kept_stride, float *new_weights, int64_t new_weights_stride,

@@ -92,7 +92,10 @@ cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int head_
 bool prefill_weights_tc_fits(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx);
 void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces,
                              int *row_pieces, int64_t *ordered);
-cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, int sms, cudaStream_t stream);
+int prefill_weights_tc_key_box(int block_size);   // tokens of a box where tiles are fetched by TMA, else 0
+int prefill_weights_tc_query_box(int group);
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, bool tma, const CUtensorMap &map_q,
+                                      const CUtensorMap &map_k, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 // Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid
 // (row tiles of the batch, Hkv * ntile, nsplit); `tall`: 64-row tiles, else 16.

@@ -16,13 +16,15 @@
 //    it (4 x 128 columns of tensor memory), two warps a lane quarter, so that a scheduler
 //    has four warps to hide an exponential's latency with;
 //  * warp 16: issues the products;
-//  * warps 17-20: fetch the tiles, 32 rows of each a warp, by 16-byte asynchronous copies
-//    laid out as the 128-byte swizzled K-major operand (row r's chunk c at c ^ (r & 7)).
-//    Rows are gathered one by one, so blocks of any size and rows of several query heads
-//    cost the same; up to two tiles of a warp are on their way, and it makes a tile's
-//    copies visible to the tensor cores (fence.proxy.async) before it reports them. (TMA
-//    gathers of four rows: 80 cycles each, a third of this rate.) The first of them
-//    draws the units and lays them out in a ring of shared memory for all others.
+//  * warp 17: draws the units, lays them out in a ring of shared memory for all others, and
+//    fetches the tiles by TMA, in the 128-byte swizzled K-major operand's layout: blocks of
+//    keys, whole tiles of query rows. That takes blocks of a power of two of 8 tokens or
+//    more and 128 to be whole query tokens; else warps 17-20 fetch 32 rows of each tile,
+//    gathered one by one, by 16-byte asynchronous copies (row r's chunk c at c ^ (r & 7)),
+//    with up to two tiles of a warp on their way, each made visible to the tensor cores
+//    (fence.proxy.async) before it is reported. The copies wait in the same queue as the
+//    exponentials: a tile takes a warp 800 to 1,200 cycles. (TMA gathers of four rows
+//    took 80 cycles each, 5,200 a tile.)
 // A unit holds two tiles, one a group, so that a streamed tile feeds 256 held rows;
 // where a KV head has 128 query rows or less, a unit of the statistics holds one, and
 // the groups take every other key tile. Long units first; those of the sums, whose
@@ -45,8 +47,7 @@ constexpr int kSide = 128;               // rows of a tile, either side
 constexpr int kGroupWarps = 8;           // two for each 32 lanes of tensor memory: columns 0 .. 63 and 64 .. 127
 constexpr int kMmaWarp = 2 * kGroupWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
-constexpr int kLoadWarps = 4;            // 32 rows of every tile each (21 warps: 96 registers a thread)
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kCopyWarps = 4;            // that gather rows: 32 of every tile each
 constexpr int kTileSpace = 192 * 1024;   // shared memory for tiles
 constexpr int kMaxSlots = 12;
 constexpr int kUnits = 4;                // units laid out ahead
@@ -270,10 +271,15 @@ __device__ __forceinline__ void add_stats(const float (&s)[32], uint64_t scale2,
     sum += a + b;
 }
 
-template <int D, bool kF16, bool kSums>
-__global__ void __launch_bounds__(kThreads, 1)
-prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p, const int held_buffers) {
+template <bool kTma>
+constexpr int kThreads = 32 * (kLoadWarp + (kTma ? 1 : kCopyWarps));
+
+template <int D, bool kF16, bool kTma, bool kSums>
+__global__ void __launch_bounds__(kThreads<kTma>, 1)
+prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ PrefillWeightsParams p, const int held_buffers) {
     using T = TcTile<D>;
+    constexpr int kLoadWarps = kTma ? 1 : kCopyWarps;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Shared *sh = reinterpret_cast<Shared *>(tiles + kTileSpace);
@@ -323,7 +329,8 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p, const 
     if (warp >= kLoadWarp) {
         // ---------------------------- units and tiles ----------------------------
         const int mine = warp - kLoadWarp;
-        const uint32_t base = smem_addr(tiles) + mine * 32 * 128;   // this warp's rows of the first slot
+        const uint32_t base = smem_addr(tiles) + mine * 32 * 128;   // (copies) this warp's rows of the first slot
+        const uint64_t policy = l2_policy_evict_last();             // (both operands are read by many)
         uint64_t *pending = nullptr;   // the barrier of the tile that is on its way
         auto report = [&]() {          // its rows have arrived
             fence_proxy_async_smem();
@@ -339,25 +346,57 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p, const 
             }
             return wait_warp(p, sh, bar, parity);
         };
-        // The lane's row of a tile (none: zeros, as for a block outside the pool).
+        // Where the lane's part of a tile comes from. TMA: its box of keys (block, first token in it), or none; else its
+        // row (none: zeros, as for a block outside the pool).
+        struct Place {
+            const uint16_t *row;
+            int blk, at;
+            bool live;
+        };
+        const int box = min(p.block_size, kSide);   // tokens of one box of keys
         auto locate = [&](const Unit &u, bool keys, int tile) {
+            Place w{nullptr, 0, 0, false};
+            if (kTma) {
+                if (!keys) {
+                    w.live = lane < D / 64;
+                    w.at = u.s.q0 + tile * (kSide / p.group);
+                } else {
+                    const int t = tile * kSide + lane / (D / 64) * box, j = t / p.block_size;
+                    w.live = t < min(u.s.ctx, (tile + 1) * kSide);
+                    w.at = t - j * p.block_size;
+                    if (w.live) w.blk = p.block_tables[static_cast<int64_t>(u.b) * p.max_blocks + j];
+                }
+                return w;
+            }
             const int r = tile * kSide + mine * 32 + lane;
-            const uint16_t *row = nullptr;
             if (keys && r < u.s.ctx) {
                 const int j = r / p.block_size, blk = p.block_tables[static_cast<int64_t>(u.b) * p.max_blocks + j];
                 if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks))
-                    row = static_cast<const uint16_t *>(p.k_cache) +
-                          ((static_cast<int64_t>(blk) * p.block_size + (r - j * p.block_size)) * p.num_kv_heads + u.head) * D;
+                    w.row = static_cast<const uint16_t *>(p.k_cache) +
+                            ((static_cast<int64_t>(blk) * p.block_size + (r - j * p.block_size)) * p.num_kv_heads + u.head) * D;
             } else if (!keys && r < u.rows) {
                 const int token = r / p.group;
-                row = static_cast<const uint16_t *>(p.query) +
-                      ((static_cast<int64_t>(u.s.q0) + token) * p.num_heads + u.head * p.group + r - token * p.group) * D;
+                w.row = static_cast<const uint16_t *>(p.query) +
+                        ((static_cast<int64_t>(u.s.q0) + token) * p.num_heads + u.head * p.group + r - token * p.group) * D;
             }
-            return row;
+            return w;
         };
-        // Fetch a tile's rows once `empty` has completed the phase of this parity (negative: the slot is free).
-        auto fetch = [&](const uint16_t *row, int slot, uint64_t *full, uint64_t *empty, int parity) {
+        // Fetch a tile once `empty` has completed the phase of this parity (negative: the slot is free).
+        auto fetch = [&](const Unit &u, bool keys, const Place &w, int slot, uint64_t *full, uint64_t *empty, int parity) {
             if (parity >= 0 && !wait_for(empty, parity)) return false;
+            if (kTma) {   // (boxes of keys past the context are left out: what the slot holds there is not looked at)
+                const int half = lane % (D / 64), bytes = (keys ? box : kSide) * 128;
+                const unsigned boxes = __popc(__ballot_sync(0xffffffffu, w.live));
+                const uint32_t to = smem_addr(tiles) + slot * T::kBytes + half * T::kHalf, bar = smem_addr(full);
+                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * bytes);
+                __syncwarp();
+                if (w.live) {
+                    if (keys) tma_load_5d(to + lane / (D / 64) * bytes, &map_k, 0, w.at, half, u.head, w.blk, bar, policy);
+                    else tma_load_5d(to, &map_q, 0, half, 0, u.head, w.at, bar, policy);
+                }
+                return true;
+            }
+            const uint16_t *row = w.row;
             // A lane copies chunk c of every kStep-th row. Several rows' places are read at a time: a copy is ordered
             // behind the reads before it.
             constexpr int kStep = 32 / T::kChunks;
@@ -422,24 +461,37 @@ prefill_weights_tc_kernel(const __grid_constant__ PrefillWeightsParams p, const 
             if (u.b < 0) break;
             if (u.lo >= u.hi) continue;
             // (a tile's rows are looked up while the one before is sent for)
-            const uint16_t *held[2] = {locate(u, kSums, u.tile), u.held > 1 ? locate(u, kSums, u.tile + 1) : nullptr};
-            const uint16_t *next = locate(u, !kSums, u.lo);
+            const Place held[2] = {locate(u, kSums, u.tile), locate(u, kSums, u.held > 1 ? u.tile + 1 : u.tile)};
+            Place next = locate(u, !kSums, u.lo);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (i >= u.held || !ok) break;
                 const int n = count[i]++, round = n / held_buffers, buf = n - round * held_buffers;
-                ok = fetch(held[i], i * held_buffers + buf, &sh->held_full[i][buf], &sh->held_empty[i][buf],
+                ok = fetch(u, kSums, held[i], i * held_buffers + buf, &sh->held_full[i][buf], &sh->held_empty[i][buf],
                            round > 0 ? (round - 1) & 1 : -1);
             }
             for (int i = u.lo; i < u.hi && ok; ++i, ++streamed) {
-                const uint16_t *row = next;
+                const Place here = next;
                 if (i + 1 < u.hi) next = locate(u, !kSums, i + 1);
                 const int round = streamed / str_slots, slot = streamed - round * str_slots;
-                ok = fetch(row, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], round > 0 ? (round - 1) & 1 : -1);
+                ok = fetch(u, !kSums, here, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], round > 0 ? (round - 1) & 1 : -1);
             }
         }
-        copy_wait<0>();
-        if (pending) report();
+        if (kTma) {   // nothing is on its way when the CTA ends: the last phase of every slot that was filled
+            auto drain = [&](uint64_t *full, int filled, int slots) {
+                for (int i = max(0, filled - slots); i < filled; ++i)
+                    if (!mbar_wait(smem_addr(full + i % slots), (i / slots) & 1)) record_status(p.status, kStatusTimeout);
+            };
+            if (lane == 0) {
+                drain(sh->held_full[0], count[0] - !ok, held_buffers);
+                drain(sh->held_full[1], count[1] - !ok, held_buffers);
+                drain(sh->str_full, streamed - !ok, str_slots);
+            }
+            __syncwarp();
+        } else {
+            copy_wait<0>();
+            if (pending) report();
+        }
     } else if (warp == kMmaWarp) {
         // ------------------------------ products ------------------------------
         constexpr uint32_t id = idesc_16bit_f32(kSide, kSide, false, false, kF16);
@@ -689,9 +741,9 @@ __global__ void __launch_bounds__(kOrderThreads) weight_parts_kernel(const __gri
 constexpr size_t kSmemBytes = 1024 + kTileSpace + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
-template <int D, bool kF16, bool kSums>
-cudaError_t launch_pass(const PrefillWeightsParams &p, int sms, cudaStream_t stream) {
-    auto kern = prefill_weights_tc_kernel<D, kF16, kSums>;
+template <int D, bool kF16, bool kTma, bool kSums>
+cudaError_t launch_pass(const PrefillWeightsParams &p, const CUtensorMap &map_q, const CUtensorMap &map_k, int sms, cudaStream_t stream) {
+    auto kern = prefill_weights_tc_kernel<D, kF16, kTma, kSums>;
     static unsigned long long done = 0;
     const cudaError_t e = ensure_smem_limit(kern, kSmemBytes, done);
     if (e != cudaSuccess) return e;
@@ -699,18 +751,18 @@ cudaError_t launch_pass(const PrefillWeightsParams &p, int sms, cudaStream_t str
     const int64_t streamed = kSums ? (static_cast<int64_t>(p.max_count) * p.group + kSide - 1) / kSide
                                    : ((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide + p.pieces - 1) / p.pieces;
     const int held_buffers = (kSums || p.pair) && streamed >= kLongUnit ? 1 : 2;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(std::min<int64_t>(unit_count<kSums>(p), sms))), dim3(kThreads),
-                         kSmemBytes, stream, 1u, p, held_buffers);
+    return launch_kernel(kern, dim3(static_cast<unsigned>(std::min<int64_t>(unit_count<kSums>(p), sms))), dim3(kThreads<kTma>),
+                         kSmemBytes, stream, 1u, map_q, map_k, p, held_buffers);
 }
 
-template <int D, bool kF16>
-cudaError_t launch_both(const PrefillWeightsParams &p, int sms, cudaStream_t stream) {
-    cudaError_t e = launch_pass<D, kF16, false>(p, sms, stream);
+template <int D, bool kF16, bool kTma>
+cudaError_t launch_both(const PrefillWeightsParams &p, const CUtensorMap &map_q, const CUtensorMap &map_k, int sms, cudaStream_t stream) {
+    cudaError_t e = launch_pass<D, kF16, kTma, false>(p, map_q, map_k, sms, stream);
     if (e == cudaSuccess)
         e = launch_kernel(weight_between_kernel,
                           dim3(static_cast<unsigned>((p.stat_rows * p.num_heads + kOrderThreads - 1) / kOrderThreads + 1)),
                           dim3(kOrderThreads), 0, stream, 1u, p, static_cast<int>(unit_count<true>(p) / p.num_kv_heads));
-    if (e == cudaSuccess) e = launch_pass<D, kF16, true>(p, sms, stream);
+    if (e == cudaSuccess) e = launch_pass<D, kF16, kTma, true>(p, map_q, map_k, sms, stream);
     if (e != cudaSuccess || p.row_pieces == 1) return e;
     const dim3 grid(static_cast<unsigned>((p.max_ctx + kOrderThreads - 1) / kOrderThreads),
                     static_cast<unsigned>(p.num_seqs * p.num_kv_heads));
@@ -757,9 +809,24 @@ void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int m
     *ordered = row_tiles >= kLongUnit && n <= kMaxOrdered ? n : 0;   // (0: taken as they are numbered)
 }
 
-cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, int sms, cudaStream_t stream) {
-    if (head_dim == 128) return f16 ? launch_both<128, true>(p, sms, stream) : launch_both<128, false>(p, sms, stream);
-    return f16 ? launch_both<64, true>(p, sms, stream) : launch_both<64, false>(p, sms, stream);
+// Tokens of a box of keys and of a box of queries where tiles are fetched by TMA (else 0).
+int prefill_weights_tc_key_box(int block_size) {
+    return block_size >= 8 && (block_size & (block_size - 1)) == 0 ? std::min(block_size, kSide) : 0;
+}
+int prefill_weights_tc_query_box(int group) { return kSide % group == 0 ? kSide / group : 0; }
+
+template <int D>
+cudaError_t launch_dim(const PrefillWeightsParams &p, bool f16, bool tma, const CUtensorMap &map_q, const CUtensorMap &map_k, int sms,
+                       cudaStream_t stream) {
+    if (tma)
+        return f16 ? launch_both<D, true, true>(p, map_q, map_k, sms, stream) : launch_both<D, false, true>(p, map_q, map_k, sms, stream);
+    return f16 ? launch_both<D, true, false>(p, map_q, map_k, sms, stream) : launch_both<D, false, false>(p, map_q, map_k, sms, stream);
+}
+
+cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, bool tma, const CUtensorMap &map_q,
+                                      const CUtensorMap &map_k, int sms, cudaStream_t stream) {
+    return head_dim == 128 ? launch_dim<128>(p, f16, tma, map_q, map_k, sms, stream)
+                           : launch_dim<64>(p, f16, tma, map_q, map_k, sms, stream);
 }
 
 }  // namespace pa
