@@ -3,19 +3,20 @@
 // heaviest others stay, in their order, moved together into other blocks.
 //
 // Two kernels.
-//  * Choice, one CTA a (sequence, KV head). Weights become unsigned keys that sort
-//    alike; a bitwise search from the top bit finds the k-th largest key (bit set
-//    where k keys or more reach it: one count over the CTA a bit). The keys stay in
-//    registers where the context has 32,768 tokens or less (32 a thread), else they
-//    are read again for each bit; once few enough share the bits found, those alone
-//    are searched on, from shared memory. Keys above the threshold are taken, and of
-//    those equal to it the first ones; ranks come from ballots and one scan over the
-//    warps, so positions leave in order without a sort and without atomics that
-//    would show in the result.
-//    Bound: the latency of 32 counts (a barrier each) and of two reads of the weights.
+//  * Choice, a CTA or a cluster of them a (sequence, KV head). Weights become unsigned keys
+//    that sort alike; the k-th largest is found digit by digit (8 bits, from the top): a
+//    histogram of the keys that share the digits found so far, and the bin in which the
+//    k-th falls. Four rounds, each a pass over keys in registers (16 a thread; contexts
+//    past 64 K are read again), three barriers, and in a cluster one exchange of 256 totals
+//    through distributed shared memory. Eight copies of the histogram, by lane: weights
+//    of one sign and few exponents fall into few bins. Keys above the threshold are
+//    taken, and of those equal to it the first ones; ranks come from ballots and one scan
+//    over the warps, so positions leave in order without a sort and without atomics
+//    that would show in the result. Bound: the latency of those rounds. (Found bit by
+//    bit, a count over 1,024 threads each: 17 us at 4,164 tokens, 37 at 32,768.)
 //  * Move: rows of 16-byte vectors, all heads of a kept place together, because a
 //    place's heads are contiguous where they go (they come from different tokens). Each
-//    element is read once and written once, so HBM is the bound.
+//    element is read once and written once, so HBM is the bound: 268 MB in 41 us.
 #include <algorithm>
 
 #include "internal.h"
@@ -25,13 +26,13 @@ namespace pa {
 
 namespace {
 
-constexpr int kChooseThreads = 1024;
+constexpr int kChooseThreads = 512;
 constexpr int kChooseWarps = kChooseThreads / 32;
-constexpr int kChooseKeys = 32;      // keys a thread, at most, that stay in registers
-constexpr int kListKeys = 2;         // keys a thread of the short list
-constexpr int kList = kListKeys * kChooseThreads;
+constexpr int kChooseKeys = 16;      // keys a thread holds
+constexpr int kChooseChunk = kChooseKeys * kChooseThreads;
+constexpr int kBins = 256, kCopies = 8;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveTokens = 32;      // places a CTA fills
+constexpr int kMoveTokens = 32;      // places a CTA fills, at most
 constexpr int kMoveHeads = 16;       //   of this many heads, at most
 constexpr int kMoveUnroll = 4;       // vectors of K and of V a thread has in flight
 
@@ -63,120 +64,130 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// The CTA's sum of one count a warp lane; `turn` alternates so that one barrier a sum suffices.
-__device__ __forceinline__ int cta_sum(int x, int (*part)[kChooseWarps], int turn) {
-    x = __reduce_add_sync(0xffffffffu, x);
-    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = x;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, part[turn][threadIdx.x & 31]);
+// (not volatile: several are on their way at once)
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-// Each warp owns the positions warp * keys * 32 + i * 32 + lane of a chunk, i < kKeys; with kResident
-// one chunk is the whole context, else the chunks follow one another.
+// CTA r of a cluster of c owns every chunk n with n % c == r of chunks of kKeys x 512 positions, and a warp of it
+// the positions warp * kKeys * 32 + i * 32 + lane of a chunk, i < kKeys. kResident: one chunk a CTA.
 template <int kKeys, bool kResident>
 __global__ void __launch_bounds__(kChooseThreads, 1)
-evict_choose_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int part[2][kChooseWarps];
+evict_choose_kernel(const __grid_constant__ EvictParams p, const int cluster) {
+    __shared__ __align__(16) int bins[kBins * kCopies];   // [bin][copy]
+    __shared__ int totals[2][kBins];                      // this CTA's, by the parity of the round
+    __shared__ int s_digit, s_over, s_scan[kBins / 32];
     __shared__ int above[kChooseWarps], equal[kChooseWarps];
-    __shared__ uint32_t list[kList];
-    __shared__ int listed;
+    __shared__ int2 s_counts[2];                          // (kept without equals, equals) of this CTA's chunk
     grid_dependency_wait();
     grid_dependents_launch();
-    const int b = blockIdx.x / p.num_kv_heads, h = blockIdx.x % p.num_kv_heads;
+    const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int unit = blockIdx.x / cluster;
+    const int b = unit / p.num_kv_heads, h = unit % p.num_kv_heads;
     const EvictSeq s = evict_seq(p, b);
-    if (s.keep <= 0) return;
+    if (s.keep <= 0) return;   // (every CTA of the cluster alike)
     const int64_t row = static_cast<int64_t>(b) * p.num_kv_heads + h;
     const float *w = p.weights + row * p.weights_stride;
     float *new_w = p.new_weights + row * p.new_weights_stride;
     int32_t *kept = p.kept + row * p.kept_stride;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (s.keep == s.len) {   // everything stays
-        for (int t = threadIdx.x; t < s.len; t += kChooseThreads) {
+        for (int t = rank * kChooseThreads + threadIdx.x; t < s.len; t += cluster * kChooseThreads) {
             kept[t] = t;
             new_w[t] = w[t];
         }
         return;
     }
     constexpr int kChunk = kKeys * kChooseThreads;
-    const int chunks = kResident ? 1 : (s.len + kChunk - 1) / kChunk;
+    const int all_chunks = (s.len + kChunk - 1) / kChunk;
+    const int rounds = kResident ? 1 : (all_chunks + cluster - 1) / cluster;   // chunks a CTA goes through
     const int first = s.sinks, last = s.len - s.recent;   // the candidates
-    const int want = s.keep - s.sinks - s.recent;         // how many of them stay
-    auto place = [&](int chunk, int i) { return chunk * kChunk + (warp * kKeys + i) * 32 + lane; };
-    auto key_at = [&](int t) -> uint32_t { return t >= first && t < last ? weight_key(w[t]) : 0u; };
-
+    int want = s.keep - s.sinks - s.recent;               // how many of them stay
+    auto place = [&](int round, int i) { return (round * cluster + rank) * kChunk + (warp * kKeys + i) * 32 + lane; };
     uint32_t key[kKeys];
-    auto load = [&](int chunk) {
+    float val[kKeys];
+    auto load = [&](int round) {
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) key[i] = key_at(place(chunk, i));
+        for (int i = 0; i < kKeys; ++i) val[i] = place(round, i) < s.len ? w[place(round, i)] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int t = place(round, i);
+            key[i] = t >= first && t < last ? weight_key(val[i]) : 0u;
+        }
     };
     if (kResident) load(0);
+    for (int i = threadIdx.x; i < kBins * kCopies; i += kChooseThreads) bins[i] = 0;
 
-    // threshold: the want-th largest key; over: how many keys are larger
+    // threshold: the want-th largest key. A round fixes the next digit of it; want counts on within the keys that
+    // share the digits so far.
     uint32_t threshold = 0;
-    int over = 0, reach = last - first, turn = 0, bit = 31;
-    if (threadIdx.x == 0) listed = 0;
     if (want > 0) {
-        for (; bit >= 0 && reach - over > kList; --bit) {
-            const uint32_t probe = threshold | (1u << bit);
-            int n = 0;
-            for (int c = 0; c < chunks; ++c) {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            const uint32_t found = shift == 24 ? 0u : ~0u << (shift + 8);   // the bits fixed so far
+            __syncthreads();   // (the histogram is empty)
+            for (int c = 0; c < rounds; ++c) {
                 if (!kResident) load(c);
 #pragma unroll
-                for (int i = 0; i < kKeys; ++i) n += key[i] >= probe;
+                for (int i = 0; i < kKeys; ++i)
+                    if (key[i] != 0u && (key[i] & found) == threshold)
+                        atomicAdd(&bins[((key[i] >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1);
             }
-            n = cta_sum(n, part, turn);
-            turn ^= 1;
-            if (n >= want) {
-                threshold = probe;
-                reach = n;
-            } else {
-                over = n;
+            __syncthreads();
+            // thread t: bin 255 - t, the largest digits first
+            int count = 0, upto = 0;
+            const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+            if (threadIdx.x < kBins) {
+                int4 *const at = reinterpret_cast<int4 *>(bins) + 2 * bin;
+                const int4 x = at[0], y = at[1];
+                count = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+                at[0] = at[1] = make_int4(0, 0, 0, 0);   // for the next round
             }
-        }
-        // the few keys that share the bits found so far
-        if (bit >= 0) {
-            __syncthreads();   // (listed is zero)
-            const uint32_t found = bit == 31 ? 0u : ~((2u << bit) - 1u);   // the mask of those bits
-            for (int c = 0; c < chunks; ++c) {
-                if (!kResident) load(c);
+            if (cluster > 1) {
+                int *const total = totals[(shift >> 3) & 1];
+                if (threadIdx.x < kBins) total[bin] = count;
+                cluster_sync_all();
+                if (threadIdx.x < kBins) {
+                    int n[kMaxClusterSplits];
 #pragma unroll
-                for (int i = 0; i < kKeys; ++i) {
-                    const bool in = key[i] != 0u && (key[i] & found) == threshold;
-                    const unsigned votes = __ballot_sync(0xffffffffu, in);
-                    if (votes == 0u) continue;
-                    int at = 0;
-                    if (lane == 0) at = atomicAdd(&listed, __popc(votes));   // (their order does not matter)
-                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1u));
-                    if (in) list[at] = key[i];
+                    for (int r = 0; r < kMaxClusterSplits; ++r)
+                        n[r] = r < cluster ? ld_cluster_s32(cluster_map(smem_addr(&total[bin]), r)) : 0;
+                    count = 0;
+#pragma unroll
+                    for (int r = 0; r < kMaxClusterSplits; ++r) count += n[r];
+                }
+            }
+            if (threadIdx.x < kBins) {
+                upto = count;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, upto, d);
+                    if (lane >= d) upto += o;
+                }
+                if (lane == 31) s_scan[warp] = upto;
+            }
+            __syncthreads();
+            if (threadIdx.x < kBins) {
+#pragma unroll
+                for (int i = 0; i < kBins / 32; ++i) upto += i < warp ? s_scan[i] : 0;
+                if (upto - count < want && upto >= want) {   // upto - count keys have a larger digit
+                    s_digit = bin;
+                    s_over = upto - count;
                 }
             }
             __syncthreads();
-            uint32_t mine[kListKeys];
-#pragma unroll
-            for (int i = 0; i < kListKeys; ++i) {
-                const int at = threadIdx.x + i * kChooseThreads;
-                mine[i] = at < listed ? list[at] : 0u;
-            }
-            const int fixed = over;   // keys above all of the list
-            for (; bit >= 0; --bit) {
-                const uint32_t probe = threshold | (1u << bit);
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < kListKeys; ++i) n += mine[i] >= probe;
-                n = fixed + cta_sum(n, part, turn);
-                turn ^= 1;
-                if (n >= want) threshold = probe;
-                else over = n;
-            }
+            threshold |= static_cast<uint32_t>(s_digit) << shift;
+            want -= s_over;
         }
     } else {
         threshold = 0xffffffffu;   // (no weight has this key)
     }
-    const int want_equal = max(want - over, 0);   // of the keys equal to the threshold, the first so many
+    const int want_equal = max(want, 0);   // of the keys equal to the threshold, the first so many
 
     // ranks: kept so far, equal keys so far, of the warps and chunks before
     int kept_before = 0, equal_before = 0;
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < rounds; ++c) {
         if (!kResident) load(c);
         int n_above = 0, n_equal = 0;
 #pragma unroll
@@ -192,21 +203,45 @@ evict_choose_kernel(const __grid_constant__ EvictParams p) {
             equal[warp] = n_equal;
         }
         __syncthreads();
+        if (cluster > 1) {   // the chunks of the CTAs before, and after, in this round
+            if (warp == 0) {
+                const int a = __reduce_add_sync(0xffffffffu, lane < kChooseWarps ? above[lane] : 0);
+                const int e = __reduce_add_sync(0xffffffffu, lane < kChooseWarps ? equal[lane] : 0);
+                if (lane == 0) s_counts[c & 1] = make_int2(a, e);
+            }
+            cluster_sync_all();
+        }
+        int others_kept = 0, others_equal = 0, all_kept = 0, all_equal = 0;
+        if (cluster > 1) {
+            for (int r = 0; r < cluster; ++r) {
+                const uint32_t at = cluster_map(smem_addr(&s_counts[c & 1]), r);
+                const int a = ld_cluster_s32(at), e = ld_cluster_s32(at + 4);
+                const int keeps = a + min(max(want_equal - equal_before - all_equal, 0), e);
+                if (r < rank) {
+                    others_kept += keeps;
+                    others_equal += e;
+                }
+                all_kept += keeps;
+                all_equal += e;
+            }
+        }
         // equal keys of the warps before, then what those warps keep
-        int eq = equal[lane], eq_scan = eq;
+        const int eq = lane < kChooseWarps ? equal[lane] : 0;
+        int eq_scan = eq;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int o = __shfl_up_sync(0xffffffffu, eq_scan, d);
             if (lane >= d) eq_scan += o;
         }
-        const int eq_first = equal_before + eq_scan - eq;
-        int keeps = above[lane] + min(max(want_equal - eq_first, 0), eq), keeps_scan = keeps;
+        const int eq_first = equal_before + others_equal + eq_scan - eq;
+        const int keeps = (lane < kChooseWarps ? above[lane] : 0) + min(max(want_equal - eq_first, 0), eq);
+        int keeps_scan = keeps;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int o = __shfl_up_sync(0xffffffffu, keeps_scan, d);
             if (lane >= d) keeps_scan += o;
         }
-        int at = kept_before + __shfl_sync(0xffffffffu, keeps_scan - keeps, warp);
+        int at = kept_before + others_kept + __shfl_sync(0xffffffffu, keeps_scan - keeps, warp);
         int eq_at = __shfl_sync(0xffffffffu, eq_first, warp);
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
@@ -220,19 +255,20 @@ evict_choose_kernel(const __grid_constant__ EvictParams p) {
             if (stays) {
                 const int to = at + __popc(votes & below);
                 kept[to] = t;
-                new_w[to] = w[t];
+                new_w[to] = val[i];
             }
             at += __popc(votes);
             eq_at += __popc(same_votes);
         }
-        kept_before += __shfl_sync(0xffffffffu, keeps_scan, 31);
-        equal_before += __shfl_sync(0xffffffffu, eq_scan, 31);
+        kept_before += cluster > 1 ? all_kept : __shfl_sync(0xffffffffu, keeps_scan, 31);
+        equal_before += cluster > 1 ? all_equal : __shfl_sync(0xffffffffu, eq_scan, 31);
     }
+    if (cluster > 1) cluster_sync_all();   // the peers have read this CTA's counts
 }
 
 __device__ __forceinline__ uint4 load_row(const uint4 *p) { return __ldcs(p); }
 
-// One CTA: kMoveTokens places of one sequence, up to kMoveHeads heads of each.
+// One CTA: p.move_tokens places of one sequence, up to kMoveHeads heads of each.
 __global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const __grid_constant__ EvictParams p) {
     __shared__ int64_t from[kMoveTokens * kMoveHeads];   // (place, head): byte offset of its row, or -1
@@ -241,8 +277,8 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
     grid_dependents_launch();
     const int b = blockIdx.y;
     const EvictSeq s = evict_seq(p, b);
-    const int j0 = blockIdx.x * kMoveTokens;
-    const int places = min(kMoveTokens, s.keep - j0);
+    const int j0 = blockIdx.x * p.move_tokens;
+    const int places = min(p.move_tokens, s.keep - j0);
     if (places <= 0) return;
     const int head0 = blockIdx.z * kMoveHeads;
     const int heads = min(kMoveHeads, p.num_kv_heads - head0);
@@ -255,9 +291,8 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
         if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) return -1;
         return (static_cast<int64_t>(blk) * p.block_size + t % p.block_size) * token_bytes;
     };
-    for (int i = threadIdx.x; i < kMoveTokens * heads; i += kMoveThreads) {
-        const int j = i % kMoveTokens, h = i / kMoveTokens;
-        if (j >= places) continue;
+    for (int i = threadIdx.x; i < places * heads; i += kMoveThreads) {
+        const int h = i / places, j = i - h * places;
         const int t = p.kept[(static_cast<int64_t>(b) * p.num_kv_heads + head0 + h) * p.kept_stride + j0 + j];
         const int64_t at = token_at(table, t);
         from[j * heads + h] = at < 0 ? -1 : at + static_cast<int64_t>(head0 + h) * p.row_bytes;
@@ -295,21 +330,27 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream) {
-    const dim3 rows(static_cast<unsigned>(p.num_seqs * p.num_kv_heads));
+cudaError_t launch_evict(EvictParams &p, int sms, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
+    const int chunks = (p.max_ctx - 1) / kChooseChunk + 1;
+    // a cluster where one CTA's registers do not hold the context
+    int cluster = 1;
+    while (cluster < kMaxClusterSplits && cluster < chunks) cluster *= 2;
     cudaError_t e;
-    if (p.max_ctx <= kChooseThreads)
-        e = launch_kernel(evict_choose_kernel<1, true>, rows, dim3(kChooseThreads), 0, stream, 1u, p);
-    else if (p.max_ctx <= 8 * kChooseThreads)
-        e = launch_kernel(evict_choose_kernel<8, true>, rows, dim3(kChooseThreads), 0, stream, 1u, p);
-    else if (p.max_ctx <= kChooseKeys * kChooseThreads)
-        e = launch_kernel(evict_choose_kernel<kChooseKeys, true>, rows, dim3(kChooseThreads), 0, stream, 1u, p);
+    if (p.max_ctx <= 2 * kChooseThreads)
+        e = launch_kernel(evict_choose_kernel<2, true>, dim3(static_cast<unsigned>(rows)), dim3(kChooseThreads), 0, stream, 1u, p, 1);
     else
-        e = launch_kernel(evict_choose_kernel<kChooseKeys, false>, rows, dim3(kChooseThreads), 0, stream, 1u, p);
+        e = launch_kernel(chunks <= cluster ? evict_choose_kernel<kChooseKeys, true> : evict_choose_kernel<kChooseKeys, false>,
+                          dim3(static_cast<unsigned>(rows * cluster)), dim3(kChooseThreads), 0, stream, static_cast<unsigned>(cluster), p,
+                          cluster);
     if (e != cudaSuccess) return e;
-    const int most = std::min(p.max_keep, p.max_ctx);
-    const dim3 grid(static_cast<unsigned>((most + kMoveTokens - 1) / kMoveTokens), static_cast<unsigned>(p.num_seqs),
-                    static_cast<unsigned>((p.num_kv_heads + kMoveHeads - 1) / kMoveHeads));
+    const int64_t most = std::min(p.max_keep, p.max_ctx);
+    const unsigned groups = static_cast<unsigned>((p.num_kv_heads + kMoveHeads - 1) / kMoveHeads);
+    // few places: fewer a CTA, so that all SMs have some (4,096 places of 8 heads of 128: 12.6 us at 32, 10.7 at 8)
+    p.move_tokens = kMoveTokens;
+    while (p.move_tokens > 8 && (most + p.move_tokens - 1) / p.move_tokens * p.num_seqs * groups < 3 * static_cast<int64_t>(sms))
+        p.move_tokens /= 2;
+    const dim3 grid(static_cast<unsigned>((most + p.move_tokens - 1) / p.move_tokens), static_cast<unsigned>(p.num_seqs), groups);
     return launch_kernel(evict_move_kernel, grid, dim3(kMoveThreads), 0, stream, 1u, p);
 }
 

@@ -96,7 +96,7 @@ int prefill_weights_tc_key_box(int block_size);   // tokens of a box where tiles
 int prefill_weights_tc_query_box(int group);
 cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, bool tma, const CUtensorMap &map_q,
                                       const CUtensorMap &map_k, int sms, cudaStream_t stream);
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams &p, int sms, cudaStream_t stream);
 // Several query tokens a sequence on the CUDA cores (prefill_simt.cu): grid
 // (row tiles of the batch, Hkv * ntile, nsplit); `tall`: 64-row tiles, else 16.
 // With nsplit > 1 the merge is launched too.

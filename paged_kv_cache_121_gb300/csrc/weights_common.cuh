@@ -150,6 +150,7 @@ struct EvictParams {
     int num_seqs, num_kv_heads, row_bytes, block_size, max_blocks, max_new_blocks, num_blocks;
     int max_ctx, max_keep;        // host bounds: what lies past them is cut
     int sinks, recent;
+    int move_tokens;              // places a CTA fills (set by the launcher)
 };
 
 }  // namespace pa
