@@ -47,7 +47,10 @@ struct StepCfg {
     static_assert(kState * 4 <= kRingBytes, "a warp's state takes its ring's place");
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void *src, bool live) {
     const int bytes = live ? 16 : 0;   // (the rest is filled with zeros)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -260,7 +263,8 @@ decode_weights_kernel(const __grid_constant__ DecodeWeightsParams p) {
     grid_dependency_wait();
 
     const int b = blockIdx.z, head0 = blockIdx.y * p.heads_per_cta;
-    const int head = head0 + warp / p.sets, set = warp % p.sets;   // this warp's KV head, its share of the tiles
+    const int sets_log = __ffs(p.sets) - 1;   // (a power of two)
+    const int head = head0 + (warp >> sets_log), set = warp & (p.sets - 1);   // this warp's KV head, its share of the tiles
     const int given = p.context_lens[b];
     int len = max(0, min(given, p.max_ctx));
     len = static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(p.max_blocks) * p.block_size));
@@ -277,46 +281,72 @@ decode_weights_kernel(const __grid_constant__ DecodeWeightsParams p) {
     const unsigned char *v_head = static_cast<const unsigned char *>(p.v_cache) + head * C::kRow;
 
     auto first_token = [&](int i) { return tok_begin + (set + i * p.sets) * C::kTile; };
-    // the slot of the lane's token of tile i (-1: nothing to read)
-    auto slot_of = [&](int i) -> int64_t {
+    // Block and place in it of the lane's token of tile i (place -1: nothing to read). The block is only loaded here
+    // and looked at a tile later: waited for at once it cost 700 cycles a tile.
+    auto look_up = [&](int i, int &blk, int &in) {
         const int t = first_token(i) + lane;
-        if (i >= tiles || lane >= C::kTile || t >= tok_end) return -1;
-        const int blk = table[t / p.block_size];
-        if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) return -1;
-        return static_cast<int64_t>(blk) * p.block_size + t % p.block_size;
+        in = -1;
+        if (i >= tiles || lane >= C::kTile || t >= tok_end) return;
+        const int j = t / p.block_size;
+        in = t - j * p.block_size;
+        blk = table[j];
     };
-    auto fetch = [&](int i, int64_t slot) {
+    auto fetch = [&](int i, int blk, int in) {
         if (i < tiles) {
-            const uint32_t k_dst = ring_addr + (i % C::kStages) * C::kStage, v_dst = k_dst + C::kTile * C::kRow;
+            const bool in_pool = in >= 0 && static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks);
+            const int64_t slot = in_pool ? static_cast<int64_t>(blk) * p.block_size + in : -1;
+            // A lane copies chunk c of every kStep-th token. The slots are read ahead: a copy is ordered behind the
+            // shuffles before it.
+            constexpr int kCopies = C::kTile * C::kChunks / 32, kStep = 32 / C::kChunks;
+            const int r0 = lane / C::kChunks, c = lane % C::kChunks;
+            int64_t from[kCopies];
 #pragma unroll
-            for (int n = 0; n < C::kTile * C::kChunks / 32; ++n) {
-                const int at = n * 32 + lane, t = at / C::kChunks, c = at % C::kChunks;
-                const int64_t from = __shfl_sync(0xffffffffu, slot, t);
-                const int64_t off = from < 0 ? 0 : from * token_bytes + c * 16;
+            for (int n = 0; n < kCopies; ++n) from[n] = __shfl_sync(0xffffffffu, slot, r0 + n * kStep);
+            const uint32_t k_dst = ring_addr + (i % C::kStages) * C::kStage, v_dst = k_dst + C::kTile * C::kRow;
+            const bool all = __all_sync(0xffffffffu, slot >= 0 || lane >= C::kTile);
+#pragma unroll
+            for (int n = 0; n < kCopies; ++n) {
+                const int t = r0 + n * kStep;
                 const uint32_t to = t * C::kRow + ((c ^ (t & 7)) << 4);
-                copy16(k_dst + to, k_head + off, from >= 0);
-                copy16(v_dst + to, v_head + off, from >= 0);
+                const int64_t off = from[n] * token_bytes + c * 16;
+                if (all) {
+                    copy16(k_dst + to, k_head + off);
+                    copy16(v_dst + to, v_head + off);
+                } else {
+                    copy16_or_zeros(k_dst + to, k_head + (from[n] < 0 ? 0 : off), from[n] >= 0);
+                    copy16_or_zeros(v_dst + to, v_head + (from[n] < 0 ? 0 : off), from[n] >= 0);
+                }
             }
         }
         copy_commit();
     };
+
+    // the old weights are on their way to L2 while the tiles are
+    if (p.decay != 0.f)
+        for (int j = 0; j < p.heads_per_cta; ++j) {
+            const float *w = p.weights + (static_cast<int64_t>(b) * p.num_kv_heads + head0 + j) * p.weights_stride;
+            for (int t = tok_begin + 32 * static_cast<int>(threadIdx.x); t < tok_end; t += 32 * blockDim.x)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(w + t));
+        }
 
     for (int first = 0; first < p.group; first += kRowsPerTile) {   // 16 query heads of each KV head a pass
         const int rows = min(kRowsPerTile, p.group - first);
         const int64_t row0 = static_cast<int64_t>(b) * p.num_heads + head * p.group + first;   // the warp's first row
         StepTile<T, D> tile;
         tile.start(static_cast<const T *>(p.query) + row0 * D, q_rows, rows, lane);
-        int64_t slot = slot_of(0);
-        for (int i = 0; i < C::kStages - 1; ++i) {
-            const int64_t now = slot;
-            slot = slot_of(i + 1);
-            fetch(i, now);
-        }
+        int blk[2] = {0, 0}, in[2];   // tiles looked up, not fetched: the next one and the one behind it
+        look_up(0, blk[0], in[0]);
+        look_up(1, blk[1], in[1]);
+        auto fetch_next = [&](int i) {
+            fetch(i, blk[0], in[0]);
+            blk[0] = blk[1];
+            in[0] = in[1];
+            look_up(i + 2, blk[1], in[1]);
+        };
+        for (int i = 0; i < C::kStages - 1; ++i) fetch_next(i);
         float *scores = p.scores + row0 * p.score_stride;
         for (int i = 0; i < tiles; ++i) {
-            const int64_t now = slot;
-            slot = slot_of(i + C::kStages);
-            fetch(i + C::kStages - 1, now);
+            fetch_next(i + C::kStages - 1);
             copy_wait<C::kStages - 1>();
             __syncwarp();
             const int t0 = first_token(i);
@@ -334,68 +364,119 @@ decode_weights_kernel(const __grid_constant__ DecodeWeightsParams p) {
         const int nsplit = p.nsplit, states = nsplit * p.sets;
         const uint32_t base = smem_addr(smem);
         auto state_addr = [&](int j, int n) {   // state n of the cluster's CTAs and warps for KV head j of the group
-            return cluster_map(base + static_cast<uint32_t>((j * p.sets + n % p.sets) * kRingBytes), n / p.sets);
+            return cluster_map(base + static_cast<uint32_t>((j * p.sets + (n & (p.sets - 1))) * kRingBytes), n >> sets_log);
         };
-        for (int i = threadIdx.x; i < p.heads_per_cta * rows; i += blockDim.x) {
-            const int j = i / rows, r = i - j * rows;
+        // Every row's statistics, and a slice of the outputs: 4 dims of one row a thread. The states are read eight at a
+        // time, all on their way before the first is used.
+        auto merge = [&](int j, int r, int d, float4 &acc) {   // (maximum, sum) of a row; d >= 0: its dims d .. d + 3 too
             float top = -INFINITY, sum = 0.f;
-            for (int n = 0; n < states; ++n) {
-                const float2 ml = ld_cluster_f32x2(state_addr(j, n) + 8 * r);
-                if (ml.y > 0.f) {
-                    const float up = fmaxf(top, ml.x);
-                    sum = sum * (sum > 0.f ? fast_exp2(top - up) : 0.f) + ml.y * fast_exp2(ml.x - up);
-                    top = up;
-                } else if (!(ml.y == 0.f)) {   // NaN
-                    sum = ml.y;
-                    top = 0.f;
-                    break;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int n0 = 0; n0 < states; n0 += 8) {
+                float2 ml[8];
+                float4 o[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    ml[n] = make_float2(-INFINITY, 0.f);
+                    o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (n0 + n < states) {
+                        const uint32_t at = state_addr(j, n0 + n);
+                        ml[n] = ld_cluster_f32x2(at + 8 * r);
+                        if (d >= 0) o[n] = ld_cluster_f32x4(at + 4 * (32 + r * C::kStateStride + d));
+                    }
                 }
+                float up = top;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) up = fmaxf(up, ml[n].x);
+                const float ref = up == -INFINITY ? 0.f : up, fade = fast_exp2(top - ref);
+                sum *= fade;
+                acc.x *= fade;
+                acc.y *= fade;
+                acc.z *= fade;
+                acc.w *= fade;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float f = fast_exp2(ml[n].x - ref);   // (an empty state's is zero)
+                    sum += f * ml[n].y;
+                    acc.x += f * o[n].x;
+                    acc.y += f * o[n].y;
+                    acc.z += f * o[n].z;
+                    acc.w += f * o[n].w;
+                }
+                top = up;
             }
-            s_row[j][r] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(top, 1.f / sum);
-        }
-        __syncthreads();
-        // a slice of the outputs: 4 dims of one row a thread
+            return make_float2(top, sum);
+        };
+        const int rank = static_cast<int>(cluster_rank());
         const int total = p.heads_per_cta * rows * (D / 4);
         const int slice = (total + nsplit - 1) / nsplit;
-        const int rank = static_cast<int>(cluster_rank());
         for (int i = rank * slice + threadIdx.x; i < min(total, (rank + 1) * slice); i += blockDim.x) {
             const int j = i / (rows * (D / 4)), rem = i - j * rows * (D / 4);
             const int r = rem / (D / 4), d = 4 * (rem - r * (D / 4));
-            const float2 ml = s_row[j][r];
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int n = 0; n < states; ++n) {
-                const uint32_t at = state_addr(j, n);
-                const float2 own = ld_cluster_f32x2(at + 8 * r);
-                const float4 o = ld_cluster_f32x4(at + 4 * (32 + r * C::kStateStride + d));
-                const float f = own.y == 0.f ? 0.f : fast_exp2(own.x - ml.x) * ml.y;
-                if (own.y == 0.f) continue;
-                acc.x += f * o.x;
-                acc.y += f * o.y;
-                acc.z += f * o.z;
-                acc.w += f * o.w;
-            }
+            float4 acc;
+            const float2 ml = merge(j, r, d, acc);
+            const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
             const int64_t at = (static_cast<int64_t>(b) * p.num_heads + (head0 + j) * p.group + first + r) * D + d;
-            store_pair_as(p.out, p.out_type, at, acc.x, acc.y);
-            store_pair_as(p.out, p.out_type, at + 2, acc.z, acc.w);
+            store_pair_as(p.out, p.out_type, at, acc.x * inv, acc.y * inv);
+            store_pair_as(p.out, p.out_type, at + 2, acc.z * inv, acc.w * inv);
         }
-        // this CTA's scores become weights
-        const int n_tok = tok_end - tok_begin;
-        for (int j = 0; j < p.heads_per_cta; ++j) {
-            const float *from = p.scores + (static_cast<int64_t>(b) * p.num_heads + (head0 + j) * p.group + first) * p.score_stride;
-            float *to = p.weights + (static_cast<int64_t>(b) * p.num_kv_heads + head0 + j) * p.weights_stride;
-            for (int i = threadIdx.x; i < n_tok; i += blockDim.x) {
-                const int t = tok_begin + i;
-                float w = 0.f;
-#pragma unroll 4
-                for (int r = 0; r < rows; ++r) {
-                    const float2 ml = s_row[j][r];
-                    w += fast_exp2(from[r * p.score_stride + t] - ml.x) * ml.y;
+        for (int i = threadIdx.x; i < p.heads_per_cta * rows; i += blockDim.x) {
+            const int j = i / rows, r = i - j * rows;
+            float4 acc;
+            const float2 ml = merge(j, r, -1, acc);
+            // (a row that weighs nothing: zeros; NaN stays)
+            s_row[j][r] = make_float2(ml.y == 0.f || ml.x == -INFINITY ? 0.f : ml.x, ml.y == 0.f ? 0.f : 1.f / ml.y);
+        }
+        __syncthreads();
+        // This CTA's scores become weights, four tokens a thread and kItems of those at once: every load of a round is on
+        // its way before the first is used.
+        constexpr int kItems = 4;
+        const int quads = (tok_end - tok_begin + 3) / 4, items = p.heads_per_cta * quads;
+        const int64_t scores0 = (static_cast<int64_t>(b) * p.num_heads + head0 * p.group + first) * p.score_stride + tok_begin;
+        float *const weights0 = p.weights + (static_cast<int64_t>(b) * p.num_kv_heads + head0) * p.weights_stride + tok_begin;
+        for (int i0 = threadIdx.x; i0 < items; i0 += blockDim.x * kItems) {
+            int head_of[kItems], at[kItems];   // KV head of the group (-1: none), first token
+            float w[kItems][4], old[kItems][4];
+#pragma unroll
+            for (int n = 0; n < kItems; ++n) {
+                const int i = i0 + n * blockDim.x, j = i / quads;
+                head_of[n] = i < items ? j : -1;
+                at[n] = 4 * (i - j * quads);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[n][e] = 0.f;
+                    // the newest token's weight starts in the first pass
+                    const int t = tok_begin + at[n] + e;
+                    const bool read = i < items && t < tok_end && (first > 0 || (t != given - 1 && p.decay != 0.f));
+                    old[n][e] = read ? weights0[j * p.weights_stride + at[n] + e] : 0.f;
                 }
-                // the newest token's weight starts here
-                if (first > 0) w += to[t];
-                else if (t != given - 1 && p.decay != 0.f) w += p.decay * to[t];
-                to[t] = w;
             }
+            for (int r0 = 0; r0 < rows; r0 += 4) {
+                float4 s[kItems][4];
+#pragma unroll
+                for (int n = 0; n < kItems; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (head_of[n] >= 0 && r0 + r < rows)
+                            s[n][r] = *reinterpret_cast<const float4 *>(
+                                p.scores + scores0 + (static_cast<int64_t>(head_of[n]) * p.group + r0 + r) * p.score_stride + at[n]);
+#pragma unroll
+                for (int n = 0; n < kItems; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (head_of[n] >= 0 && r0 + r < rows) {
+                            const float2 ml = s_row[head_of[n]][r0 + r];
+                            w[n][0] += fast_exp2(s[n][r].x - ml.x) * ml.y;
+                            w[n][1] += fast_exp2(s[n][r].y - ml.x) * ml.y;
+                            w[n][2] += fast_exp2(s[n][r].z - ml.x) * ml.y;
+                            w[n][3] += fast_exp2(s[n][r].w - ml.x) * ml.y;
+                        }
+            }
+#pragma unroll
+            for (int n = 0; n < kItems; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (head_of[n] >= 0 && tok_begin + at[n] + e < tok_end)
+                        weights0[head_of[n] * p.weights_stride + at[n] + e] = w[n][e] + (first > 0 ? old[n][e] : p.decay * old[n][e]);
         }
         cluster_sync_all();   // the peers have read this CTA's states
     }
