@@ -24,6 +24,7 @@
 //  * More than 16 query heads a KV head: the passes follow one another in the CTA.
 #include <algorithm>
 
+#include "async_copy.cuh"
 #include "internal.h"
 #include "mma_tile.cuh"
 #include "weights_common.cuh"
@@ -46,19 +47,6 @@ struct StepCfg {
     static constexpr int kState = 32 + kRowsPerTile * kStateStride;
     static_assert(kState * 4 <= kRingBytes, "a warp's state takes its ring's place");
 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void *src, bool live) {
-    const int bytes = live ? 16 : 0;   // (the rest is filled with zeros)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
 
 // One warp's query rows and running state, 16-bit caches.
 template <typename T, int D>

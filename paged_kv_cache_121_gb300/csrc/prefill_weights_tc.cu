@@ -34,6 +34,7 @@
 // products and copies, frees its tensor memory and returns.
 #include <algorithm>
 
+#include "async_copy.cuh"
 #include "internal.h"
 #include "packed_math.cuh"
 #include "tcgen05.cuh"
@@ -87,19 +88,6 @@ struct Shared {
     __align__(16) float off[2 * kGroupWarps][kSide / 2];   // [warp]: minus what to take from its streamed rows' scores
     float part[2][kSide];                         // [group]: the sums over the second half of the columns
 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void *src, bool live) {
-    const int bytes = live ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
 
 // Whether the phase of this parity has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
