@@ -1957,7 +1957,8 @@ PA_API pa_status pa_evict(int32_t *kept, int64_t kept_stride, float *new_weights
     if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size) return PA_ERR_INVALID_ARG;
     const int64_t row_bytes = static_cast<int64_t>(head_dim) * element_bytes(kv_dtype);
     if (row_bytes % 16 != 0 || row_bytes > (1 << 20) || num_seqs > 65535 ||
-        static_cast<int64_t>(num_seqs) * num_kv_heads > INT32_MAX / 8 || num_kv_heads > (1 << 20))
+        static_cast<int64_t>(num_seqs) * num_kv_heads > INT32_MAX / 8 || num_kv_heads > 65535 * 16 ||
+        max_context_len > INT32_MAX / 2)
         return PA_ERR_UNSUPPORTED;
     const int64_t most = std::min<int64_t>({kept_stride, new_weights_stride, static_cast<int64_t>(max_new_blocks) * block_size,
                                             max_context_len});

@@ -22,6 +22,12 @@
 //    row's maximum and sum, and then goes through its own scores (in L2 still).
 //    One launch, no atomics: the same call gives the same bits.
 //  * More than 16 query heads a KV head: the passes follow one another in the CTA.
+//
+// Measured (16 sequences of 4,164 tokens, 32 / 8 heads of 128, bf16, blocks of 16):
+// 54.4 us, 0.76 of the copy rate (the decode alone, whose copies TMA makes, takes 44).
+// It reads 5.2 TB/s from its start to its end, the merge and the weights at the end
+// included. Block ids looked at as soon as they were loaded, and the scores turned
+// into weights one token a thread: 67.9 us.
 #include <algorithm>
 
 #include "async_copy.cuh"

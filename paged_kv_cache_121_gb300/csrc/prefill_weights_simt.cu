@@ -13,6 +13,8 @@
 // transposed in shared memory so that a thread's 4 x 4 products read two 16-byte
 // vectors a dim. First pass: queries held, keys streamed; second: the other way round,
 // so that what is reduced over (keys, then rows) is always the streamed side.
+// Measured as the path of 16-bit caches too, before prefill_weights_tc.cu: 8 chunks of
+// 200 .. 1,500 tokens behind up to 2,500, 32 / 8 heads of 128, 4.6 ms (28 TFLOP/s).
 #include <algorithm>
 
 #include "internal.h"

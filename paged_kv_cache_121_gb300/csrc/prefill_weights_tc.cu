@@ -30,6 +30,17 @@
 // the groups take every other key tile. Long units first; those of the sums, whose
 // lengths differ most, are drawn from a counter, those of the statistics (cut into
 // pieces of the context) go round the CTAs back and forth.
+//
+// Measured (GB300, 32 / 8 heads of 128). Windows of 32 queries, 16 prompts of 4,100
+// tokens, bf16, blocks of 16: 90 us = statistics 40, between 5, sums 54 (bytes 44 %,
+// tensor pipe 18 %, exponentials 20 %, issue slots 31 % of their rates: a tile comes in
+// about 2,100 cycles, and its 16 boxes of 2 KB have a share in that, since with blocks
+// of 128 the sums take a fifth less; an L2 policy of evict-first or one more tile in
+// flight change nothing). 8 chunks of 200 .. 1,500 tokens behind up to 2,500, fp16,
+// blocks of 32: 169 us = 78 + 7 + 95 (tensor pipe 37 and 30 %, exponentials 39 and
+// 30 %, issue slots 57 and 50 %). Gathered by four copy warps the same two took 123 and
+// 210 us; by one, with a warp a lane quarter and units as they are numbered, 171 and 441.
+//
 // Every wait is bounded; on expiry the kernel records a timeout, waits (bounded) for its
 // products and copies, frees its tensor memory and returns.
 #include <algorithm>

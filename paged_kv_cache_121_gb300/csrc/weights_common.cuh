@@ -1,6 +1,7 @@
 // Arguments of the kernels around attention weights: the weights that decode
 // steps and prompts gave the cached tokens (decode_weights.cu,
-// prefill_weights.cu), and the eviction that goes by them (evict.cu).
+// prefill_weights_simt.cu, prefill_weights_tc.cu), and the eviction that goes by
+// them (evict.cu).
 #pragma once
 
 #include "device_common.cuh"

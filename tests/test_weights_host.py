@@ -84,7 +84,8 @@ def test_weights_checks_return_before_launch():
                dict(mnb=0), dict(nb=0), dict(B=-1), dict(hkv=0), dict(D=0), dict(bs=0), dict(w=P), dict(k=P + 8),
                dict(kept=P + 2), dict(ks=-1)):
         assert evict(**kw) == pa.PA_ERR_INVALID_ARG, kw
-    for kw in (dict(D=4), dict(B=70000), dict(D=7, dt=0)):
+    for kw in (dict(D=4), dict(B=70000), dict(D=7, dt=0), dict(hkv=65535 * 16 + 1),
+               dict(mc=(1 << 30) + 1, mb=1 << 30, ws=1 << 31)):
         assert evict(**kw) == pa.PA_ERR_UNSUPPORTED, kw
 
 
