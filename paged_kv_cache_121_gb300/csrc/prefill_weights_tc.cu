@@ -8,6 +8,8 @@
 //  * statistics: query rows held, keys streamed; a thread keeps its row's running
 //    maximum and sum of 2^(s - maximum);
 //  * sums: keys held, query rows streamed; a thread adds up 2^(s - o_row) for its key.
+//    Where a KV head has 128 query rows or less, they are the held side (and N) again: a
+//    tile of keys is then done with its one product.
 //
 // Bound: the products and the exponentials, 512 cycles a tile each (two passes: twice
 // the products and exponentials of one attention's scores); for windows of few queries,
@@ -26,24 +28,26 @@
 //    exponentials: a tile takes a warp 800 to 1,200 cycles. (TMA gathers of four rows
 //    took 80 cycles each, 5,200 a tile.)
 // A unit holds two tiles, one a group, so that a streamed tile feeds 256 held rows;
-// where a KV head has 128 query rows or less, a unit of the statistics holds one, and
-// the groups take every other key tile. Long units first; those of the sums, whose
+// where a KV head has 128 query rows or less, a unit holds those, and the groups take
+// every other key tile (windows of 32 queries in 16 prompts: the sums 54 us with the
+// keys held, two key tiles a unit for one of rows, and 42 so). Long units first; those of the sums, whose
 // lengths differ most, are drawn from a counter, those of the statistics (cut into
 // pieces of the context) go round the CTAs back and forth.
 //
 // Measured (GB300, 32 / 8 heads of 128). Windows of 32 queries, 16 prompts of 4,100
-// tokens, bf16, blocks of 16: 90 us = statistics 40, between 5, sums 54 (bytes 44 %,
-// tensor pipe 18 %, exponentials 20 %, issue slots 31 % of their rates: a tile comes in
-// about 2,100 cycles, and its 16 boxes of 2 KB have a share in that, since with blocks
-// of 128 the sums take a fifth less; an L2 policy of evict-first or one more tile in
-// flight change nothing). 8 chunks of 200 .. 1,500 tokens behind up to 2,500, fp16,
-// blocks of 32: 169 us = 78 + 7 + 95 (tensor pipe 37 and 30 %, exponentials 39 and
-// 30 %, issue slots 57 and 50 %). Gathered by four copy warps the same two took 123 and
+// tokens, bf16, blocks of 16: 77.8 us = statistics 40, between 5, sums 42 (alone, under
+// the profiler; bytes 44 %, tensor pipe 18 %, exponentials 20 %, issue slots 31 and 35 %
+// of their rates: a tile comes in about 2,100 cycles, and its 16 boxes of 2 KB have a
+// share in that, since with blocks of 128 a pass takes a quarter less; an L2 policy of
+// evict-first or one more tile in flight change nothing). 8 chunks of 200 .. 1,500 tokens behind up to 2,500, fp16,
+// blocks of 32: 169 us = 78 + 7 + 92 (tensor pipe 37 and 31 %, exponentials 39 and
+// 32 %, issue slots 57 and 50 %). Gathered by four copy warps the same two took 123 and
 // 210 us; by one, with a warp a lane quarter and units as they are numbered, 171 and 441.
 //
 // Every wait is bounded; on expiry the kernel records a timeout, waits (bounded) for its
 // products and copies, frees its tensor memory and returns.
 #include <algorithm>
+#include <climits>
 
 #include "async_copy.cuh"
 #include "internal.h"
@@ -122,7 +126,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <bool kSums>
 __host__ __device__ __forceinline__ int64_t unit_count(const PrefillWeightsParams &p) {
     const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-    if (kSums) return (static_cast<int64_t>(p.max_ctx) + 2 * kSide - 1) / (2 * kSide) * p.row_pieces * heads;
+    if (kSums && p.pair) return (static_cast<int64_t>(p.max_ctx) + 2 * kSide - 1) / (2 * kSide) * p.row_pieces * heads;
     const int64_t side = p.pair ? 2 * kSide : kSide;
     return (static_cast<int64_t>(p.max_count) * p.group + side - 1) / side * p.pieces * heads;
 }
@@ -157,7 +161,7 @@ __device__ __forceinline__ bool lay_out_sums(const PrefillWeightsParams &p, int 
 // Unit number `at`, longest first; false where there is nothing in it. (Units, rows and keys fit 30 bits.)
 template <bool kSums>
 __device__ __forceinline__ bool lay_out(const PrefillWeightsParams &p, unsigned at, Unit &u) {
-    if (kSums) {
+    if (kSums && p.pair) {
         const int n = static_cast<int>(at / static_cast<unsigned>(p.num_kv_heads));
         u.head = static_cast<int>(at) - n * p.num_kv_heads;
         return lay_out_sums(p, p.order ? p.order[n] : n, u);
@@ -178,7 +182,7 @@ __device__ __forceinline__ bool lay_out(const PrefillWeightsParams &p, unsigned 
     u.held = min(per_unit, row_tiles - u.tile);
     auto end = [&](int tile) {     // one past the last key tile that the row tile sees
         const int row = min(u.rows, (tile + 1) * kSide) - 1;
-        return (u.s.sees(row / p.group) + kSide - 1) / kSide;
+        return ((kSums ? u.s.ctx : u.s.sees(row / p.group)) + kSide - 1) / kSide;   // (every key has a sum)
     };
     const int end0 = end(u.tile), end1 = u.held > 1 ? end(u.tile + 1) : 0;
     const int most = max(end0, end1), per = (most + p.pieces - 1) / p.pieces;
@@ -273,17 +277,20 @@ __device__ __forceinline__ void add_stats(const float (&s)[32], uint64_t scale2,
 template <bool kTma>
 constexpr int kThreads = 32 * (kLoadWarp + (kTma ? 1 : kCopyWarps));
 
-template <int D, bool kF16, bool kTma, bool kSums>
+enum Pass { kStats, kSumsKeysHeld, kSumsRowsHeld };   // (the last: one row tile a KV head, as the statistics take it)
+template <int D, bool kF16, bool kTma, int kPass>
 __global__ void __launch_bounds__(kThreads<kTma>, 1)
 prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ PrefillWeightsParams p, const int held_buffers) {
     using T = TcTile<D>;
     constexpr int kLoadWarps = kTma ? 1 : kCopyWarps;
+    constexpr bool kSums = kPass != kStats;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Shared *sh = reinterpret_cast<Shared *>(tiles + kTileSpace);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool split = !kSums && !p.pair;                // the groups take every other streamed tile of one held tile
+    const bool split = kSums ? kPass == kSumsRowsHeld : !p.pair;   // the groups take every other streamed tile of one held tile
+    constexpr bool held_keys = kPass == kSumsKeysHeld;             // (the other operand is streamed)
     const int held_slots = (split ? 1 : 2) * held_buffers;
     const int str_slots = T::kSlots - held_slots;        // streamed tiles, behind the held ones
 
@@ -434,7 +441,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                 // Long units of the sums are drawn, once the tiles of the one before are on their way: drawn earlier they
                 // would wait here while other CTAs have none. Others go round the CTAs back and forth (a draw would
                 // take as long as a short unit).
-                const bool draws = kSums && held_buffers == 1;
+                const bool draws = held_keys && held_buffers == 1;
                 bool found = false;
                 while (!found && (at < units || (!draws && turn * gridDim.x < units))) {
                     if (at < units) found = lay_out<kSums>(p, at, u);
@@ -460,20 +467,20 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
             if (u.b < 0) break;
             if (u.lo >= u.hi) continue;
             // (a tile's rows are looked up while the one before is sent for)
-            const Place held[2] = {locate(u, kSums, u.tile), locate(u, kSums, u.held > 1 ? u.tile + 1 : u.tile)};
-            Place next = locate(u, !kSums, u.lo);
+            const Place held[2] = {locate(u, held_keys, u.tile), locate(u, held_keys, u.held > 1 ? u.tile + 1 : u.tile)};
+            Place next = locate(u, !held_keys, u.lo);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (i >= u.held || !ok) break;
                 const int n = count[i]++, round = n / held_buffers, buf = n - round * held_buffers;
-                ok = fetch(u, kSums, held[i], i * held_buffers + buf, &sh->held_full[i][buf], &sh->held_empty[i][buf],
+                ok = fetch(u, held_keys, held[i], i * held_buffers + buf, &sh->held_full[i][buf], &sh->held_empty[i][buf],
                            round > 0 ? (round - 1) & 1 : -1);
             }
             for (int i = u.lo; i < u.hi && ok; ++i, ++streamed) {
                 const Place here = next;
-                if (i + 1 < u.hi) next = locate(u, !kSums, i + 1);
+                if (i + 1 < u.hi) next = locate(u, !held_keys, i + 1);
                 const int round = streamed / str_slots, slot = streamed - round * str_slots;
-                ok = fetch(u, !kSums, here, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], round > 0 ? (round - 1) & 1 : -1);
+                ok = fetch(u, !held_keys, here, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], round > 0 ? (round - 1) & 1 : -1);
             }
         }
         if (kTma) {   // nothing is on its way when the CTA ends: the last phase of every slot that was filled
@@ -528,11 +535,13 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                             if (c >= 2 && !wait_one(p, sh, &sh->s_free[g][c & 1], ((c >> 1) - 1) & 1)) return false;
                             tc_fence_after();
                             const uint64_t hd = tile_at(split ? buf[0] : g * held_buffers + buf[g]);
+                            // what is reduced over lies along the columns: keys, in the sums rows
+                            const uint64_t ad = kSums && split ? sd : hd, bd = kSums && split ? hd : sd;
                             const uint32_t to_col = tmem + static_cast<uint32_t>((2 * g + (c & 1)) * kSide);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint64_t step = desc_step((kk / 4) * T::kHalf + (kk % 4) * 32);
-                                tc_mma_16bit(to_col, hd + step, sd + step, id, kk > 0 ? 1u : 0u);
+                                tc_mma_16bit(to_col, ad + step, bd + step, id, kk > 0 ? 1u : 0u);
                             }
                             tc_commit(smem_addr(&sh->s_full[g][c & 1]));
                         }
@@ -568,7 +577,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
         const int g = warp / kGroupWarps, h = (warp / 4) & 1, R = (warp & 3) * 32 + lane;   // group, half of the columns, lane
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
-        int count = 0;            // tiles scored
+        int count = 0, joined = 0;   // tiles scored; sums put together
         bool ok = true, ahead = false;
         float next_off[2] = {0.f, 0.f};   // sums: the offsets of two of this warp's columns in the next tile, once `ahead`
         float *const off = sh->off[warp];
@@ -591,17 +600,50 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
             int whole_from = 0, whole_to = 0;   // sums: row tiles whose rows all exist and see all of the key tile. (Rows past the
                                                 //   last one are zeros, whose products with infinite keys are no numbers)
             if (!kSums && held_row < rows) row_sees = u->s.sees(held_row / p.group);
-            if (kSums) {
-                const int64_t token = static_cast<int64_t>(held_row) - u->s.past;
+            auto key_tile = [&](int t) {
+                const int64_t token = static_cast<int64_t>(t) * kSide + R - u->s.past;
                 first_row = token <= 0 ? 0 : token >= u->s.count ? rows : static_cast<int>(token) * p.group;
-                const int64_t all = static_cast<int64_t>(tile + 1) * kSide - 1 - u->s.past;   // the first token that sees it all
-                whole_to = (tile + 1) * kSide <= u->s.ctx && all < u->s.count ? rows / kSide : 0;
+                const int64_t all = static_cast<int64_t>(t + 1) * kSide - 1 - u->s.past;   // the first token that sees it all
+                whole_to = (t + 1) * kSide <= u->s.ctx && all < u->s.count ? rows / kSide : 0;
                 whole_from = all <= 0 || whole_to == 0 ? 0 : (static_cast<int>(all) * p.group + kSide - 1) / kSide;
+            };
+            auto weight_at = [&](int key) {
+                return p.weights + (static_cast<int64_t>(u->b) * p.num_kv_heads + u->head) * p.weights_stride + key;
+            };
+            float old = 0.f;   // of the thread's key, on its way while the scores are
+            auto look_up_old = [&](int key) {
+                old = h == 0 && key < u->s.ctx && key < u->s.fresh && p.decay != 0.f ? *weight_at(key) : 0.f;
+            };
+            // The two halves of the columns.
+            auto join = [&]() {
+                if (h == 1) {
+                    if (joined > 0 && !wait_warp(p, sh, &sh->part_free[g], (joined - 1) & 1)) return false;
+                    sh->part[g][R] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh->part_full[g]));
+                } else {
+                    if (!wait_warp(p, sh, &sh->part_full[g], joined & 1)) return false;
+                    sum += sh->part[g][R];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh->part_free[g]));
+                }
+                ++joined;
+                return true;
+            };
+            if (kSums && !split) key_tile(tile);
+            if (kSums && split && u->lo < u->hi) {   // one tile of rows: their offsets serve the unit
+                columns(u, u->tile);
+                *reinterpret_cast<float2 *>(off + lane * 2) = make_float2(-next_off[0], -next_off[1]);
+                __syncwarp();
             }
             const int step = split ? 2 : 1, last = u->to[g];
             for (int i = u->from[g] + (split ? g : 0); i < last; i += step, ++count) {
                 const int buf = count & 1;
-                if (kSums) {
+                if (kSums && split) {
+                    key_tile(i);
+                    look_up_old(i * kSide + R);
+                    sum = 0.f;
+                } else if (kSums) {
                     if (!ahead) columns(u, i);
                     *reinterpret_cast<float2 *>(off + lane * 2) = make_float2(-next_off[0], -next_off[1]);
                     ahead = false;
@@ -616,7 +658,8 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                 }
                 if (!wait_warp(p, sh, &sh->s_full[g][buf], (count >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
-                const bool whole = i >= whole_from && i < whole_to;
+                const int row_tile = split ? tile : i;   // (of the sums)
+                const bool whole = row_tile >= whole_from && row_tile < whole_to;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     const int col = h * 64 + part * 32;
@@ -627,7 +670,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&sh->s_free[g][buf]));
                     }
-                    const int c0 = i * kSide + col;   // the first column's row (statistics: key)
+                    const int c0 = (kSums ? row_tile : i) * kSide + col;   // the first column's row (statistics: key)
                     if (kSums) {
                         sum += whole ? sum_weights<false>(s, off + part * 32, scale2, 0, 32)
                                      : sum_weights<true>(s, off + part * 32, scale2, first_row - c0, rows - c0);
@@ -643,27 +686,24 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                         else add_stats<false>(s, scale2, p.scale_log2, top, sum);
                     }
                 }
+                if (kSums && split) {
+                    if (!join()) { ok = false; break; }
+                    const int key = i * kSide + R;
+                    if (h == 0 && key < u->s.ctx) *weight_at(key) = sum + p.decay * old;
+                }
                 if (kSums) __syncwarp();   // the offsets have been read
             }
             if (!ok) break;
-            if (kSums) {   // the two halves of the columns
-                if (h == 1) {
-                    if (k > 0 && !wait_warp(p, sh, &sh->part_free[g], (k - 1) & 1)) break;
-                    sh->part[g][R] = sum;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh->part_full[g]));
-                } else {
-                    if (!wait_warp(p, sh, &sh->part_full[g], k & 1)) break;
-                    sum += sh->part[g][R];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh->part_free[g]));
-                }
-                if (h == 0 && g < u->held && held_row < u->s.ctx) {
-                    float *w = p.weights + (static_cast<int64_t>(u->b) * p.num_kv_heads + u->head) * p.weights_stride + held_row;
-                    if (p.row_pieces > 1)
-                        p.parts[((static_cast<int64_t>(u->piece) * p.num_seqs + u->b) * p.num_kv_heads + u->head) * p.max_ctx + held_row] = sum;
-                    else
-                        *w = sum + (held_row < u->s.fresh && p.decay != 0.f ? p.decay * *w : 0.f);
+            if (kSums) {
+                if (!split) {
+                    look_up_old(p.row_pieces > 1 ? INT_MAX : held_row);
+                    if (!join()) break;
+                    if (h == 0 && g < u->held && held_row < u->s.ctx) {
+                        if (p.row_pieces > 1)
+                            p.parts[((static_cast<int64_t>(u->piece) * p.num_seqs + u->b) * p.num_kv_heads + u->head) * p.max_ctx + held_row] = sum;
+                        else
+                            *weight_at(held_row) = sum + p.decay * old;
+                    }
                 }
             } else if ((split || g < u->held) && held_row < rows) {
                 const int token = held_row / p.group;
@@ -740,28 +780,31 @@ __global__ void __launch_bounds__(kOrderThreads) weight_parts_kernel(const __gri
 constexpr size_t kSmemBytes = 1024 + kTileSpace + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
-template <int D, bool kF16, bool kTma, bool kSums>
+template <int D, bool kF16, bool kTma, int kPass>
 cudaError_t launch_pass(const PrefillWeightsParams &p, const CUtensorMap &map_q, const CUtensorMap &map_k, int sms, cudaStream_t stream) {
-    auto kern = prefill_weights_tc_kernel<D, kF16, kTma, kSums>;
+    constexpr bool kSums = kPass != kStats;
+    auto kern = prefill_weights_tc_kernel<D, kF16, kTma, kPass>;
     static unsigned long long done = 0;
     const cudaError_t e = ensure_smem_limit(kern, kSmemBytes, done);
     if (e != cudaSuccess) return e;
     // A unit that streams many tiles: more of them on their way. Short units: the next one's held tiles too.
-    const int64_t streamed = kSums ? (static_cast<int64_t>(p.max_count) * p.group + kSide - 1) / kSide
-                                   : ((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide + p.pieces - 1) / p.pieces;
-    const int held_buffers = (kSums || p.pair) && streamed >= kLongUnit ? 1 : 2;
+    const int64_t streamed = kPass == kSumsKeysHeld ? (static_cast<int64_t>(p.max_count) * p.group + kSide - 1) / kSide
+                                             : ((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide + p.pieces - 1) / p.pieces;
+    const int held_buffers = p.pair && streamed >= kLongUnit ? 1 : 2;
     return launch_kernel(kern, dim3(static_cast<unsigned>(std::min<int64_t>(unit_count<kSums>(p), sms))), dim3(kThreads<kTma>),
                          kSmemBytes, stream, 1u, map_q, map_k, p, held_buffers);
 }
 
 template <int D, bool kF16, bool kTma>
 cudaError_t launch_both(const PrefillWeightsParams &p, const CUtensorMap &map_q, const CUtensorMap &map_k, int sms, cudaStream_t stream) {
-    cudaError_t e = launch_pass<D, kF16, kTma, false>(p, map_q, map_k, sms, stream);
+    cudaError_t e = launch_pass<D, kF16, kTma, kStats>(p, map_q, map_k, sms, stream);
     if (e == cudaSuccess)
         e = launch_kernel(weight_between_kernel,
                           dim3(static_cast<unsigned>((p.stat_rows * p.num_heads + kOrderThreads - 1) / kOrderThreads + 1)),
                           dim3(kOrderThreads), 0, stream, 1u, p, static_cast<int>(unit_count<true>(p) / p.num_kv_heads));
-    if (e == cudaSuccess) e = launch_pass<D, kF16, kTma, true>(p, map_q, map_k, sms, stream);
+    if (e == cudaSuccess)
+        e = p.pair ? launch_pass<D, kF16, kTma, kSumsKeysHeld>(p, map_q, map_k, sms, stream)
+                   : launch_pass<D, kF16, kTma, kSumsRowsHeld>(p, map_q, map_k, sms, stream);
     if (e != cudaSuccess || p.row_pieces == 1) return e;
     const dim3 grid(static_cast<unsigned>((p.max_ctx + kOrderThreads - 1) / kOrderThreads),
                     static_cast<unsigned>(p.num_seqs * p.num_kv_heads));
