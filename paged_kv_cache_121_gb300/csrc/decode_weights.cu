@@ -16,7 +16,10 @@
 //    token & 7), so that the matrix loads have no bank conflicts.
 //  * 16-bit caches: products on mma.m16n8k16 (M = the query heads, 16 at most a pass;
 //    bound by memory, so the wider tcgen05 tiles would stand empty), softmax online in
-//    base 2, weights of V in two 16-bit parts, as in decode_mma.cu. fp32: CUDA cores.
+//    base 2. fp32: CUDA cores.
+//  * The weights of V enter the products in parts of the caches' type, as many as keep
+//    fp32's bits: two of fp16 (11 bits each and their signs), three of bf16 (8 bits each).
+//    Two of bf16 left 2^-17 of a weight, seen in fp32 outputs.
 //  * The warps' states meet in shared memory, the cluster's CTAs through distributed
 //    shared memory; each CTA merges a slice of the outputs and, for itself, every
 //    row's maximum and sum, and then goes through its own scores (in L2 still).
@@ -54,11 +57,29 @@ struct StepCfg {
     static_assert(kState * 4 <= kRingBytes, "a warp's state takes its ring's place");
 };
 
+// Weights as a sum of 16-bit parts, two weights a register: bf16 takes the upper halves of what is left, whose 24 bits
+// three parts hold exactly.
+template <bool kF16, int kParts>
+__device__ __forceinline__ void split_parts(float x, float y, uint32_t (&part)[kParts]) {
+    if constexpr (kF16) {
+        split_f16x2(x, y, part[0], part[1]);
+    } else {
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) {
+            const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+            part[n] = __byte_perm(a, b, 0x7632);
+            x -= __uint_as_float(a & 0xffff0000u);
+            y -= __uint_as_float(b & 0xffff0000u);
+        }
+    }
+}
+
 // One warp's query rows and running state, 16-bit caches.
 template <typename T, int D>
 struct StepTile {
     using C = StepCfg<T, D>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
+    static constexpr int kParts = kF16 ? 2 : 3;   // of a weight
     WarpState<D> st;
     uint32_t qa[D / 16][4];
 
@@ -129,15 +150,21 @@ struct StepTile {
         }
         // (a row that has seen nothing but -inf has m = -inf: its weights are zeros)
         const float b0 = st.m0 == -INFINITY ? 0.f : st.m0, b1 = st.m1 == -INFINITY ? 0.f : st.m1;
-        uint32_t hi[4], lo[4];
+        uint32_t part[kParts][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float p0 = fast_exp2(s[j][0] - b0), p1 = fast_exp2(s[j][1] - b0);
             const float p2 = fast_exp2(s[j][2] - b1), p3 = fast_exp2(s[j][3] - b1);
             st.l0 += p0 + p1;
             st.l1 += p2 + p3;
-            split_x2<kF16>(p0, p1, hi[2 * j], lo[2 * j]);
-            split_x2<kF16>(p2, p3, hi[2 * j + 1], lo[2 * j + 1]);
+            uint32_t of0[kParts], of1[kParts];
+            split_parts<kF16>(p0, p1, of0);
+            split_parts<kF16>(p2, p3, of1);
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) {
+                part[n][2 * j] = of0[n];
+                part[n][2 * j + 1] = of1[n];
+            }
         }
 #pragma unroll
         for (int dn = 0; dn < D / 8; dn += 2) {
@@ -145,10 +172,11 @@ struct StepTile {
             const int tok = (mi & 1) * 8 + (lane & 7), c = dn + (mi >> 1);
             uint32_t v0, v1, v2, v3;
             ldmatrix_x4_trans(vbase + tok * C::kRow + ((c ^ (tok & 7)) << 4), v0, v1, v2, v3);
-            mma_16816<kF16>(st.o[dn], hi, v0, v1);
-            mma_16816<kF16>(st.o[dn + 1], hi, v2, v3);
-            mma_16816<kF16>(st.o[dn], lo, v0, v1);
-            mma_16816<kF16>(st.o[dn + 1], lo, v2, v3);
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) {
+                mma_16816<kF16>(st.o[dn], part[n], v0, v1);
+                mma_16816<kF16>(st.o[dn + 1], part[n], v2, v3);
+            }
         }
     }
 

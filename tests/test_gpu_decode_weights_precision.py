@@ -1,0 +1,44 @@
+"""pa_decode_weights keeps 24 bits of every softmax weight on its way to the outputs.
+
+Queries have one dim that is not zero, so that a score is one product, exact in fp32; value t is 1 in dim t and zero
+elsewhere, so that dim t of an output is the weight of token t alone.
+
+Tolerance, with e = 2^-24 (half a step of fp32). Scores are at most 1, base 2 below 1.45: their factor (scale times
+log2 of e) rounds once ahead and once as a product, the maximum alike, and their difference once more:
+ln 2 (4 * 1.45 + 2.9) e < 7 e; exp2 is good to 2 units, 4 e. So a weight is off by less than 11 e of itself, the sum
+under it by as much and by its own roundings, at most n / 16 + 8 <= 15 (n <= 100 tokens, partial sums over lanes and
+warps); the merge of the warps multiplies and adds twice more (their factors are exp2: 4 e), the quotient rounds
+twice. Together under 2 * 11 + 15 + 8 + 4 = 49 e for exact parts of the weights; the weights' parts in 16 bits may add
+2 e (two of fp16: 11 bits and a sign each; three of bf16: none). The output rounds by half a step, e, and dims whose
+value is zero stay zero."""
+import pytest
+import torch
+
+import paged_kv_cache_121_gb300 as pa
+from weights_cases import DT, E, Paged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("hq,hkv,d,lens", [(16, 2, 64, (64, 33, 7)), (8, 8, 128, (100,) * 5), (40, 2, 128, (97, 64))])
+def test_outputs_hold_24_bits_of_a_weight(dt, hq, hkv, d, lens):
+    paged = Paged(lens, hkv, d, 16, dt, 21)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    q = torch.zeros(len(lens), hq, d, dtype=DT[dt], device="cuda")
+    q[:, :, 0] = 1
+    want = torch.zeros(len(lens), hq, d, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        key = (torch.rand(n, hkv, generator=g, device="cuda") * 2 - 1).to(DT[dt])
+        t = torch.arange(n, device="cuda")
+        blk = torch.from_numpy(paged.table[b].astype("int64")).cuda()[t // paged.bs]
+        paged.k[blk, t % paged.bs] = 0
+        paged.k[blk, t % paged.bs, :, 0] = key
+        paged.v[blk, t % paged.bs] = torch.eye(n, d, dtype=DT[dt], device="cuda")[:, None].expand(n, hkv, d)
+        want[b, :, :n] = torch.softmax(key.double(), 0).T.repeat_interleave(hq // hkv, 0)
+    out = torch.full((len(lens), hq, d), float("nan"), device="cuda")
+    w = torch.zeros(len(lens), hkv, paged.max_ctx, device="cuda")
+    ws = torch.empty(pa.pa_decode_weights_workspace_size(len(lens), hq, hkv, d, 16, paged.max_ctx), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_weights(out, w, q, paged.k, paged.v, paged.tables, paged.context_lens, paged.max_ctx, 1.0, ws)
+    err = (out.double() - want).abs()
+    assert bool((err <= 52 * E * want).all()), float((err / want.clamp(min=1e-30)).max() / E)
