@@ -36,6 +36,7 @@
 #include "async_copy.cuh"
 #include "internal.h"
 #include "mma_tile.cuh"
+#include "packed_math.cuh"
 #include "weights_common.cuh"
 
 namespace pa {
@@ -166,17 +167,27 @@ struct StepTile {
                 part[n][2 * j + 1] = of1[n];
             }
         }
+        // A tile's products are summed from zero, then added: the tensor cores cut off what reaches below a sum's last bit,
+        // always in one direction, which over the tiles of a context came to 2^-17 of an output.
 #pragma unroll
         for (int dn = 0; dn < D / 8; dn += 2) {
             const int mi = lane >> 3;
             const int tok = (mi & 1) * 8 + (lane & 7), c = dn + (mi >> 1);
-            uint32_t v0, v1, v2, v3;
-            ldmatrix_x4_trans(vbase + tok * C::kRow + ((c ^ (tok & 7)) << 4), v0, v1, v2, v3);
+            uint32_t v[4];
+            ldmatrix_x4_trans(vbase + tok * C::kRow + ((c ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
+            float o[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-            for (int n = 0; n < kParts; ++n) {
-                mma_16816<kF16>(st.o[dn], part[n], v0, v1);
-                mma_16816<kF16>(st.o[dn + 1], part[n], v2, v3);
+            for (int n = kParts - 1; n >= 0; --n) {   // the smallest first
+                mma_16816<kF16>(o[0], part[n], v[0], v[1]);
+                mma_16816<kF16>(o[1], part[n], v[2], v[3]);
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float *to = st.o[dn + i];
+                    unpair(add2(pair(to[e], to[e + 1]), pair(o[i][e], o[i][e + 1])), to[e], to[e + 1]);
+                }
         }
     }
 

@@ -42,3 +42,32 @@ def test_outputs_hold_24_bits_of_a_weight(dt, hq, hkv, d, lens):
     pa.pa_decode_weights(out, w, q, paged.k, paged.v, paged.tables, paged.context_lens, paged.max_ctx, 1.0, ws)
     err = (out.double() - want).abs()
     assert bool((err <= 52 * E * want).all()), float((err / want.clamp(min=1e-30)).max() / E)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_outputs_are_not_cut_in_one_direction(dt):
+    """Many positive values of one size: an output is off by roundings of either sign, whose mean over all outputs
+    is near nothing, and by what the tensor cores cut off within one tile, 2 e a product at most and three of them a
+    tile. (Cut at every tile of a context, 66 of them here, the loss would be ten times that.) Mean of the relative
+    errors: 6 e, and 2 e for what is left of the roundings: a sum of 66 tiles rounds by less than sqrt(66) e in the
+    root mean square, its mean over 2,048 rows by a 45th of that."""
+    B, hq, hkv, d, n = 64, 32, 8, 128, 2100
+    paged = Paged((n,) * B, hkv, d, 16, dt, 23)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    q = torch.zeros(B, hq, d, dtype=DT[dt], device="cuda")
+    q[:, :, 0] = 1
+    paged.k.zero_()
+    paged.k[..., 0] = (torch.rand(paged.k.shape[:3], generator=g, device="cuda") * 2 - 1).to(DT[dt])
+    paged.v.copy_(torch.rand(paged.v.shape, generator=g, device="cuda") * 0.5 + 0.5)
+    out = torch.empty(B, hq, d, device="cuda")
+    w = torch.zeros(B, hkv, n, device="cuda")
+    ws = torch.empty(pa.pa_decode_weights_workspace_size(B, hq, hkv, d, 16, n), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_weights(out, w, q, paged.k, paged.v, paged.tables, paged.context_lens, n, 1.0, ws)
+    t = torch.arange(n, device="cuda")
+    mean = 0.0
+    for b in range(B):
+        blk = torch.from_numpy(paged.table[b].astype("int64")).cuda()[t // 16]
+        p = torch.softmax(paged.k[blk, t % 16, :, 0].double(), 0)
+        want = torch.einsum("th,thd->hd", p, paged.v[blk, t % 16].double()).repeat_interleave(hq // hkv, 0)
+        mean += float(((out[b].double() - want) / want).mean()) / B
+    assert abs(mean) <= 8 * E, mean / E
