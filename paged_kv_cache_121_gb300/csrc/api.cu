@@ -1053,7 +1053,7 @@ struct WeightsPlan {
     int pair, pieces, row_pieces;   // 16-bit caches: prefill_weights_tc's cut
     int64_t ordered;     //   and the units it puts in order
     int nsplit;          // pieces that a row's statistics are made in
-    size_t offsets_at, stats_at, order_at, parts_at, total;   // workspace bytes: the counter, the rows' offsets, ...
+    size_t rows_at, offsets_at, stats_at, order_at, parts_at, total;   // workspace bytes: the counter, the rows' statistics, ...
 };
 
 WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms, bool tc) {
@@ -1074,8 +1074,9 @@ WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, in
                                   s.max_ctx / kWeightStatsMinSplit, kMaxSplits})));
     }
     const size_t all = static_cast<size_t>(pl.stat_rows) * s.num_heads;
-    pl.offsets_at = 256;
-    pl.stats_at = pl.offsets_at + align256(all * sizeof(float));
+    pl.rows_at = 256;
+    pl.offsets_at = pl.rows_at + align256(all * sizeof(float2));
+    pl.stats_at = pl.offsets_at + (tc ? align256(all * sizeof(float)) : 0);
     pl.order_at = pl.stats_at + (pl.nsplit > 1 ? align256(pl.nsplit * all * sizeof(float2)) : 0);
     pl.parts_at = pl.order_at + align256(static_cast<size_t>(pl.ordered) * sizeof(int));
     pl.total = pl.parts_at + (pl.row_pieces > 1 ? align256(static_cast<size_t>(pl.row_pieces) * s.num_seqs * s.num_kv_heads * s.max_ctx *
@@ -1898,7 +1899,8 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.weights = weights;
     char *ws = static_cast<char *>(workspace);
     p.counter = reinterpret_cast<int *>(ws);
-    p.offsets = reinterpret_cast<float *>(ws + pl.offsets_at);
+    p.rows = reinterpret_cast<float2 *>(ws + pl.rows_at);
+    p.offsets = tc ? reinterpret_cast<float *>(ws + pl.offsets_at) : nullptr;
     p.stats = reinterpret_cast<float2 *>(ws + pl.stats_at);
     p.order = pl.ordered ? reinterpret_cast<int *>(ws + pl.order_at) : nullptr;
     p.parts = reinterpret_cast<float *>(ws + pl.parts_at);
@@ -1922,9 +1924,9 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     p.pair = pl.pair;
     p.pieces = pl.pieces;
     p.scale_log2 = scale * kLog2e;
-    // masked scores are infinities before the scale on the tensor cores: a zero scale would make them
-    // NaN; the smallest normal number gives the same weights, all alike
-    if (tc && std::fabs(p.scale_log2) < FLT_MIN) p.scale_log2 = FLT_MIN;
+    // masked scores are infinities ahead of the scale: a zero scale would make them NaN; the smallest
+    // number gives the same weights, all alike
+    if (p.scale_log2 == 0.f) p.scale_log2 = FLT_TRUE_MIN;
     p.decay = decay;
     p.status = status_word(dev);
     if (!p.status) return PA_ERR_CUDA;

@@ -2,8 +2,9 @@
 // CUDA cores (fp32 caches; 16-bit caches take prefill_weights_tc.cu).
 //
 // Mathematics. weights[t] gains the sum over rows i (query tokens that count x query
-// heads of the KV head) of 2^(s_it - o_i), s = scale * q.k * log2(e), o_i = the row's
-// maximum + log2 of its sum. The sum over rows needs every row's o_i, so K is passed
+// heads of the KV head) of 2^((s_it - b_i) scale) / l_i, s = q.k, scale times log2(e), b_i
+// the row's score that weighs most, l_i the sum of those powers. The sum over rows needs
+// every row's b_i and l_i, so K is passed
 // over twice: first the rows' statistics, then the sums. The scores are computed again
 // in the second pass: kept they would be 4 bytes a pair to write and read, some
 // hundred times the bytes of K.
@@ -104,6 +105,7 @@ weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     const int per = (key_tiles + p.nsplit - 1) / p.nsplit;
     load_tile<D>(held, [&](int r) { return at.query(r0 + r); });
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    const float sign = p.scale_log2 < 0.f ? -1.f : 1.f, size = fabsf(p.scale_log2);
     int sees[4];
     float m[4], l[4];
 #pragma unroll
@@ -124,14 +126,14 @@ weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
             float top = m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                q[i][j] = kt * kSide + 4 * x + j < sees[i] ? q[i][j] * p.scale_log2 : -INFINITY;
+                q[i][j] = kt * kSide + 4 * x + j < sees[i] ? q[i][j] * sign : -INFINITY;
                 top = fmaxf(top, q[i][j]);
             }
             const float base = top == -INFINITY ? 0.f : top;
-            l[i] *= fast_exp2(m[i] - base);
+            l[i] *= fast_exp2((m[i] - base) * size);
             m[i] = top;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) l[i] += fast_exp2(q[i][j] - base);
+            for (int j = 0; j < 4; ++j) l[i] += fast_exp2((q[i][j] - base) * size);
         }
     }
     // the 16 threads of a row
@@ -140,7 +142,7 @@ weight_stats_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
         float top = m[i];
 #pragma unroll
         for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float sum = l[i] * fast_exp2(m[i] - (top == -INFINITY ? 0.f : top));
+        float sum = l[i] * fast_exp2((m[i] - (top == -INFINITY ? 0.f : top)) * size);
 #pragma unroll
         for (int d = 1; d < 16; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         const int64_t r = r0 + 4 * y + i;
@@ -154,7 +156,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
 weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     extern __shared__ __align__(16) float tiles[];
-    __shared__ float offset[kSide];
+    __shared__ float2 stats[kSide];
     __shared__ int sees[kSide];
     float *held = tiles, *streamed = tiles + D * kPitch;
     grid_dependency_wait();
@@ -175,7 +177,7 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
         if (threadIdx.x < kSide) {
             const int64_t r = r0 + threadIdx.x;
             const bool live = r < rows;
-            offset[threadIdx.x] = live ? p.offsets[(s.stat0 + r / p.group) * p.num_heads + head * p.group + r % p.group] : INFINITY;
+            stats[threadIdx.x] = live ? p.rows[(s.stat0 + r / p.group) * p.num_heads + head * p.group + r % p.group] : make_float2(0.f, 0.f);
             sees[threadIdx.x] = live ? s.sees(static_cast<int>(r / p.group)) : 0;
         }
         __syncthreads();
@@ -183,11 +185,11 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
         tile_product<D>(held, streamed, q);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float o = offset[4 * x + j];
+            const float2 row = stats[4 * x + j];
             const int n = sees[4 * x + j];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (t0 + 4 * y + i < n) sum[i] += fast_exp2(q[i][j] * p.scale_log2 - o);
+                if (t0 + 4 * y + i < n) sum[i] += fast_exp2((q[i][j] - row.x) * p.scale_log2) * row.y;
         }
     }
 #pragma unroll
@@ -202,7 +204,7 @@ weight_sums_simt_kernel(const __grid_constant__ PrefillWeightsParams p) {
     }
 }
 
-__global__ void __launch_bounds__(kThreads) weight_offsets_kernel(const __grid_constant__ PrefillWeightsParams p) {
+__global__ void __launch_bounds__(kThreads) weight_merge_kernel(const __grid_constant__ PrefillWeightsParams p) {
     grid_dependency_wait();
     grid_dependents_launch();
     merge_stats(p, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x);
@@ -220,7 +222,7 @@ cudaError_t launch_simt(const PrefillWeightsParams &p, cudaStream_t stream) {
                     static_cast<unsigned>(p.num_seqs));
     e = launch_kernel(weight_stats_simt_kernel<D>, rows, dim3(kThreads), smem, stream, 1u, p);
     if (e == cudaSuccess && p.nsplit > 1)
-        e = launch_kernel(weight_offsets_kernel, dim3(static_cast<unsigned>((p.stat_rows * p.num_heads + kThreads - 1) / kThreads)),
+        e = launch_kernel(weight_merge_kernel, dim3(static_cast<unsigned>((p.stat_rows * p.num_heads + kThreads - 1) / kThreads)),
                           dim3(kThreads), 0, stream, 1u, p);
     if (e != cudaSuccess) return e;
     const dim3 keys(static_cast<unsigned>((static_cast<int64_t>(p.max_ctx) + kSide - 1) / kSide),

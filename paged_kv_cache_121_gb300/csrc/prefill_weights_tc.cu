@@ -6,8 +6,8 @@
 // memory with a held row a lane, so that what is reduced over lies along a thread's own
 // columns:
 //  * statistics: query rows held, keys streamed; a thread keeps its row's running
-//    maximum and sum of 2^(s - maximum);
-//  * sums: keys held, query rows streamed; a thread adds up 2^(s - o_row) for its key.
+//    maximum and sum;
+//  * sums: keys held, query rows streamed; a thread adds up the rows' weights of its key.
 //    Where a KV head has 128 query rows or less, they are the held side (and N) again: a
 //    tile of keys is then done with its one product.
 //
@@ -100,7 +100,7 @@ struct Shared {
     uint32_t tmem;
     int abort_flag;
     Unit unit[kUnits];
-    __align__(16) float off[2 * kGroupWarps][kSide / 2];   // [warp]: minus what to take from its streamed rows' scores
+    __align__(16) float minus[2 * kGroupWarps][kSide / 2], inverse[2 * kGroupWarps][kSide / 2];   // [warp]: of its columns' rows
     float part[2][kSide];                         // [group]: the sums over the second half of the columns
 };
 
@@ -225,20 +225,34 @@ __device__ __forceinline__ bool wait_warp(const PrefillWeightsParams &p, Shared 
     return __all_sync(0xffffffffu, wait_one(p, sh, bar, parity));
 }
 
-// Sum of 2^(s * scale - offset) over 32 streamed rows; kMasked: only over columns see .. end - 1.
-template <bool kMasked>
-__device__ __forceinline__ float sum_weights(const float (&s)[32], const float *minus_off, uint64_t scale2, int see, int end) {
+// Sum of a key's weights from 32 columns' rows; kMasked: only over columns see .. end - 1 (the product of a row that is
+// left out may be no number). kFolded: `minus` holds minus the rows' folded_stats, else minus their best scores.
+// What the warp reads of its rows is read by every lane, 16 bytes in 4 cycles of the shared memory: the one number takes
+// as long as the tile's exponentials, two took the keys-held pass of the ragged chunks from 92 us to 112.
+template <bool kMasked, bool kFolded>
+__device__ __forceinline__ float sum_weights(const float (&s)[32], const float *minus, const float *inverse, uint64_t scale2,
+                                             int see, int end) {
     uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
     for (int c = 0; c < 32; c += 4) {
-        const float4 o = *reinterpret_cast<const float4 *>(minus_off + c);
+        const float4 m = *reinterpret_cast<const float4 *>(minus + c);
+        const uint64_t s0 = pair(s[c], s[c + 1]), s1 = pair(s[c + 2], s[c + 3]), m0 = pair(m.x, m.y), m1 = pair(m.z, m.w);
         float e[4];
-        unpair(fma2(pair(s[c], s[c + 1]), scale2, pair(o.x, o.y)), e[0], e[1]);
-        unpair(fma2(pair(s[c + 2], s[c + 3]), scale2, pair(o.z, o.w)), e[2], e[3]);
+        unpair(kFolded ? fma2(s0, scale2, m0) : mul2(add2(s0, m0), scale2), e[0], e[1]);
+        unpair(kFolded ? fma2(s1, scale2, m1) : mul2(add2(s1, m1), scale2), e[2], e[3]);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            e[n] = fast_exp2(e[n]);
-            if (kMasked && (c + n < see || c + n >= end)) e[n] = 0.f;
+        for (int n = 0; n < 4; ++n) e[n] = fast_exp2(e[n]);
+        if (!kFolded) {
+            const float4 inv = *reinterpret_cast<const float4 *>(inverse + c);
+            e[0] *= inv.x;
+            e[1] *= inv.y;
+            e[2] *= inv.z;
+            e[3] *= inv.w;
+        }
+        if (kMasked) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (c + n < see || c + n >= end) e[n] = 0.f;
         }
         acc[0] = add2(acc[0], pair(e[0], e[1]));
         acc[1] = add2(acc[1], pair(e[2], e[3]));
@@ -248,7 +262,7 @@ __device__ __forceinline__ float sum_weights(const float (&s)[32], const float *
     return a + b;
 }
 
-// A row's maximum (raw scores, times the scale's sign) and sum of 2^(s * scale - maximum) go on with 32 keys.
+// A row's maximum (raw scores, times the scale's sign) and sum of 2^((s - best) * scale) go on with 32 keys.
 template <bool kNegative>
 __device__ __forceinline__ void add_stats(const float (&s)[32], uint64_t scale2, float scale, float &top, float &sum) {
     float best[4] = {top, top, top, top};
@@ -258,15 +272,15 @@ __device__ __forceinline__ void add_stats(const float (&s)[32], uint64_t scale2,
         for (int n = 0; n < 4; ++n)
             best[n] = kNegative ? max3(best[n], -s[c + 2 * n], -s[c + 2 * n + 1]) : max3(best[n], s[c + 2 * n], s[c + 2 * n + 1]);
     const float up = max3(fmaxf(best[0], best[1]), best[2], best[3]);
-    const float size = fabsf(scale), ref = up == -INFINITY ? 0.f : up * size;   // (nothing seen yet: 2^-inf = 0)
-    sum *= fast_exp2(top * size - ref);
+    const float ref = up == -INFINITY ? 0.f : up;   // (nothing seen yet: 2^-inf = 0)
+    sum *= fast_exp2((top - ref) * fabsf(scale));
     top = up;
-    const uint64_t minus = pair(-ref, -ref);
+    const uint64_t minus = kNegative ? pair(ref, ref) : pair(-ref, -ref);
     uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
         float a, b;
-        unpair(fma2(pair(s[2 * c], s[2 * c + 1]), scale2, minus), a, b);
+        unpair(mul2(add2(pair(s[2 * c], s[2 * c + 1]), minus), scale2), a, b);
         acc[c & 1] = add2(acc[c & 1], pair(fast_exp2(a), fast_exp2(b)));
     }
     float a, b;
@@ -579,15 +593,31 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
         int count = 0, joined = 0;   // tiles scored; sums put together
         bool ok = true, ahead = false;
-        float next_off[2] = {0.f, 0.f};   // sums: the offsets of two of this warp's columns in the next tile, once `ahead`
-        float *const off = sh->off[warp];
+        float next_off[2] = {0.f, 0.f};   // sums, keys held: folded_stats of two of this warp's columns in the next tile, once `ahead`
+        bool folded = false;              // all of a tile's columns are
+        float *const minus = sh->minus[warp], *const inverse = sh->inverse[warp];
+        // A row's place among those of all KV heads.
+        auto place = [&](const Unit *u, int r) {
+            return u->s.stat0 * p.num_heads + u->head * p.group + r + static_cast<int64_t>(p.group_div.of(r)) * (p.num_heads - p.group);
+        };
         auto columns = [&](const Unit *u, int i) {   // (loaded here, used a tile later)
-            const float *from = p.offsets + u->s.stat0 * p.num_heads + u->head * p.group;
-            const int r = i * kSide + h * 64 + lane * 2, rows = u->rows, skip = p.num_heads - p.group;
+            const int r = i * kSide + h * 64 + lane * 2, rows = u->rows;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)   // (a row's place among those of all KV heads)
-                next_off[n] = r + n < rows ? from[r + n + static_cast<int64_t>(p.group_div.of(r + n)) * skip] : INFINITY;
+            for (int n = 0; n < 2; ++n) next_off[n] = r + n < rows ? p.offsets[place(u, r + n)] : INFINITY;
             ahead = true;
+        };
+        auto lay_down_two_numbers = [&](const Unit *u, int i) {
+            const int r = i * kSide + h * 64 + lane * 2, rows = u->rows;
+            float2 row[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) row[n] = r + n < rows ? p.rows[place(u, r + n)] : make_float2(0.f, 0.f);
+            *reinterpret_cast<float2 *>(minus + lane * 2) = make_float2(-row[0].x, -row[1].x);
+            *reinterpret_cast<float2 *>(inverse + lane * 2) = make_float2(row[0].y, row[1].y);
+        };
+        auto lay_down_columns = [&](const Unit *u, int i) {
+            folded = __all_sync(0xffffffffu, next_off[0] == next_off[0] && next_off[1] == next_off[1]);
+            if (folded) *reinterpret_cast<float2 *>(minus + lane * 2) = make_float2(-next_off[0], -next_off[1]);
+            else lay_down_two_numbers(u, i);
         };
         for (int k = 0; ok; ++k) {
             if (!unit_ready(k)) break;
@@ -631,9 +661,8 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                 return true;
             };
             if (kSums && !split) key_tile(tile);
-            if (kSums && split && u->lo < u->hi) {   // one tile of rows: their offsets serve the unit
-                columns(u, u->tile);
-                *reinterpret_cast<float2 *>(off + lane * 2) = make_float2(-next_off[0], -next_off[1]);
+            if (kSums && split && u->lo < u->hi) {   // one tile of rows: their statistics serve the unit
+                lay_down_two_numbers(u, u->tile);
                 __syncwarp();
             }
             const int step = split ? 2 : 1, last = u->to[g];
@@ -645,7 +674,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                     sum = 0.f;
                 } else if (kSums) {
                     if (!ahead) columns(u, i);
-                    *reinterpret_cast<float2 *>(off + lane * 2) = make_float2(-next_off[0], -next_off[1]);
+                    lay_down_columns(u, i);
                     ahead = false;
                     if (i + 1 < last) {
                         columns(u, i + 1);
@@ -672,8 +701,14 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                     }
                     const int c0 = (kSums ? row_tile : i) * kSide + col;   // the first column's row (statistics: key)
                     if (kSums) {
-                        sum += whole ? sum_weights<false>(s, off + part * 32, scale2, 0, 32)
-                                     : sum_weights<true>(s, off + part * 32, scale2, first_row - c0, rows - c0);
+                        const float *const m = minus + part * 32, *const inv = inverse + part * 32;
+                        if (held_keys && folded)
+                            sum += whole ? sum_weights<false, true>(s, m, inv, scale2, 0, 32)
+                                         : sum_weights<true, true>(s, m, inv, scale2, first_row - c0, rows - c0);
+                        else if (!held_keys && whole)
+                            sum += sum_weights<false, false>(s, m, inv, scale2, 0, 32);
+                        else
+                            sum += sum_weights<true, false>(s, m, inv, scale2, first_row - c0, rows - c0);
                     } else {
                         const bool negative = p.scale_log2 < 0.f;
                         if (__any_sync(0xffffffffu, c0 + 32 > row_sees)) {
@@ -691,7 +726,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                     const int key = i * kSide + R;
                     if (h == 0 && key < u->s.ctx) *weight_at(key) = sum + p.decay * old;
                 }
-                if (kSums) __syncwarp();   // the offsets have been read
+                if (kSums) __syncwarp();   // the columns' statistics have been read
             }
             if (!ok) break;
             if (kSums) {
@@ -707,8 +742,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
                 }
             } else if ((split || g < u->held) && held_row < rows) {
                 const int token = held_row / p.group;
-                leave_stats(p, 2 * (split ? 2 * u->piece + g : u->piece) + h, u->s.stat0 + token, u->head * p.group + held_row - token * p.group,
-                            top * fabsf(p.scale_log2), sum);
+                leave_stats(p, 2 * (split ? 2 * u->piece + g : u->piece) + h, u->s.stat0 + token, u->head * p.group + held_row - token * p.group, top, sum);
             }
             unit_read(k);
         }

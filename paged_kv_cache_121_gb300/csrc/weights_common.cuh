@@ -49,7 +49,8 @@ struct PrefillWeightsParams {
     const void *k_cache;
     const int32_t *block_tables, *context_lens, *query_start;
     float *weights;               // [num_seqs, num_kv_heads, weights_stride]
-    float *offsets;               // [stat_rows][num_heads]: what to take from a row's scores (base 2) before 2^x
+    float2 *rows;                 // [stat_rows][num_heads]: a row's score that weighs most and 1 / sum (see row_stats)
+    float *offsets;               //   the same in one number, where that will do (prefill_weights_tc; see folded_stats)
     float2 *stats;                // nsplit > 1: [nsplit][stat_rows][num_heads] maximum and sum of each piece
     int *counter;                 // prefill_weights_tc: units of the second pass drawn beyond one a CTA
     int *order;                   //   its units (one KV head's), longest first, or null (as they are numbered)
@@ -66,7 +67,7 @@ struct PrefillWeightsParams {
     int pieces, pair;             // prefill_weights_tc: ranges of keys a unit of rows is cut into; 1: a unit is two
                                   //   row tiles, else one whose two halves of each range make a piece each
     int row_pieces;               // ranges of rows that a unit of keys is cut into
-    float scale_log2, decay;
+    float scale_log2, decay;      // (scale_log2 is not zero: masked scores are infinities ahead of it)
 };
 
 // One sequence's extent, clamped so that no index leaves its array whatever the device-side lengths hold.
@@ -107,16 +108,31 @@ __device__ __forceinline__ WeightSeq weight_seq(const PrefillWeightsParams &p, i
     return s;
 }
 
-// What to take from a row's scores: maximum + log2(sum), so that 2^x are its weights. A row that weighs
-// nothing takes plus infinity.
-__device__ __forceinline__ float row_offset(float top, float sum) {
-    return sum > 0.f ? top + log2f(sum) : sum == 0.f ? INFINITY : sum;   // (the last: NaN)
+// A row's weights are 2^((s - best) * scale) / sum of them, s its products q.k and `best` the one that weighs most, in
+// both passes alike: the difference is taken first, where it is exact for those that weigh anything, so that scores of
+// any size leave weights that add up to 1. (Maximum and logarithm of the sum in one number lost the sum, and the
+// rounding of the scaled maximum, from scores of 2^12 on.)
+// What the passes hand on: the maximum of s * sign(scale) and the sum; in the end (best, 1 / sum). A row that weighs
+// nothing has an inverse of zero, one with a NaN that.
+__device__ __forceinline__ float2 row_stats(const PrefillWeightsParams &p, float top, float sum) {
+    if (sum == 0.f) return make_float2(0.f, 0.f);
+    return make_float2(p.scale_log2 < 0.f ? -top : top, 1.f / sum);
 }
 
-// A row's statistics over one piece of its context; the only piece leaves the offset itself.
+// best * scale + log2(sum), so that 2^(s * scale - that) is the weight: half of row_stats to read, one instruction less
+// a score. It rounds by 2^-19 at most up to this size, 1.3e-6 of the row's weights and no more than fp32 rounds a
+// scaled score of that size by. NaN for larger ones (and rows with a NaN): they take the two numbers.
+constexpr float kFoldedMost = 64.f;
+__device__ __forceinline__ float folded_stats(const PrefillWeightsParams &p, float top, float sum) {
+    if (sum == 0.f) return INFINITY;
+    const float offset = fmaf(top, fabsf(p.scale_log2), log2f(sum));
+    return fabsf(offset) <= kFoldedMost ? offset : __int_as_float(0x7fffffff);
+}
+
+// A row's statistics over one piece of its context; the only piece leaves the row's own.
 __device__ __forceinline__ void leave_stats(const PrefillWeightsParams &p, int piece, int64_t stat, int head, float top,
                                             float sum) {
-    if (p.nsplit == 1) p.offsets[stat * p.num_heads + head] = row_offset(top, sum);
+    if (p.nsplit == 1) p.rows[stat * p.num_heads + head] = row_stats(p, top, sum);   // (offsets: more pieces alone)
     else p.stats[(piece * p.stat_rows + stat) * p.num_heads + head] = make_float2(top, sum);
 }
 
@@ -124,6 +140,7 @@ __device__ __forceinline__ void leave_stats(const PrefillWeightsParams &p, int p
 __device__ __forceinline__ void merge_stats(const PrefillWeightsParams &p, int64_t i) {
     const int64_t all = p.stat_rows * p.num_heads;
     if (i >= all) return;
+    const float size = fabsf(p.scale_log2);
     float top = -INFINITY, sum = 0.f;
     for (int s0 = 0; s0 < p.nsplit; s0 += 8) {
         float2 ml[8];
@@ -132,11 +149,12 @@ __device__ __forceinline__ void merge_stats(const PrefillWeightsParams &p, int64
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             const float up = fmaxf(top, ml[s].x), ref = up == -INFINITY ? 0.f : up;
-            sum = sum * fast_exp2(top - ref) + ml[s].y * fast_exp2(ml[s].x - ref);
+            sum = sum * fast_exp2((top - ref) * size) + ml[s].y * fast_exp2((ml[s].x - ref) * size);
             top = up;
         }
     }
-    p.offsets[i] = row_offset(top, sum);
+    p.rows[i] = row_stats(p, top, sum);
+    if (p.offsets) p.offsets[i] = folded_stats(p, top, sum);
 }
 
 struct EvictParams {
