@@ -509,7 +509,8 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
  *   new_tables    [num_seqs, max_new_blocks] int32: blocks of the same pool. None
  *                 may be a block that this call reads or lists twice; the old
  *                 blocks are not written, so ones that other sequences share
- *                 stay right (pa_bm_compact hands out such blocks).
+ *                 stay right (one pa_bm_compact_group over the call's sequences
+ *                 hands out such blocks).
  *   keep_lens     [num_seqs] int32; at most kept_stride, new_weights_stride and
  *                 max_new_blocks * block_size (longer ones are cut). Negative:
  *                 the sequence is left alone.
@@ -781,16 +782,26 @@ PA_API pa_status pa_bm_append_slot(pa_bm *bm, int64_t seq, int64_t *slot, int64_
  * reference on each block. */
 PA_API pa_status pa_bm_fork(pa_bm *bm, int64_t parent, int64_t child);
 
-/* Room for a compacted copy of `seq` (pa_evict): takes cdiv(num_tokens,
- * block_size) fresh blocks, which become the sequence's table (written to
- * new_table[0..cap), its length to *n) and num_tokens its token count, and drops
- * one reference on each of its old blocks, those reaching zero returning to the
- * front of the free queue in block-table order. Fresh ones are taken before old
- * ones are released, so the two never meet in one call; the caller moves the data
- * before the released blocks are written again, and reads the old table
- * (pa_bm_block_table) ahead of this call. num_tokens is at most the sequence's
- * (PA_ERR_INVALID_ARG); PA_ERR_OUT_OF_BLOCKS, a short cap (*n is still set) and a
- * swapped-out sequence (PA_ERR_INVALID_ARG) leave the manager unchanged. */
+/* Room for compacted copies of a group of resident sequences (each id once), for
+ * one pa_evict of all of them: sequence i takes cdiv(num_tokens[i], block_size)
+ * fresh blocks, which become its table, and num_tokens[i], at most the tokens it
+ * holds, its token count. The new tables are written to new_tables[0..cap), one
+ * after another, and their whole length to *n. Then one reference on each old
+ * block is dropped, those reaching zero returning to the front of the free queue:
+ * sequence 0's first, in block-table order. Fresh ones are taken for the whole
+ * group before any old one is released, so that within one call no new block is
+ * an old one. The caller reads the old tables (pa_bm_block_table) ahead of this
+ * call, and moves the data before the released blocks are written again: before
+ * anything else is taken from the manager, another group's blocks among them.
+ * All or nothing: PA_ERR_OUT_OF_BLOCKS, PA_ERR_NOT_FOUND, and PA_ERR_INVALID_ARG
+ * (an id twice, too many tokens, a swapped-out sequence, a short cap: *n is set
+ * then) leave the manager unchanged. */
+PA_API pa_status pa_bm_compact_group(pa_bm *bm, const int64_t *seqs, int num_seqs, const int *num_tokens,
+                                     int32_t *new_tables, int cap, int *n);
+
+/* pa_bm_compact_group of one sequence. Not for several sequences of one pa_evict:
+ * the second call hands out the blocks that the first one released, which the
+ * eviction has yet to read. */
 PA_API pa_status pa_bm_compact(pa_bm *bm, int64_t seq, int num_tokens, int32_t *new_table, int cap, int *n);
 
 /* Drops one reference on each of the sequence's blocks; blocks reaching zero

@@ -60,6 +60,7 @@ SIGNATURES = {
     "pa_evict": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_void_p,
                          c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                          c_int, c_void_p]),
+    "pa_bm_compact_group": (c_int, [c_void_p, P_I64, c_int, P_INT, P_I32, c_int, P_INT]),
     "pa_bm_compact": (c_int, [c_void_p, c_int64, c_int, P_I32, c_int, P_INT]),
     "pa_decode_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
     "pa_decode_plan": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p]),

@@ -614,8 +614,23 @@ class BlockManager:
     def fork(self, parent: int, child: int) -> None:
         _check(self._lib.pa_bm_fork(self._h, parent, child), "pa_bm_fork")
 
+    def compact_group(self, seqs, num_tokens):
+        """The blocks of compacted copies of the sequences that one :func:`pa_evict` takes (num_tokens[i] of seqs[i], at
+        most what it holds), now their tables; none is an old block of the group, and those are released."""
+        ids, counts = np.ascontiguousarray(seqs, dtype=np.int64), np.ascontiguousarray(num_tokens, dtype=np.int32)
+        if ids.ndim != 1 or counts.shape != ids.shape:
+            raise ValueError("num_tokens must have one entry for each sequence")
+        need = [-(-max(int(t), 0) // self.block_size) for t in counts]
+        buf, n = (ctypes.c_int32 * max(1, sum(need)))(), ctypes.c_int(0)
+        _check(self._lib.pa_bm_compact_group(self._h, ids.ctypes.data_as(_lib.P_I64), ids.size,
+                                             counts.ctypes.data_as(_lib.P_INT), buf, sum(need), ctypes.byref(n)),
+               "pa_bm_compact_group")
+        at = np.concatenate([[0], np.cumsum(need)]).astype(int)
+        return [[int(b) for b in buf[lo:hi]] for lo, hi in zip(at, at[1:])]
+
     def compact(self, seq: int, num_tokens: int):
-        """The blocks of a compacted copy of ``seq`` (:func:`pa_evict`), now its table; its old ones are released."""
+        """:meth:`compact_group` of one sequence. Not one by one for the sequences of one eviction: the second would be
+        handed blocks that the first one's data still lies in."""
         cap = -(-max(num_tokens, 0) // self.block_size)
         buf, n = (ctypes.c_int32 * max(1, cap))(), ctypes.c_int(0)
         _check(self._lib.pa_bm_compact(self._h, seq, num_tokens, buf, cap, ctypes.byref(n)), "pa_bm_compact")

@@ -234,28 +234,42 @@ PA_API pa_status pa_bm_fork(pa_bm *bm, int64_t parent, int64_t child) {
     return PA_OK;
 }
 
-PA_API pa_status pa_bm_compact(pa_bm *bm, int64_t seq, int num_tokens, int32_t *new_table, int cap, int *n) {
-    if (!bm || !n || num_tokens < 0) return PA_ERR_INVALID_ARG;
-    auto it = bm->seqs.find(seq);
-    if (it == bm->seqs.end()) return PA_ERR_NOT_FOUND;
-    Sequence &s = it->second;
-    if (s.swapped || num_tokens > s.tokens) return PA_ERR_INVALID_ARG;
-    const int64_t need = (static_cast<int64_t>(num_tokens) + bm->block_size - 1) / bm->block_size;
-    *n = static_cast<int>(need);
-    if (cap < need || (need > 0 && !new_table)) return PA_ERR_INVALID_ARG;
-    if (need > bm->q.count) return PA_ERR_OUT_OF_BLOCKS;
-    std::vector<int32_t> fresh;
+// All fresh blocks are taken before any old one is released, so that no sequence of the group is
+// handed what another one's data still lies in. Whatever can fail comes ahead of the first change.
+PA_API pa_status pa_bm_compact_group(pa_bm *bm, const int64_t *seqs, int num_seqs, const int *num_tokens,
+                                     int32_t *new_tables, int cap, int *n) {
+    if (!bm || !n || (num_seqs > 0 && !num_tokens)) return PA_ERR_INVALID_ARG;
     try {
-        fresh.reserve(static_cast<size_t>(need));
+        std::vector<Sequence *> group;
+        const pa_status st = collect_group(bm, seqs, num_seqs, false, group);
+        if (st != PA_OK) return st;
+        std::vector<std::vector<int32_t>> tables(group.size());
+        int64_t need = 0;
+        for (size_t i = 0; i < group.size(); ++i) {
+            if (num_tokens[i] < 0 || num_tokens[i] > group[i]->tokens) return PA_ERR_INVALID_ARG;
+            need += (static_cast<int64_t>(num_tokens[i]) + bm->block_size - 1) / bm->block_size;
+        }
+        if (need > INT32_MAX) return PA_ERR_OUT_OF_BLOCKS;   // (more than any pool has)
+        *n = static_cast<int>(need);
+        if (cap < need || (need > 0 && !new_tables)) return PA_ERR_INVALID_ARG;
+        if (need > bm->q.count) return PA_ERR_OUT_OF_BLOCKS;
+        for (size_t i = 0; i < group.size(); ++i)
+            tables[i].resize((static_cast<size_t>(num_tokens[i]) + bm->block_size - 1) / bm->block_size);
+        for (std::vector<int32_t> &table : tables)
+            for (int32_t &b : table) *new_tables++ = b = bm->pop_front();
+        for (size_t i = 0; i < group.size(); ++i) {
+            group[i]->table.swap(tables[i]);
+            group[i]->tokens = num_tokens[i];
+        }
+        for (auto old = tables.rbegin(); old != tables.rend(); ++old) release_blocks(bm, *old);
     } catch (const std::bad_alloc &) {
         return PA_ERR_OUT_OF_BLOCKS;   // (nothing has changed)
     }
-    for (int64_t i = 0; i < need; ++i) fresh.push_back(bm->pop_front());
-    std::copy(fresh.begin(), fresh.end(), new_table);
-    s.table.swap(fresh);
-    s.tokens = num_tokens;
-    release_blocks(bm, fresh);
     return PA_OK;
+}
+
+PA_API pa_status pa_bm_compact(pa_bm *bm, int64_t seq, int num_tokens, int32_t *new_table, int cap, int *n) {
+    return pa_bm_compact_group(bm, &seq, 1, &num_tokens, new_table, cap, n);
 }
 
 PA_API pa_status pa_bm_free(pa_bm *bm, int64_t seq) {
