@@ -477,7 +477,13 @@ PA_API pa_status pa_decode_weights(void *out, pa_dtype out_dtype, float *weights
  *               sequence's do (the entries of all its query tokens start from
  *               zero all the same)
  *   workspace   at least pa_prefill_weights_workspace_size() bytes, 16-byte
- *               aligned (the rows' statistics), as above
+ *               aligned (the rows' statistics), as above. The size of larger
+ *               arguments will do: what it has no room for is cut into fewer
+ *               pieces, which costs time where there are few rows and changes
+ *               the order of sums (the same call with the same size of
+ *               workspace gives the same bits). It does not grow with every
+ *               argument: for all the pieces of several shapes, the largest of
+ *               their sizes.
  *   Supported: as pa_decode_weights. */
 PA_API size_t pa_prefill_weights_workspace_size(int num_seqs, int num_tokens, int num_heads, int num_kv_heads,
                                                 int head_dim, int block_size, int max_query_len,

@@ -1056,7 +1056,9 @@ struct WeightsPlan {
     size_t rows_at, offsets_at, stats_at, order_at, parts_at, total;   // workspace bytes: the counter, the rows' statistics, ...
 };
 
-WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms, bool tc) {
+// The cut with at most so many pieces of a row's statistics and of the rows of a key's sum.
+WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, int window, int sms, bool tc,
+                         int max_pieces = kMaxSplits, int max_row_pieces = kMaxSplits) {
     WeightsPlan pl{};
     pl.max_count = window > 0 ? std::min(window, max_query) : max_query;
     const int64_t compact_rows = static_cast<int64_t>(s.num_seqs) * pl.max_count;
@@ -1064,14 +1066,14 @@ WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, in
     pl.stat_rows = std::min<int64_t>(compact_rows, num_tokens);
     const int64_t rows = static_cast<int64_t>(pl.max_count) * (s.num_heads / s.num_kv_heads);
     if (tc) {
-        plan_prefill_weights_tc(s.num_seqs, s.num_kv_heads, rows, s.max_ctx, sms, &pl.pair, &pl.pieces, &pl.row_pieces,
-                                &pl.ordered);
+        plan_prefill_weights_tc(s.num_seqs, s.num_kv_heads, rows, s.max_ctx, sms, max_pieces, max_row_pieces, &pl.pair,
+                                &pl.pieces, &pl.row_pieces, &pl.ordered);
         pl.nsplit = pl.pair ? 2 * pl.pieces : 4 * pl.pieces;   // (the columns' halves are two pieces)
     } else {
         const int64_t tiles = s.num_seqs * static_cast<int64_t>(s.num_kv_heads) * cdiv64(rows, prefill_weights_simt_rows());
         pl.nsplit = static_cast<int>(std::max<int64_t>(
             1, std::min<int64_t>({static_cast<int64_t>(sms) * kWeightStatsCtasPerSm / std::max<int64_t>(tiles, 1),
-                                  s.max_ctx / kWeightStatsMinSplit, kMaxSplits})));
+                                  s.max_ctx / kWeightStatsMinSplit, max_pieces})));
     }
     const size_t all = static_cast<size_t>(pl.stat_rows) * s.num_heads;
     pl.rows_at = 256;
@@ -1082,6 +1084,25 @@ WeightsPlan plan_weights(const DecodeShape &s, int num_tokens, int max_query, in
     pl.total = pl.parts_at + (pl.row_pieces > 1 ? align256(static_cast<size_t>(pl.row_pieces) * s.num_seqs * s.num_kv_heads * s.max_ctx *
                                                            sizeof(float)) : 0);
     return pl;
+}
+
+// The cut that a workspace of `have` bytes holds: where it was made for other sizes (a batch of 16 prompts of 4,100
+// tokens and windows of 32 fills the SMs with one piece, one of 15 takes five), fewer pieces, one at the least.
+WeightsPlan plan_weights_within(const DecodeShape &s, int num_tokens, int max_query, int window, int sms, bool tc, size_t have) {
+    WeightsPlan pl = plan_weights(s, num_tokens, max_query, window, sms, tc);
+    while (pl.total > have && pl.row_pieces > 1)
+        pl = plan_weights(s, num_tokens, max_query, window, sms, tc, kMaxSplits, pl.row_pieces - 1);
+    for (int most = tc ? pl.pieces : pl.nsplit; pl.total > have && most > 1; --most)
+        pl = plan_weights(s, num_tokens, max_query, window, sms, tc, most - 1, 1);
+    return pl;
+}
+
+// What no call asks more than once it is cut into single pieces; it grows with every size (and a window).
+size_t weights_workspace_floor(const DecodeShape &s, int num_tokens, int max_query, int window) {
+    const int64_t count = window > 0 ? std::min(window, max_query) : max_query;
+    const size_t all = static_cast<size_t>(std::min<int64_t>(s.num_seqs * count, num_tokens)) * s.num_heads;
+    return 256 + align256(all * sizeof(float2)) + align256(all * sizeof(float)) + align256(4 * all * sizeof(float2)) +
+           align256(static_cast<size_t>(prefill_weights_tc_most_ordered()) * sizeof(int));
 }
 
 pa_status check_prefill_weights(const DecodeShape &s, int num_tokens, int max_query, int window) {
@@ -1860,8 +1881,9 @@ PA_API size_t pa_prefill_weights_workspace_size(int num_seqs, int num_tokens, in
     if (current_device(&dev) != PA_OK) return 0;
     const int sms = sm_count(dev);
     if (sms <= 0) return 0;
-    return std::max(plan_weights(s, num_tokens, max_query_len, window, sms, false).total,
-                    plan_weights(s, num_tokens, max_query_len, window, sms, true).total);
+    return std::max({plan_weights(s, num_tokens, max_query_len, window, sms, false).total,
+                     plan_weights(s, num_tokens, max_query_len, window, sms, true).total,
+                     weights_workspace_floor(s, num_tokens, max_query_len, window)});
 }
 
 PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, const void *query, pa_dtype q_dtype,
@@ -1887,7 +1909,7 @@ PA_API pa_status pa_prefill_weights(float *weights, int64_t weights_stride, cons
     const int sms = sm_count(dev);
     if (sms <= 0) return PA_ERR_CUDA;
     const bool tc = is16(kv_dtype);
-    const WeightsPlan pl = plan_weights(s, num_tokens, max_query_len, window, sms, tc);
+    const WeightsPlan pl = plan_weights_within(s, num_tokens, max_query_len, window, sms, tc, workspace_bytes);
     if (!workspace || workspace_bytes < pl.total || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     PrefillWeightsParams p;
     std::memset(&p, 0, sizeof p);

@@ -90,8 +90,9 @@ cudaError_t launch_decode_weights(DecodeWeightsParams &p, int type, int head_dim
 int prefill_weights_simt_rows();                    // rows of a tile
 cudaError_t launch_prefill_weights_simt(const PrefillWeightsParams &p, int head_dim, cudaStream_t stream);   // fp32
 bool prefill_weights_tc_fits(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx);
-void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces,
-                             int *row_pieces, int64_t *ordered);
+void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int max_pieces,
+                             int max_row_pieces, int *pair, int *pieces, int *row_pieces, int64_t *ordered);
+int64_t prefill_weights_tc_most_ordered();        // units it puts in order, at most
 int prefill_weights_tc_key_box(int block_size);   // tokens of a box where tiles are fetched by TMA, else 0
 int prefill_weights_tc_query_box(int group);
 cudaError_t launch_prefill_weights_tc(const PrefillWeightsParams &p, bool f16, int head_dim, bool tma, const CUtensorMap &map_q,

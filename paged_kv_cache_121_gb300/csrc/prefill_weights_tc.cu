@@ -860,15 +860,17 @@ bool prefill_weights_tc_fits(int num_seqs, int num_kv_heads, int64_t rows, int m
 constexpr int kFewUnits = 3;
 constexpr int kMaxRowPieces = 8;
 constexpr int64_t kMaxOrdered = 4096;   // units that one CTA puts in order
-void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int *pair, int *pieces,
-                             int *row_pieces, int64_t *ordered) {
+int64_t prefill_weights_tc_most_ordered() { return kMaxOrdered; }
+
+void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int max_ctx, int sms, int max_pieces,
+                             int max_row_pieces, int *pair, int *pieces, int *row_pieces, int64_t *ordered) {
     *pair = rows > kSide;
     const int64_t side = *pair ? 2 * kSide : kSide, heads = static_cast<int64_t>(num_seqs) * num_kv_heads;
     const int64_t units = heads * ((rows + side - 1) / side);
     const int64_t tiles = (static_cast<int64_t>(max_ctx) + kSide - 1) / kSide;
     double best = 0;
     *pieces = 1;
-    for (int n = 1; n <= kMaxSplits / 4 && n <= tiles; ++n) {
+    for (int n = 1; n <= kMaxSplits / 4 && n <= tiles && n <= max_pieces; ++n) {
         const double rounds = static_cast<double>((units * n + sms - 1) / sms);
         const double time = rounds * (static_cast<double>((tiles + n - 1) / n) * (*pair ? 2 : 1) + (*pair ? 3 : 1));
         if (n == 1 || time < best * 0.97) {
@@ -879,7 +881,8 @@ void plan_prefill_weights_tc(int num_seqs, int num_kv_heads, int64_t rows, int m
     const int64_t key_units = (static_cast<int64_t>(max_ctx) + 2 * kSide - 1) / (2 * kSide) * heads;
     const int64_t row_tiles = (rows + kSide - 1) / kSide;
     *row_pieces = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>({(kFewUnits * sms + key_units - 1) / std::max<int64_t>(key_units, 1), row_tiles / 4, kMaxRowPieces})));
+        1, std::min<int64_t>({(kFewUnits * sms + key_units - 1) / std::max<int64_t>(key_units, 1), row_tiles / 4, kMaxRowPieces,
+                                  max_row_pieces})));
     if (heads > 65535) *row_pieces = 1;
     const int64_t n = key_units / num_kv_heads * *row_pieces;
     *ordered = row_tiles >= kLongUnit && n <= kMaxOrdered ? n : 0;   // (0: taken as they are numbered)
