@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libpa.so")
 
 SOURCES = ["api.cu", "decode_mma.cu", "decode_balanced.cu", "prefix_mma.cu", "prefix_tc.cu", "decode_simt.cu", "cache_ops.cu", "rope.cu", "norm_rope.cu", "decode_weights.cu", "prefill_weights_simt.cu", "prefill_weights_tc.cu", "evict.cu", "prefill_simt.cu", "prefill_tc.cu", "prefill_rows.cu",
            "decode_static.cu", "health.cu", "block_manager.cpp"]
-HEADERS = ["device_common.cuh", "mma_tile.cuh", "tcgen05.cuh", "prompt_common.cuh", "rope_common.cuh", "weights_common.cuh", "packed_math.cuh", "async_copy.cuh", "internal.h"]
+HEADERS = ["device_common.cuh", "mma_tile.cuh", "tcgen05.cuh", "prompt_common.cuh", "rope_common.cuh", "weights_common.cuh", "packed_math.cuh", "async_copy.cuh", "tile_ring.h", "internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -53,6 +53,7 @@
 #include "internal.h"
 #include "packed_math.cuh"
 #include "tcgen05.cuh"
+#include "tile_ring.h"
 #include "weights_common.cuh"
 
 namespace pa {
@@ -447,7 +448,7 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
         };
         const unsigned units = static_cast<unsigned>(unit_count<kSums>(p));
         unsigned turn = 0, at = blockIdx.x;
-        int count[2] = {0, 0}, streamed = 0;   // held tiles so far, first and second of a unit; streamed ones
+        TileRing held_ring[2] = {TileRing(held_buffers), TileRing(held_buffers)}, str_ring(str_slots);
         bool ok = true;
         for (int k = 0; ok; ++k) {
             Unit u;
@@ -486,26 +487,28 @@ prefill_weights_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (i >= u.held || !ok) break;
-                const int n = count[i]++, round = n / held_buffers, buf = n - round * held_buffers;
+                const int buf = held_ring[i].slot();
                 ok = fetch(u, held_keys, held[i], i * held_buffers + buf, &sh->held_full[i][buf], &sh->held_empty[i][buf],
-                           round > 0 ? (round - 1) & 1 : -1);
+                           held_ring[i].empty_parity());
+                held_ring[i].count(ok);
             }
-            for (int i = u.lo; i < u.hi && ok; ++i, ++streamed) {
+            for (int i = u.lo; i < u.hi && ok; ++i) {
                 const Place here = next;
                 if (i + 1 < u.hi) next = locate(u, !held_keys, i + 1);
-                const int round = streamed / str_slots, slot = streamed - round * str_slots;
-                ok = fetch(u, !held_keys, here, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], round > 0 ? (round - 1) & 1 : -1);
+                const int slot = str_ring.slot();
+                ok = fetch(u, !held_keys, here, held_slots + slot, &sh->str_full[slot], &sh->str_empty[slot], str_ring.empty_parity());
+                str_ring.count(ok);
             }
         }
         if (kTma) {   // nothing is on its way when the CTA ends: the last phase of every slot that was filled
-            auto drain = [&](uint64_t *full, int filled, int slots) {
-                for (int i = max(0, filled - slots); i < filled; ++i)
-                    if (!mbar_wait(smem_addr(full + i % slots), (i / slots) & 1)) record_status(p.status, kStatusTimeout);
+            auto drain = [&](uint64_t *full, const TileRing &ring) {
+                for (int i = ring.first_left(); i < ring.sent; ++i)
+                    if (!mbar_wait(smem_addr(full + i % ring.slots), ring.full_parity(i))) record_status(p.status, kStatusTimeout);
             };
             if (lane == 0) {
-                drain(sh->held_full[0], count[0] - !ok, held_buffers);
-                drain(sh->held_full[1], count[1] - !ok, held_buffers);
-                drain(sh->str_full, streamed - !ok, str_slots);
+                drain(sh->held_full[0], held_ring[0]);
+                drain(sh->held_full[1], held_ring[1]);
+                drain(sh->str_full, str_ring);
             }
             __syncwarp();
         } else {
