@@ -445,7 +445,9 @@ PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa
  * entry needs initialisation, and with decay 0 the old ones are not read.
  * Entries at or past the context are left as they were. decay is finite and
  * not negative. Statistics and sums are fp32 and no atomics add them: the
- * same call gives the same bits.
+ * same call gives the same bits. Scores may have any size, before and after the
+ * scale, below 2^125; a row whose visible scores are all minus infinity weighs
+ * nothing.
  * ---------------------------------------------------------------------- */
 
 /* pa_decode, and the weights of its rows: one query token a sequence, the
@@ -456,7 +458,9 @@ PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa
  *                   aligned (the rows' scores); its contents need no
  *                   initialisation. Calls that share a workspace must not
  *                   overlap on the GPU.
- *   everything else as pa_decode; any block size from 1 to 256. */
+ *   everything else as pa_decode; any block size from 1 to 256. Softmax
+ *   weights keep fp32's bits on their way to the outputs, and sums of outputs
+ *   are fp32. */
 PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                int block_size, int max_context_len);
 

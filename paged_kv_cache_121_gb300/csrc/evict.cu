@@ -18,7 +18,7 @@
 //  * Move: rows of 16-byte vectors, all heads of a kept place together, because a
 //    place's heads are contiguous where they go (they come from different tokens). Each
 //    element is read once and written once, so HBM is the bound: 268 MB in 41 us
-//    (0.97 of the copy rate; the choice of that call takes 11.7 us, that of 8 heads of one
+//    (0.98 of the copy rate; the choice of that call takes 11.7 us, that of 8 heads of one
 //    context of 32,768 tokens 15.4).
 #include <algorithm>
 

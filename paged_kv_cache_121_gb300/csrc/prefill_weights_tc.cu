@@ -12,7 +12,8 @@
 //    tile of keys is then done with its one product.
 //
 // Bound: the products and the exponentials, 512 cycles a tile each (two passes: twice
-// the products and exponentials of one attention's scores); for windows of few queries,
+// the products and exponentials of one attention's scores), and in the sums as many for the
+// rows' numbers, read from shared memory (sum_weights); for windows of few queries,
 // reading K twice. So neither waits for the other. Persistent CTAs, one an SM, of
 //  * warps 0-7 and 8-15: two groups, each with a tile of scores in work and one behind
 //    it (4 x 128 columns of tensor memory), two warps a lane quarter, so that a scheduler
@@ -35,14 +36,16 @@
 // pieces of the context) go round the CTAs back and forth.
 //
 // Measured (GB300, 32 / 8 heads of 128). Windows of 32 queries, 16 prompts of 4,100
-// tokens, bf16, blocks of 16: 77.8 us = statistics 40, between 5, sums 42 (alone, under
-// the profiler; bytes 44 %, tensor pipe 18 %, exponentials 20 %, issue slots 31 and 35 %
-// of their rates: a tile comes in about 2,100 cycles, and its 16 boxes of 2 KB have a
-// share in that, since with blocks of 128 a pass takes a quarter less; an L2 policy of
-// evict-first or one more tile in flight change nothing). 8 chunks of 200 .. 1,500 tokens behind up to 2,500, fp16,
-// blocks of 32: 169 us = 78 + 7 + 92 (tensor pipe 37 and 31 %, exponentials 39 and
-// 32 %, issue slots 57 and 50 %). Gathered by four copy warps the same two took 123 and
-// 210 us; by one, with a warp a lane quarter and units as they are numbered, 171 and 441.
+// tokens, bf16, blocks of 16: 80.3 us = statistics 40, between 5, sums 43 (each alone, under
+// the profiler; bytes 45 and 42 %, tensor pipe 23 and 22 %, exponentials 25 and 22 %, issue
+// slots 34 and 44 % of their rates: a tile comes in about 2,100 cycles, and its 16 boxes of
+// 2 KB have a share in that, since with blocks of 128 a pass takes a quarter less; an L2 policy
+// of evict-first or one more tile in flight change nothing). 8 chunks of 200 .. 1,500 tokens
+// behind up to 2,500, fp16, blocks of 32: 174 us = 82 + 7 + 99 (tensor pipe 43 and 34 %,
+// exponentials 46 and 35 %, issue slots 60 and 52 %; in a loop of calls 78, 5 and 95).
+// Gathered by four copy warps (blocks of 24) the same two take 93 and 217 us. Of a first
+// version, by one copy warp, with a warp a lane quarter and units as they are numbered, 171
+// and 441.
 //
 // Every wait is bounded; on expiry the kernel records a timeout, waits (bounded) for its
 // products and copies, frees its tensor memory and returns.
