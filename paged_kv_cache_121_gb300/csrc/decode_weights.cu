@@ -136,8 +136,9 @@ struct StepTile {
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
         }
-        // the reference maximum moves only where a score passes it by 2^kRescaleSlack
-        const bool up0 = m0 > st.m0 + kRescaleSlack, up1 = m1 > st.m1 + kRescaleSlack;
+        // The reference maximum moves only where a score passes it by kRescaleSlack. (Differences: a sum with a score of
+        // 2^27 would round by 8, and a weight leave fp16.)
+        const bool up0 = m0 - st.m0 > kRescaleSlack, up1 = m1 - st.m1 > kRescaleSlack;
         if (__any_sync(0xffffffffu, up0 || up1)) {
             const float n0 = up0 ? m0 : st.m0, n1 = up1 ? m1 : st.m1;
             const float a0 = up0 ? fast_exp2(st.m0 - n0) : 1.f, a1 = up1 ? fast_exp2(st.m1 - n1) : 1.f;

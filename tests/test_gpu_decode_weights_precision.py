@@ -71,3 +71,31 @@ def test_outputs_are_not_cut_in_one_direction(dt):
         want = torch.einsum("th,thd->hd", p, paged.v[blk, t % 16].double()).repeat_interleave(hq // hkv, 0)
         mean += float(((out[b].double() - want) / want).mean()) / B
     assert abs(mean) <= 8 * E, mean / E
+
+
+@pytest.mark.parametrize("run", [16, 32, 64, 128])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (16, 1, 128)])
+def test_fp16_scores_that_rise_by_single_steps(hq, hkv, d, run):
+    """Scores of 2^27 (base 2) and more, where fp32's steps are 16, rising by a step or two every `run` tokens: a
+    running maximum that is not moved for so little, because 8 more than it rounds to the same, makes weights of 2^16,
+    which fp16 does not hold. Raw scores are 2^30 + 128 t, exact; a step is 23 (base 2), rounded to 16 or 32, so that
+    all but the last run weigh 2^-16 of it at most and half as much again each run before: in all, of 12 equal runs,
+    below 2^-15, and an output is the mean of the last run's values within 2^-14 of the largest one."""
+    n = 12 * run
+    paged = Paged((n,), hkv, d, 16, "fp16", 27)
+    t = torch.arange(n, device="cuda")
+    blk = torch.from_numpy(paged.table[0].astype("int64")).cuda()[t // 16]
+    q = torch.zeros(1, hq, d, dtype=torch.float16, device="cuda")
+    q[:, :, 0], q[:, :, 1] = 2.0 ** 15, 1
+    paged.k[blk, t % 16] = 0
+    paged.k[blk, t % 16, :, 0] = 2.0 ** 15
+    paged.k[blk, t % 16, :, 1] = (128.0 * (t // run)).half()[:, None].expand(n, hkv)
+    out = torch.empty(1, hq, d, device="cuda")
+    w = torch.zeros(1, hkv, n, device="cuda")
+    ws = torch.empty(pa.pa_decode_weights_workspace_size(1, hq, hkv, d, 16, n), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_weights(out, w, q, paged.k, paged.v, paged.tables, paged.context_lens, n, 2.0 ** -3, ws)
+    v = paged.seq_v[0].double()
+    want = v[-run:].mean(0).repeat_interleave(hq // hkv, 0)
+    assert bool(((out[0].double() - want).abs() <= 2.0 ** -14 * v.abs().max()).all())
+    share = w[0].double() / (hq // hkv)
+    assert bool(((share[:, -run:] - 1 / run).abs() <= 2.0 ** -14 / run).all()) and bool((share[:, :-run] <= 2.0 ** -15 / run).all())
