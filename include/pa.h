@@ -460,7 +460,7 @@ PA_API pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query, pa
  *                   overlap on the GPU.
  *   everything else as pa_decode; any block size from 1 to 256. On their
  *   way to the outputs softmax weights keep 24 bits (fp16 caches: 22, and none
- *   below 2^-25 of the row's largest); sums of outputs are fp32. */
+ *   below 2^-32 of the row's largest); sums of outputs are fp32. */
 PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                int block_size, int max_context_len);
 

@@ -19,7 +19,7 @@
 //    base 2. fp32: CUDA cores.
 //  * The weights of V enter the products in parts of the caches' type: three of bf16, which
 //    hold fp32's 24 bits (two left 2^-17 of a weight, seen in fp32 outputs), or two of fp16,
-//    22 bits and none below 2^-25 of a row's largest weight. Errors of fp32 outputs against
+//    22 bits and none below 2^-32 of a row's largest weight. Errors of fp32 outputs against
 //    64 bits, relative in norm, at 300 .. 32,768 tokens: 1.6e-7 .. 6.3e-7, half of what the
 //    same in fp32 operations leaves.
 //  * The warps' states meet in shared memory, the cluster's CTAs through distributed
@@ -85,6 +85,9 @@ struct StepTile {
     using C = StepCfg<T, D>;
     static constexpr bool kF16 = std::is_same<T, __half>::value;
     static constexpr int kParts = kF16 ? 2 : 3;   // of a weight
+    // fp16 weights are raised by 2^7, as far as the slack below leaves room: what its smallest numbers cut off lies
+    // that much lower.
+    static constexpr float kRaise = kF16 ? 7.f : 0.f;
     WarpState<D> st;
     uint32_t qa[D / 16][4];
 
@@ -136,11 +139,11 @@ struct StepTile {
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
         }
-        // The reference maximum moves only where a score passes it by kRescaleSlack. (Differences: a sum with a score of
-        // 2^27 would round by 8, and a weight leave fp16.)
-        const bool up0 = m0 - st.m0 > kRescaleSlack, up1 = m1 - st.m1 > kRescaleSlack;
+        // The reference (a maximum less kRaise) moves only where a score passes that maximum by kRescaleSlack. (Differences:
+        // a sum with a score of 2^27 would round by 8, and a weight leave fp16.)
+        const bool up0 = m0 - st.m0 > kRescaleSlack + kRaise, up1 = m1 - st.m1 > kRescaleSlack + kRaise;
         if (__any_sync(0xffffffffu, up0 || up1)) {
-            const float n0 = up0 ? m0 : st.m0, n1 = up1 ? m1 : st.m1;
+            const float n0 = up0 ? m0 - kRaise : st.m0, n1 = up1 ? m1 - kRaise : st.m1;
             const float a0 = up0 ? fast_exp2(st.m0 - n0) : 1.f, a1 = up1 ? fast_exp2(st.m1 - n1) : 1.f;
             st.m0 = n0;
             st.m1 = n1;

@@ -73,6 +73,34 @@ def test_outputs_are_not_cut_in_one_direction(dt):
     assert abs(mean) <= 8 * E, mean / E
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("hq,hkv,d,lens", [(16, 2, 64, (64, 33, 7)), (8, 8, 128, (100,) * 5), (40, 2, 128, (97, 64))])
+def test_small_weights_keep_their_bits(dt, hq, hkv, d, lens):
+    """The same with scores from -8 to 0: weights down to 2^-11.6 of the largest. Scores of 11.6 (base 2) round by
+    ln 2 (4 + 1) 11.6 e < 41 e, exp2 by 4: in place of 49 e, 2 * 45 + 15 + 8 + 4 = 117 e. fp16's parts end 2^-32 below the
+    largest weight (2^-25 of numbers that are raised by 2^7), half a step of that for each of two."""
+    paged = Paged(lens, hkv, d, 16, dt, 25)
+    g = torch.Generator(device="cuda").manual_seed(26)
+    q = torch.zeros(len(lens), hq, d, dtype=DT[dt], device="cuda")
+    q[:, :, 0] = 1
+    want = torch.zeros(len(lens), hq, d, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        key = (torch.rand(n, hkv, generator=g, device="cuda") * -8).to(DT[dt])
+        key[n // 2] = 0
+        t = torch.arange(n, device="cuda")
+        blk = torch.from_numpy(paged.table[b].astype("int64")).cuda()[t // paged.bs]
+        paged.k[blk, t % paged.bs] = 0
+        paged.k[blk, t % paged.bs, :, 0] = key
+        paged.v[blk, t % paged.bs] = torch.eye(n, d, dtype=DT[dt], device="cuda")[:, None].expand(n, hkv, d)
+        want[b, :, :n] = torch.softmax(key.double(), 0).T.repeat_interleave(hq // hkv, 0)
+    out = torch.full((len(lens), hq, d), float("nan"), device="cuda")
+    w = torch.zeros(len(lens), hkv, paged.max_ctx, device="cuda")
+    ws = torch.empty(pa.pa_decode_weights_workspace_size(len(lens), hq, hkv, d, 16, paged.max_ctx), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_weights(out, w, q, paged.k, paged.v, paged.tables, paged.context_lens, paged.max_ctx, 1.0, ws)
+    err = (out.double() - want).abs()
+    assert bool((err <= 120 * E * want + (2.0 ** -32 if dt == "fp16" else 0.0)).all()), float((err / want.clamp(min=1e-30)).max() / E)
+
+
 @pytest.mark.parametrize("run", [16, 32, 64, 128])
 @pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (16, 1, 128)])
 def test_fp16_scores_that_rise_by_single_steps(hq, hkv, d, run):
